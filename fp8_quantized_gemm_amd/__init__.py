@@ -11,6 +11,9 @@ _API = (
     "fp8_quantize_act", "fp8_gemm", "fp8_linear",
     # per-token activation / per-channel weight scales
     "fp8_quantize_rows", "fp8_gemm_rowwise", "fp8_linear_rowwise",
+    # a scale per block of 128: quantizers, GEMM, quantize + GEMM
+    "fp8_quantize_blocks", "fp8_quantize_weight_blocks", "fp8_gemm_blockwise",
+    "fp8_linear_blockwise",
     # delayed scaling with an amax history
     "DelayedScaling", "fp8_quantize_act_delayed", "fp8_linear_delayed",
     # FP8 KV-cache quantizer (one scale per head)

@@ -9,6 +9,7 @@
 #include <initializer_list>
 #include <utility>
 
+#include "block.hpp"
 #include "common.hpp"
 #include "fp8q.h"
 
@@ -512,6 +513,88 @@ fp8q_status nested_linear_fp8_e4m3(const uint16_t* a, const uint8_t* hi, uint16_
     FP8Q_TRY(check_device());
     return linear_common("nested_linear_fp8_e4m3", a, FP8Q_FP16, hi, nullptr, y, q, scale, amax, M,
                          N, K, WF_E4M3_SC8, OUT_FP16, 0, (hipStream_t)stream);
+}
+
+fp8q_status fp8_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* q,
+                                float* scale, fp8q_stream stream)
+{
+    if (!x || !q || !scale) return FP8Q_ERR_NULL;
+    if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
+    if (rows < 1 || rows > kMaxDim || cols < 16 || (cols % 16) != 0 || cols > kMaxK)
+        return FP8Q_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(q) || !aligned4(scale)) return FP8Q_ERR_ALIGN;
+    const uint64_t n = u64(rows) * u64(cols);
+    FP8Q_TRY(check_apart({{q, n}, {scale, 4 * u64(blocks_of(cols)) * u64(rows)}}, {{x, 2 * n}}));
+    FP8Q_TRY(check_device());
+    return finish("fp8_quantize_blocks",
+                  launch_quantize_blocks(x, dtype, rows, cols, q, scale, (hipStream_t)stream));
+}
+
+fp8q_status fp8_quantize_weight_blocks(const void* w, int dtype, int64_t batch, int64_t rows,
+                                       int64_t cols, uint8_t* q, float* scale, fp8q_stream stream)
+{
+    if (!w || !q || !scale) return FP8Q_ERR_NULL;
+    if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
+    if (batch < 1 || rows < 1 || rows > kMaxDim || cols < 16 || (cols % 16) != 0 || cols > kMaxK ||
+        rows > ((int64_t)1 << 40) / cols || batch > ((int64_t)1 << 40) / (rows * cols))
+        return FP8Q_ERR_SHAPE;
+    if (!aligned16(w) || !aligned16(q) || !aligned4(scale)) return FP8Q_ERR_ALIGN;
+    const uint64_t n = u64(batch) * u64(rows) * u64(cols);
+    FP8Q_TRY(check_apart(
+        {{q, n}, {scale, 4 * u64(batch) * u64(blocks_of(rows)) * u64(blocks_of(cols))}}, {{w, 2 * n}}));
+    FP8Q_TRY(check_device());
+    return finish("fp8_quantize_weight_blocks",
+                  launch_quantize_weight_blocks(w, dtype, batch, rows, cols, q, scale,
+                                                (hipStream_t)stream));
+}
+
+namespace {
+// The block-scaled product, dispatched on M like the FP8 GEMM.
+hipError_t dispatch_block(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
+                          uint16_t* y, int64_t M, int64_t N, int64_t K, hipStream_t st)
+{
+    return M <= kGemvBlockMaxM ? launch_gemv_block(qa, sa, qw, sw, y, (int)M, (int)N, (int)K, st)
+                               : launch_tile_block(qa, sa, qw, sw, y, (int)M, (int)N, (int)K, st);
+}
+
+uint64_t act_scale_bytes(int64_t M, int64_t K) { return 4 * u64(blocks_of(K)) * u64(M); }
+uint64_t weight_scale_bytes(int64_t N, int64_t K) { return 4 * u64(blocks_of(N)) * u64(blocks_of(K)); }
+}  // namespace
+
+fp8q_status fp8_gemm_blockwise(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                               const float* sw, uint16_t* y, int64_t M, int64_t N, int64_t K,
+                               fp8q_stream stream)
+{
+    if (!qa || !sa || !qw || !sw || !y) return FP8Q_ERR_NULL;
+    FP8Q_TRY(check_gemm_sizes(M, N, K));
+    if (!aligned16(qa) || !aligned16(qw) || !aligned16(y) || !aligned4(sa) || !aligned4(sw))
+        return FP8Q_ERR_ALIGN;
+    FP8Q_TRY(check_apart({{y, u64(M) * u64(N) * 2}},
+                         {{qa, u64(M) * u64(K)}, {sa, act_scale_bytes(M, K)},
+                          {qw, u64(N) * u64(K)}, {sw, weight_scale_bytes(N, K)}}));
+    FP8Q_TRY(check_device());
+    return finish("fp8_gemm_blockwise",
+                  dispatch_block(qa, sa, qw, sw, y, M, N, K, (hipStream_t)stream));
+}
+
+fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, const float* sw,
+                                 uint16_t* y, uint8_t* q, float* sa, int64_t M, int64_t N,
+                                 int64_t K, fp8q_stream stream)
+{
+    if (!x || !qw || !sw || !y || !q || !sa) return FP8Q_ERR_NULL;
+    if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
+    FP8Q_TRY(check_gemm_sizes(M, N, K));
+    if (!aligned16(x) || !aligned16(qw) || !aligned16(y) || !aligned16(q) || !aligned4(sw) ||
+        !aligned4(sa))
+        return FP8Q_ERR_ALIGN;
+    const Buf bx{x, u64(M) * u64(K) * 2}, bw{qw, u64(N) * u64(K)}, bsw{sw, weight_scale_bytes(N, K)},
+        by{y, u64(M) * u64(N) * 2}, bq{q, u64(M) * u64(K)}, bsa{sa, act_scale_bytes(M, K)};
+    FP8Q_TRY(check_apart({bq, bsa}, {bx, bw, bsw, by}));
+    FP8Q_TRY(check_apart({by}, {bw, bsw}));
+    FP8Q_TRY(check_device());
+    hipError_t e = launch_quantize_blocks(x, dtype, M, K, q, sa, (hipStream_t)stream);
+    if (e == hipSuccess) e = dispatch_block(q, sa, qw, sw, y, M, N, K, (hipStream_t)stream);
+    return finish("fp8_linear_blockwise", e);
 }
 
 fp8q_status fp8q_e4m3_encode_f32(const float* v, uint8_t* q, int64_t n, fp8q_stream stream)

@@ -1,0 +1,482 @@
+// Block-scaled FP8: quantizers with a scale per block of 128 and the product
+// of block-scaled operands.
+//
+//   s = fl32(amax / 448) over the block (1 when amax == 0),
+//   q = E4M3_rne_sat(fl32(x / s)),
+//   y[m, n] = bf16( sum_b sa[b, m] sw[n / 128, b] sum_{k in block b} qa[m, k] qw[n, k] ).
+//
+// A block's products are accumulated in fp32 by the matrix cores from a zero
+// accumulator, then added to the running fp32 sum with one FMA per output and
+// block, so no rounding to fewer bits happens before the final bf16.
+//
+// Activation scales are stored [K blocks, M]: the scales that a tile needs in
+// one K step are then contiguous.
+#include <algorithm>
+
+#include "block.hpp"
+#include "tile.hpp"
+
+namespace fp8q {
+namespace {
+
+// ---------------------------------------------------------------- quantizers
+// Max over a row of 16 lanes (DPP); valid in all 16.
+__device__ __forceinline__ float row16_max(float v)
+{
+    FP8Q_DPP_MAX(v, 0xB1, 0xf);   // quad_perm [1,0,3,2]
+    FP8Q_DPP_MAX(v, 0x4E, 0xf);   // quad_perm [2,3,0,1]
+    FP8Q_DPP_MAX(v, 0x141, 0xf);  // row_half_mirror
+    FP8Q_DPP_MAX(v, 0x140, 0xf);  // row_mirror
+    return v;
+}
+
+// 16 lanes own a 1 x 128 block, 8 values each, and keep it in registers
+// between its amax and its codes.  Cells (row, K block) are numbered row
+// first within chunks of RT rows, so that the scales of a chunk, stored
+// [K blocks, rows], are written next to each other.
+constexpr int kQbThreads = 256;
+constexpr int kQbUnroll = 2;
+template <int DT, int RT>
+__global__ __launch_bounds__(kQbThreads) void quant_blocks_kernel(
+    const uint16_t* __restrict__ x, int64_t rows, int cols, int kblocks, int per_chunk,
+    uint8_t* __restrict__ q, float* __restrict__ scale)
+{
+    const int64_t chunk = blockIdx.x / per_chunk;
+    const int part = blockIdx.x - (int)(chunk * per_chunk);
+    const int c8 = (threadIdx.x & 15) * 8;
+    const int cell0 = part * (kQbThreads / 16) * kQbUnroll + (threadIdx.x >> 4);
+    v4i v[kQbUnroll];
+    int64_t at[kQbUnroll];
+#pragma unroll
+    for (int u = 0; u < kQbUnroll; ++u) {
+        const int cell = cell0 + u * (kQbThreads / 16);
+        const int kb = cell / RT;
+        const int64_t row = chunk * RT + cell % RT;
+        const int col = kb * kBlock + c8;
+        at[u] = kb < kblocks && row < rows && col < cols ? row * cols + col : -1;
+        v[u] = at[u] >= 0 ? *reinterpret_cast<const v4i*>(x + at[u]) : v4i{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int u = 0; u < kQbUnroll; ++u) {
+        const float a = row16_max(vec_absmax<DT>(v[u]));
+        const float s = scale_from_amax(a);
+        if (at[u] >= 0) {
+            *reinterpret_cast<v2i*>(q + at[u]) = vec_quantize<DT>(v[u], Quotient(s));
+            if (c8 == 0) {
+                const int cell = cell0 + u * (kQbThreads / 16);
+                scale[(cell / RT) * rows + chunk * RT + cell % RT] = s;
+            }
+        }
+    }
+}
+
+// One workgroup per 128 x 128 block of a weight matrix: 8 vectors of 8
+// values per thread, kept between the amax and the codes.
+constexpr int kQwThreads = 256;
+template <int DT>
+__global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
+    const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int nblocks, int kblocks,
+    uint8_t* __restrict__ q, float* __restrict__ scale)
+{
+    __shared__ float lds[kQwThreads / 64];
+    const int64_t cell = blockIdx.x;
+    const int64_t bn = cell / kblocks;                   // batch * nblocks + row block
+    const int kb = (int)(cell - bn * kblocks);
+    const int64_t batch = bn / nblocks;
+    const int64_t row0 = (bn - batch * nblocks) * kBlock + (threadIdx.x >> 4);
+    const int64_t col = (int64_t)kb * kBlock + (threadIdx.x & 15) * 8;
+    const int64_t base = batch * rows * cols + col;
+    constexpr int V = kBlock / (kQwThreads / 16);
+    v4i v[V];
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t row = row0 + j * (kQwThreads / 16);
+        v[j] = row < rows && col < cols ? *reinterpret_cast<const v4i*>(w + base + row * cols)
+                                        : v4i{0, 0, 0, 0};
+        m = fmaxf(m, vec_absmax<DT>(v[j]));
+    }
+    const float a = block_max<kQwThreads>(m, lds);
+    const float s = scale_from_amax(a);
+    const Quotient d(s);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        const int64_t row = row0 + j * (kQwThreads / 16);
+        if (row < rows && col < cols)
+            *reinterpret_cast<v2i*>(q + base + row * cols) = vec_quantize<DT>(v[j], d);
+    }
+    if (threadIdx.x == 0) scale[cell] = s;
+}
+
+// ---------------------------------------------------------------- decode product (M <= 16)
+// The weight matrix is read once and bounds the time, so the loads are shaped
+// for it: a wave's load instruction reads the 128-byte lines of eight weight
+// rows, lane (r, g) = (l % 16, l / 16) the 16-byte unit 4 (r / 8) + g of row
+// r % 8.  That is also the operand layout of the product, without any
+// exchange between lanes: as the first operand of v_mfma_f32_16x16x32 the
+// eight lanes r and r + 8 of a row carry its two 64-byte halves as two
+// separate operand rows, and the activations are loaded in the same way for
+// eight tokens as the second operand.  Of the 16 x 16 results the two
+// diagonal 8 x 8 quadrants pair equal halves, and their sum is the block's
+// product; the other two are dropped.  The matrix cores have that half to
+// spare at these sizes.  A lane's four results are weight rows (4 g .. 4 g +
+// 3) % 8 for the one token r % 8, so it needs one activation scale.
+//
+// A workgroup owns 8 * RT weight rows (RT row tiles that share the activation
+// loads); its waves interleave over the K blocks.  Tokens come in MT groups
+// of eight.
+constexpr int kGbWaves = 16;
+constexpr int kGbUnroll = 2;
+
+__device__ __forceinline__ v4f mfma_pair(const v4i& w, const v4i& a, v4f c)
+{
+    const long w0 = __builtin_bit_cast(long, v2i{w[0], w[1]}), w1 = __builtin_bit_cast(long, v2i{w[2], w[3]});
+    const long a0 = __builtin_bit_cast(long, v2i{a[0], a[1]}), a1 = __builtin_bit_cast(long, v2i{a[2], a[3]});
+    c = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(w0, a0, c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(w1, a1, c, 0, 0, 0);
+}
+
+template <int MT, int RT>
+__global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
+    const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
+    const float* __restrict__ sw, uint16_t* __restrict__ y, int M, int N, int K)
+{
+    constexpr int U = kGbUnroll;
+    __shared__ float red[kGbWaves][2][MT * RT][8][9];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4, half = r >> 3;
+    const int n0 = blockIdx.x * 8 * RT;
+    const int koff = (half * 4 + g) * 16;
+    const int nblk = (K + kBlock - 1) / kBlock;
+
+    const rsrc_t rw = make_rsrc(qw + (size_t)n0 * K, (uint32_t)(min(8 * RT, N - n0) * K));
+    const rsrc_t ra = make_rsrc(qa, (uint32_t)(M * K));
+    const rsrc_t rs = make_rsrc(sa, (uint32_t)(M * nblk * 4));
+    const float* const swb = sw + (size_t)(n0 >> 7) * nblk;
+    const uint32_t off = (uint32_t)((r & 7) * K + koff);       // of row or token r % 8
+
+    v4f acc[MT][RT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc[m][t] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    for (int kb0 = wave; kb0 < nblk; kb0 += kGbWaves * U) {
+        v4i w[U][RT], a[U][MT];
+        float s[U][MT], sb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = kb0 + u * kGbWaves;
+            const bool in = kb * kBlock + koff < K;
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+                w[u][t] = buf_load16<CP_NT>(rw, in ? off + t * 8 * K + kb * kBlock : kOOB);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                a[u][m] = buf_load16(ra, in ? off + m * 8 * K + kb * kBlock : kOOB);
+                // tokens past M read another token's scale or zero: their results are dropped
+                s[u][m] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    rs, kb < nblk ? (uint32_t)((kb * M + m * 8 + (r & 7)) * 4) : kOOB, 0, 0));
+            }
+            sb[u] = kb < nblk ? swb[kb] : 0.0f;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float f = s[u][m] * sb[u];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const v4f p = mfma_pair(w[u][t], a[u][m], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][t][e] = __builtin_fmaf(p[e], f, acc[m][t][e]);
+                }
+            }
+    }
+
+    if ((g >> 1) == half) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t = 0; t < RT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    red[wave][half][m * RT + t][r & 7][(4 * g + e) & 7] = acc[m][t][e];
+    }
+    __syncthreads();
+    for (int o = threadIdx.x; o < MT * RT * 64; o += kGbWaves * 64) {
+        const int row = o & 7, t = (o >> 3) % RT, mm = (o >> 3) / RT;     // token mm, row 8 t + row
+        const int n = n0 + t * 8 + row;
+        if (mm >= M || n >= N) continue;
+        float v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kGbWaves; ++w)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) v += red[w][h][(mm >> 3) * RT + t][mm & 7][row];
+        y[(size_t)mm * N + n] = (uint16_t)f32_to_bf16_bits(v);
+    }
+}
+
+// ---------------------------------------------------------------- tile product (M > 16)
+// The ring-buffered tile GEMM: BM x BN outputs per workgroup, K steps of 128
+// = one block, both operands and the step's activation scales brought to LDS
+// by direct global->LDS loads, AST stages for the activations and their
+// scales, WST >= AST for the weights.  A wave's TN columns lie inside one
+// 128-row weight block (TN divides 128 and tiles start at multiples of BN),
+// so its weight scale is one scalar per step.
+//
+// Each v_mfma_f32_16x16x128 covers exactly one block.  It starts from a zero
+// accumulator, and its four results are folded into the running sum with the
+// product of the two scales: four FMAs beside the matrix instruction's 32
+// cycles.
+template <int BM, int BN, int WM, int WN, int AST, int WST>
+__global__ __launch_bounds__(WM * WN * 64) __attribute__((amdgpu_waves_per_eu(2)))
+void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__ sa,
+                       const uint8_t* __restrict__ qw, const float* __restrict__ sw,
+                       uint16_t* __restrict__ y, int M, int N, int K)
+{
+    constexpr int NW = WM * WN;
+    constexpr int BK = kBlock;
+    constexpr int TM = BM / WM, TN = BN / WN;
+    constexpr int FM = TM / 16, FN = TN / 16;
+    static_assert(BM % 64 == 0 && 128 % TN == 0, "one weight scale per wave, whole scale loads");
+    constexpr int ASTAGE = BM * BK, WSTAGE = BN * BK;
+    constexpr int ABPW = BM / 8 / NW, WBPW = BN / 8 / NW;   // 1 KiB DMA blocks per wave per step
+    static_assert(ABPW * 8 * NW == BM && WBPW * 8 * NW == BN, "whole DMA blocks per wave");
+    static_assert(AST >= 2 && WST >= AST, "ring depths");
+    constexpr int AL = ABPW + 1;                            // loads of one activation stage
+    constexpr int ALLOW = (AST < WST ? WBPW : 0) + (AST - 2) * (AL + WBPW);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    uint8_t* const a_lds = lds;
+    uint8_t* const w_lds = lds + AST * ASTAGE;
+    float* const s_lds = reinterpret_cast<float*>(lds + AST * ASTAGE + WST * WSTAGE);  // AST x BM
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / WN, wn = wave % WN;
+    const int r = lane & 15, g = lane >> 4;
+
+    const int tiles_m = (int)(((int64_t)M + BM - 1) / BM);
+    const int bid = xcd_remap(blockIdx.x, gridDim.x);
+    const int m0 = (bid % tiles_m) * BM;
+    const int n0 = (bid / tiles_m) * BN;
+    const int rows_m = min(BM, M - m0);
+    const rsrc_t ra = make_rsrc(qa + (size_t)m0 * K, (uint32_t)(rows_m * K));
+    const rsrc_t rw = make_rsrc(qw + (size_t)n0 * K, (uint32_t)(min(BN, N - n0) * K));
+
+    // lane l of a DMA block lands in row 8b + l/8 at position l%8, which
+    // holds unit (l%8) ^ (l/8) of that row
+    const int du = (lane & 7) ^ (lane >> 3);
+    const uint32_t rowoff = (uint32_t)((lane >> 3) * K + du * 16);
+    const int nk = (K + BK - 1) / BK;
+    // the lane's offset in step kt; past the end of K it is moved out of range
+    // by an addition (offsets within a tile are below 2^31), not by a branch:
+    // the K loop stays one basic block
+    auto koff = [&](int kt) {
+        const bool kin = kt < nk && kt * BK + du * 16 < K;
+        return rowoff + (uint32_t)(kt * BK) + (kin ? 0u : kOOB);
+    };
+    // 64 scales per wave and step; with more waves than BM / 64 some load the
+    // same ones, which keeps the wait counts of all waves equal
+    const int srow = (wave % (BM / 64)) * 64;
+    auto dma_a = [&](int kt) {
+        const uint32_t off = koff(kt);
+        uint8_t* base = a_lds + (kt % AST) * ASTAGE + wave * ABPW * 1024;
+#pragma unroll
+        for (int j = 0; j < ABPW; ++j)
+            dma_load16(ra, base + j * 1024, (uint32_t)((wave * ABPW + j) * 8 * K) + off);
+        const int ks = min(kt, nk - 1);
+        const rsrc_t rs = make_rsrc(sa + (size_t)ks * M + m0, (uint32_t)(rows_m * 4));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rs, (__attribute__((address_space(3))) void*)(s_lds + (kt % AST) * BM + srow), 4,
+            (uint32_t)((srow + lane) * 4), 0, 0, 0);
+    };
+    auto dma_w = [&](int kt) {
+        const uint32_t off = koff(kt);
+        uint8_t* base = w_lds + (kt % WST) * WSTAGE + wave * WBPW * 1024;
+#pragma unroll
+        for (int j = 0; j < WBPW; ++j)
+            dma_load16(rw, base + j * 1024, (uint32_t)((wave * WBPW + j) * 8 * K) + off);
+    };
+    // a wave whose columns lie past N reads the last row block's scales
+    const int nb_last = (N - 1) >> 7;
+    const float* const swb = sw + (size_t)min((n0 + wn * TN) >> 7, nb_last) * nk;
+
+    v4f acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    // load groups and waits as in gemm_f8_kernel: the group issued after step
+    // j holds A(j + AST) (with its scales) then W(j + WST)
+#pragma unroll
+    for (int j = -WST; j < 0; ++j) {
+        if (j + AST >= 0) dma_a(j + AST);
+        dma_w(j + WST);
+    }
+    float swk = swb[0];
+    wait_vm<ALLOW + AL + WBPW>();
+    __syncthreads();
+
+    for (int kt = 0; kt < nk; ++kt) {
+        const uint8_t* As = a_lds + (kt % AST) * ASTAGE;
+        const uint8_t* Ws = w_lds + (kt % WST) * WSTAGE;
+        const float* Ss = s_lds + (kt % AST) * BM + wm * TM + r;
+        const float swn = swb[min(kt + 1, nk - 1)];
+        auto frag = [&](const uint8_t* S, int row) {
+            return cat(*reinterpret_cast<const v4i*>(S + swz128(row, g)),
+                       *reinterpret_cast<const v4i*>(S + swz128(row, g + 4)));
+        };
+        v8i wf[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) wf[j] = frag(Ws, wn * TN + j * 16 + r);
+        v8i af[2];
+        af[0] = frag(As, wm * TM + r);
+        // block products of one activation fragment, folded into the sums
+        // while the next fragment's MFMAs run
+        v4f p[2][FN];
+        float f[2];
+        auto fold = [&](int i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[i][j][e] = __builtin_fmaf(p[i & 1][j][e], f[i & 1], acc[i][j][e]);
+            // keep the compiler from moving the sums past the end of the step
+            // (it would hold every block product until then)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+        };
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            if (i + 1 < FM) af[(i + 1) & 1] = frag(As, wm * TM + (i + 1) * 16 + r);
+            f[i & 1] = Ss[i * 16] * swk;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                p[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                    wf[j], af[i & 1], v4f{0.f, 0.f, 0.f, 0.f}, WF_E4M3, WF_E4M3, 0, 0, 0, 0);
+            if (i > 0) fold(i - 1);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        fold(FM - 1);
+        swk = swn;
+        wait_vm<ALLOW>();
+        __syncthreads();                       // stage k of both rings is free
+        dma_a(kt + AST);
+        dma_w(kt + WST);
+    }
+    wait_vm<0>();                              // nothing left in flight into LDS
+
+    // acc[i][j][e] is output row mb + 16 i + r, column nb + 16 j + 4 g + e
+    const int mb = m0 + wm * TM, nb = n0 + wn * TN;
+    const bool vec = (N & 3) == 0;             // 8-byte aligned groups of 4 columns
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int m = mb + i * 16 + r;
+        if (m >= M) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int n = nb + j * 16 + 4 * g;
+            uint16_t* dst = y + (size_t)m * N + n;
+            if (vec && n + 3 < N) {
+                const uint32_t lo = f32_to_bf16_bits(acc[i][j][0]) | (f32_to_bf16_bits(acc[i][j][1]) << 16);
+                const uint32_t hi = f32_to_bf16_bits(acc[i][j][2]) | (f32_to_bf16_bits(acc[i][j][3]) << 16);
+                *reinterpret_cast<v2i*>(dst) = v2i{(int)lo, (int)hi};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < N) dst[e] = (uint16_t)f32_to_bf16_bits(acc[i][j][e]);
+            }
+        }
+    }
+}
+
+template <int BM, int BN, int WM, int WN, int AST, int WST>
+hipError_t launch_block_tile(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
+                             uint16_t* y, int M, int N, int K, hipStream_t stream)
+{
+    auto kern = gemm_block_kernel<BM, BN, WM, WN, AST, WST>;
+    constexpr size_t lds = ((size_t)AST * BM + (size_t)WST * BN) * 128 + (size_t)AST * BM * 4;
+    static_assert(lds <= 160 * 1024, "LDS of one CU");
+    static std::atomic<uint64_t> attr_devices{0};
+    if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern), lds, attr_devices);
+        e != hipSuccess)
+        return e;
+    const int64_t grid = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    kern<<<(int)grid, WM * WN * 64, lds, stream>>>(qa, sa, qw, sw, y, M, N, K);
+    return hipGetLastError();
+}
+
+template <int DT, int RT>
+hipError_t launch_quant_blocks_rt(const void* x, int64_t rows, int64_t cols, uint8_t* q,
+                                  float* scale, hipStream_t stream)
+{
+    const int64_t kblocks = blocks_of(cols);
+    const int64_t cells = kblocks * RT, per_wg = kQbThreads / 16 * kQbUnroll;
+    const int64_t per_chunk = (cells + per_wg - 1) / per_wg;
+    const int64_t grid = per_chunk * ((rows + RT - 1) / RT);
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    quant_blocks_kernel<DT, RT><<<(int)grid, kQbThreads, 0, stream>>>(
+        static_cast<const uint16_t*>(x), rows, (int)cols, (int)kblocks, (int)per_chunk, q, scale);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_quant_blocks_dt(const void* x, int64_t rows, int64_t cols, uint8_t* q,
+                                  float* scale, hipStream_t stream)
+{
+    return rows >= 16 ? launch_quant_blocks_rt<DT, 16>(x, rows, cols, q, scale, stream)
+                      : launch_quant_blocks_rt<DT, 1>(x, rows, cols, q, scale, stream);
+}
+
+}  // namespace
+
+hipError_t launch_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* q,
+                                  float* scale, hipStream_t stream)
+{
+    return dtype == DT_BF16 ? launch_quant_blocks_dt<DT_BF16>(x, rows, cols, q, scale, stream)
+                            : launch_quant_blocks_dt<DT_FP16>(x, rows, cols, q, scale, stream);
+}
+
+hipError_t launch_quantize_weight_blocks(const void* w, int dtype, int64_t batch, int64_t rows,
+                                         int64_t cols, uint8_t* q, float* scale, hipStream_t stream)
+{
+    const int64_t nb = blocks_of(rows), kb = blocks_of(cols);
+    const int64_t grid = batch * nb * kb;
+    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const auto* x = static_cast<const uint16_t*>(w);
+    if (dtype == DT_BF16)
+        quant_weight_blocks_kernel<DT_BF16><<<(int)grid, kQwThreads, 0, stream>>>(
+            x, rows, cols, (int)nb, (int)kb, q, scale);
+    else
+        quant_weight_blocks_kernel<DT_FP16><<<(int)grid, kQwThreads, 0, stream>>>(
+            x, rows, cols, (int)nb, (int)kb, q, scale);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                             const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
+{
+    constexpr int RT = 2;
+    const int grid = (int)(((int64_t)N + 8 * RT - 1) / (8 * RT));
+    if (M <= 8)
+        gemv_block_kernel<1, RT><<<grid, kGbWaves * 64, 0, stream>>>(qa, sa, qw, sw, y, M, N, K);
+    else
+        gemv_block_kernel<2, RT><<<grid, kGbWaves * 64, 0, stream>>>(qa, sa, qw, sw, y, M, N, K);
+    return hipGetLastError();
+}
+
+hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                             const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
+{
+    if (M > 512) return launch_block_tile<256, 256, 2, 4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
+    if (M > 64) return launch_block_tile<128, 128, 2, 4, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
+    return launch_block_tile<64, 64, 2, 2, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
+}
+
+}  // namespace fp8q

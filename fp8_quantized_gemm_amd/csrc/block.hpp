@@ -1,0 +1,31 @@
+// Launchers of the block-scaled FP8 operators: E4M3 codes with one fp32 scale
+// per 128 values along K (activations) or per 128 x 128 block (weights).
+#pragma once
+
+#include "common.hpp"
+
+namespace fp8q {
+
+constexpr int kBlock = 128;              // values per scale along K, weight rows per scale
+inline int64_t blocks_of(int64_t n) { return (n + kBlock - 1) / kBlock; }
+
+// x[rows, cols] -> codes and scale[K blocks, rows], one per 1 x 128 block.
+hipError_t launch_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols, uint8_t* q,
+                                  float* scale, hipStream_t stream);
+// w[batch, rows, cols] -> codes and scale[batch, row blocks, K blocks].
+hipError_t launch_quantize_weight_blocks(const void* w, int dtype, int64_t batch, int64_t rows,
+                                         int64_t cols, uint8_t* q, float* scale,
+                                         hipStream_t stream);
+
+// The product of block-scaled codes, sa[K blocks, M] and sw[N blocks, K
+// blocks], M <= kGemvBlockMaxM on the weight-streaming kernel, larger M on
+// the MFMA tile kernel.
+constexpr int kGemvBlockMaxM = 16;
+hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                             const float* sw, uint16_t* y, int M, int N, int K,
+                             hipStream_t stream);
+hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                             const float* sw, uint16_t* y, int M, int N, int K,
+                             hipStream_t stream);
+
+}  // namespace fp8q

@@ -20,32 +20,10 @@
 // (which share the weight tile) land on the same XCD and its L2.
 #include <atomic>
 
-#include "common.hpp"
+#include "tile.hpp"
 
 namespace fp8q {
 namespace {
-
-constexpr int kCUs = 256;                // compute units of an MI355X
-
-
-__device__ __forceinline__ v8i cat(const v4i& lo, const v4i& hi)
-{
-    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-}
-
-// Workgroups are dispatched round-robin over the 8 XCDs; map the launch index
-// so that each XCD receives a contiguous range of logical tile ids.
-__device__ __forceinline__ int xcd_remap(int bid, int nb)
-{
-    const int q = nb >> 3, rem = nb & 7;
-    const int xcd = bid & 7, idx = bid >> 3;
-    return xcd < rem ? xcd * (q + 1) + idx : rem * (q + 1) + (xcd - rem) * q + idx;
-}
-
-// Byte offset of 16-byte unit `u` of row `row` in a tile with 128-byte rows.
-__device__ __forceinline__ int swz128(int row, int u) { return row * 128 + ((u ^ (row & 7)) << 4); }
-// ... with 64-byte rows (4 units).
-__device__ __forceinline__ int swz64(int row, int u) { return row * 64 + ((u ^ ((row >> 1) & 3)) << 4); }
 
 template <int OUTF, int FM = 4, int FN = 4>
 __device__ __forceinline__ void store_tile(uint16_t* __restrict__ y, const v4f (&acc)[FM][FN], float s,
@@ -65,18 +43,6 @@ __device__ __forceinline__ void store_tile(uint16_t* __restrict__ y, const v4f (
         }
     }
 }
-
-// The compiler does not order LDS reads after asynchronous direct-to-LDS
-// loads, so a kernel that uses them waits explicitly (s_waitcnt vmcnt) for
-// its own loads and then synchronizes the workgroup before reading.
-template <int N_OUTSTANDING>
-__device__ __forceinline__ void wait_vm()
-{
-    // s_waitcnt vmcnt(N) with expcnt and lgkmcnt left at their maxima (gfx9 encoding)
-    static_assert(N_OUTSTANDING >= 0 && N_OUTSTANDING < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N_OUTSTANDING & 15) | ((N_OUTSTANDING >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
 
 // ---------------------------------------------------------------- FP8 tile GEMM
 // BM x BN output tile per workgroup of WM x WN waves, each wave owning a

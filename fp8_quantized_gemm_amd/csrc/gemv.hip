@@ -24,7 +24,7 @@
 // lane l holds D[4g + i][l % 16], i = 0..3.
 #include <algorithm>
 
-#include "common.hpp"
+#include "tile.hpp"
 
 namespace fp8q {
 namespace {
@@ -35,11 +35,6 @@ __device__ __forceinline__ v4f mfma_f8(const v8i& a, const v8i& b, const v4f& c)
     // A (activations) is always E4M3; B (weights) is E4M3 or E5M2.
     constexpr int BF = mfma_format(WFMT);
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, WF_E4M3, BF, 0, 0, 0, 0);
-}
-
-__device__ __forceinline__ v8i cat(const v4i& lo, const v4i& hi)
-{
-    return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
 // Weight loads of whole 128-byte lines.  For one 128-byte K block of a
@@ -491,7 +486,6 @@ constexpr int kGemvUnroll = 2;
 // 2 x 256 workgroups a CU streams at most ceil(tiles / 256) tiles (768 tiles:
 // three per CU, where 384 workgroups of two left half the CUs with four;
 // measured on the QKV projection at M = 4 / 8: 13.5 -> 12.0 / 14.8 -> 13.4 us).
-constexpr int kCUs = 256;                  // compute units of an MI355X
 constexpr int kGemvSlots = 2 * kCUs;
 inline int64_t gemv_tiles_per_workgroup(int64_t N)
 {

@@ -52,6 +52,10 @@ _SIGS = {
     "nested_linear_fp8_e4m3": (_i, [_p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
     "fp8_linear_delayed": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _i64, _p, _i64, _i64, _i64,
                                 _p]),
+    "fp8_quantize_blocks": (_i, [_p, _i, _i64, _i64, _p, _p, _p]),
+    "fp8_quantize_weight_blocks": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p]),
+    "fp8_gemm_blockwise": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
+    "fp8_linear_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -272,6 +276,118 @@ def fp8_quantize_kv(x: torch.Tensor, q: torch.Tensor | None = None,
         _dev(x, "x"), code, T, H, D, _dev(q, "q", torch.uint8, (T, H, D)),
         _vector(scale, "scale", H), _vector(amax, "amax", H), _stream(x)))
     return q, scale, amax
+
+
+# Values per scale along K, and weight rows per scale, of the block-scaled calls.
+BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK
+
+
+def _ptr(t: torch.Tensor, name: str, dtype, shape, index: int) -> int:
+    """_dev without its cost where nothing is wrong (a decode call takes a few
+    microseconds); index is the current device's."""
+    if (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    return _dev(t, name, dtype, shape).value or 0
+
+
+def _where(t: torch.Tensor):
+    """The current device's index and its current stream."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError("the arguments must be CUDA (HIP) tensors")
+    index = torch.cuda.current_device()
+    return index, torch.cuda.current_stream(index).cuda_stream
+
+
+def fp8_quantize_blocks(x: torch.Tensor, q: torch.Tensor | None = None,
+                        scale: torch.Tensor | None = None):
+    """One E4M3 scale per 1 x 128 block of x[rows, cols] (bf16/fp16), along cols.
+    Returns (q uint8 [rows, cols], scale float32 [ceil(cols / 128), rows])."""
+    code = _dtype_code(x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be 2-D [rows, cols], got {tuple(x.shape)}")
+    rows, cols = x.shape
+    if q is None:
+        q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((_blocks(cols), rows), dtype=torch.float32, device=x.device)
+    index, stream = _where(x)
+    _check("fp8_quantize_blocks", lib.fp8_quantize_blocks(
+        _ptr(x, "x", x.dtype, x.shape, index), code, rows, cols,
+        _ptr(q, "q", torch.uint8, (rows, cols), index),
+        _ptr(scale, "scale", torch.float32, (_blocks(cols), rows), index), stream))
+    return q, scale
+
+
+def fp8_quantize_weight_blocks(w: torch.Tensor, q: torch.Tensor | None = None,
+                               scale: torch.Tensor | None = None):
+    """One E4M3 scale per 128 x 128 block of each matrix of w[..., N, K] (bf16/fp16;
+    leading dimensions count matrices, such as experts).  Returns (q uint8 like w,
+    scale float32 [..., ceil(N / 128), ceil(K / 128)])."""
+    code = _dtype_code(w)
+    if w.dim() < 2:
+        raise ValueError(f"w must be [..., N, K], got {tuple(w.shape)}")
+    N, K = w.shape[-2:]
+    lead = tuple(w.shape[:-2])
+    batch = 1
+    for d in lead:
+        batch *= d
+    sshape = lead + (_blocks(N), _blocks(K))
+    if q is None:
+        q = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    if scale is None:
+        scale = torch.empty(sshape, dtype=torch.float32, device=w.device)
+    index, stream = _where(w)
+    _check("fp8_quantize_weight_blocks", lib.fp8_quantize_weight_blocks(
+        _ptr(w, "w", w.dtype, w.shape, index), code, batch, N, K,
+        _ptr(q, "q", torch.uint8, w.shape, index),
+        _ptr(scale, "scale", torch.float32, sshape, index), stream))
+    return q, scale
+
+
+def fp8_gemm_blockwise(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+                       y: torch.Tensor | None = None) -> torch.Tensor:
+    """y[M,N] bf16 = sum over 128-blocks b of sa[b,m] * sw[n/128,b] * (qa . qw^T)_b:
+    E4M3 codes with sa float32 [ceil(K/128), M] and sw float32 [ceil(N/128),
+    ceil(K/128)], fp32 accumulation."""
+    M, N, K = _mnk(qa, qw)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=qa.device)
+    kb = _blocks(K)
+    index, stream = _where(qa)
+    _check("fp8_gemm_blockwise", lib.fp8_gemm_blockwise(
+        _ptr(qa, "qa", torch.uint8, (M, K), index), _ptr(sa, "sa", torch.float32, (kb, M), index),
+        _ptr(qw, "qw", torch.uint8, (N, K), index),
+        _ptr(sw, "sw", torch.float32, (_blocks(N), kb), index),
+        _ptr(y, "y", torch.bfloat16, (M, N), index), M, N, K, stream))
+    return y
+
+
+def fp8_linear_blockwise(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
+                         y: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                         sa: torch.Tensor | None = None):
+    """fp8_quantize_blocks on x[M,K], then fp8_gemm_blockwise with the weight's codes
+    and block scales.  Returns (y, q, sa)."""
+    code = _dtype_code(x)
+    M, N, K = _mnk(x, qw)
+    kb = _blocks(K)
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    if sa is None:
+        sa = torch.empty((kb, M), dtype=torch.float32, device=x.device)
+    index, stream = _where(x)
+    _check("fp8_linear_blockwise", lib.fp8_linear_blockwise(
+        _ptr(x, "x", x.dtype, (M, K), index), code, _ptr(qw, "qw", torch.uint8, (N, K), index),
+        _ptr(sw, "sw", torch.float32, (_blocks(N), kb), index),
+        _ptr(y, "y", torch.bfloat16, (M, N), index), _ptr(q, "q", torch.uint8, (M, K), index),
+        _ptr(sa, "sa", torch.float32, (kb, M), index), M, N, K, stream))
+    return y, q, sa
 
 
 class DelayedScaling:

@@ -1,6 +1,6 @@
 /*
- * fp8q.h - C ABI of libfp8q: FP8 E4M3 linear layers (per-tensor scales, or per-token
- * activation and per-channel weight scales) and the
+ * fp8q.h - C ABI of libfp8q: FP8 E4M3 linear layers (per-tensor scales, per-token
+ * activation and per-channel weight scales, or a scale per block of 128) and the
  * NestedFP dual-precision GEMM on AMD MI355X (gfx950).
  *
  * Pages whose statement of the problem these calls follow:
@@ -30,8 +30,9 @@
  *    input or output (FP8Q_ERR_OVERLAP): other workgroups still read and
  *    write those bytes.  Inputs may share memory with each other.  The one
  *    exception is the y of the linear calls (fp8_linear, fp8_linear_rowwise,
- *    fp8_linear_delayed, nested_linear_fp8, nested_linear_fp8_e4m3), which
- *    may lie over their activation input (in place).
+ *    fp8_linear_delayed, fp8_linear_blockwise, nested_linear_fp8,
+ *    nested_linear_fp8_e4m3), which may lie over their activation input (in
+ *    place).
  *    A failed launch returns FP8Q_ERR_LAUNCH; faults inside a kernel surface
  *    at the caller's next synchronization, as for any HIP work.
  *  - Calls on different streams are independent (no shared mutable state).
@@ -354,6 +355,53 @@ FP8Q_API fp8q_status nested_gemm_fp8_e4m3(const uint8_t* qa, const float* sa, co
 FP8Q_API fp8q_status nested_linear_fp8_e4m3(const uint16_t* a, const uint8_t* hi, uint16_t* y,
                                             uint8_t* q, float* scale, float* amax, int64_t M,
                                             int64_t N, int64_t K, fp8q_stream stream);
+
+/*
+ * Block scaling: an fp32 scale for every 128 values along K.  Activations
+ * have one scale per 1 x 128 block, weights one per 128 x 128 block; the last
+ * block of a row or column range may be shorter.  KB = ceil(K / 128),
+ * NB = ceil(N / 128).
+ *
+ * fp8_quantize_blocks - x[rows, cols] into 1 x 128 blocks along cols; each
+ *   block is quantized exactly as fp8_quantize_act would quantize it alone:
+ *   x[rows,cols]    in : bf16/fp16 bit patterns (dtype as for fp8_quantize_act)
+ *   q[rows,cols]    out: E4M3 codes
+ *   scale[KB,rows]  out: fl32(amax / 448) of the block, or 1.0 when amax == 0
+ *                        (K-block major: one K step's scales are contiguous)
+ *   1 <= rows <= 2^31-1;  16 <= cols <= 2^22 and cols % 16 == 0.  One launch.
+ *
+ * fp8_quantize_weight_blocks - w[batch, rows, cols] into 128 x 128 blocks
+ *   (offline, like every weight quantization; batch counts matrices of one
+ *   shape, such as the experts of a layer):
+ *   q[batch,rows,cols] out, scale[batch,NB,KB] out (rows = N, cols = K).
+ *   batch, rows >= 1;  cols as above;  batch*rows*cols <= 2^40.
+ *
+ * fp8_gemm_blockwise - y[m,n] = bf16( sum_b sa[b,m] * sw[n/128,b] *
+ *   sum_{k in block b} dec(qa[m,k]) dec(qw[n,k]) ), fp32 accumulation within
+ *   and across blocks, one rounding at the end.
+ *   qa[M,K], sa[KB,M] in: activation codes and scales
+ *   qw[N,K], sw[NB,KB] in: weight codes and scales
+ *   y[M,N]   out: bf16 bit patterns
+ *   Size rules as fp8_gemm.  M <= 16 runs the weight-streaming kernel.
+ *
+ * fp8_linear_blockwise - fp8_quantize_blocks on the activation, then
+ *   fp8_gemm_blockwise on its codes; bit-identical to the two calls made in
+ *   sequence:
+ *   x[M,K] in : bf16/fp16 activation;  qw[N,K], sw[NB,KB] in
+ *   y[M,N] out;  q[M,K], sa[KB,M] out: the activation's codes and scales
+ *   y may lie over x.  Size rules as fp8_gemm.
+ */
+FP8Q_API fp8q_status fp8_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols,
+                                         uint8_t* q, float* scale, fp8q_stream stream);
+FP8Q_API fp8q_status fp8_quantize_weight_blocks(const void* w, int dtype, int64_t batch,
+                                                int64_t rows, int64_t cols, uint8_t* q,
+                                                float* scale, fp8q_stream stream);
+FP8Q_API fp8q_status fp8_gemm_blockwise(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                                        const float* sw, uint16_t* y, int64_t M, int64_t N,
+                                        int64_t K, fp8q_stream stream);
+FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw,
+                                          const float* sw, uint16_t* y, uint8_t* q, float* sa,
+                                          int64_t M, int64_t N, int64_t K, fp8q_stream stream);
 
 /*
  * fp8q_e4m3_encode_f32 - the device E4M3 encoder used by fp8_quantize_act,
