@@ -14,6 +14,8 @@ _API = (
     # a scale per block of 128: quantizers, GEMM, quantize + GEMM
     "fp8_quantize_blocks", "fp8_quantize_weight_blocks", "fp8_gemm_blockwise",
     "fp8_linear_blockwise",
+    # mixture-of-experts layer on block-scaled weights
+    "fp8_moe_blockwise", "moe_work_bytes",
     # delayed scaling with an amax history
     "DelayedScaling", "fp8_quantize_act_delayed", "fp8_linear_delayed",
     # FP8 KV-cache quantizer (one scale per head)

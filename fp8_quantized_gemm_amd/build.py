@@ -18,7 +18,7 @@ OUT = os.path.join(HERE, "libfp8q.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quant.hip", "gemv.hip", "linear.hip", "gemm.hip", "nested.hip", "block.hip",
-           "api.hip"]
+           "moe.hip", "api.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -597,6 +597,43 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
     return finish("fp8_linear_blockwise", e);
 }
 
+int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k)
+{
+    if (T < 1 || T > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || I < 16 || I > kMoeMaxDim)
+        return 0;
+    return kMoeRoutingBytes + T * top_k * I * 2;
+}
+
+fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits, const uint8_t* w13,
+                              const float* s13, const uint8_t* w2, const float* s2, uint16_t* y,
+                              int32_t* ids, float* weights, void* work, int64_t T, int64_t H,
+                              int64_t I, int64_t E, int64_t top_k, int renormalize,
+                              fp8q_stream stream)
+{
+    if (!x || !logits || !w13 || !s13 || !w2 || !s2 || !y || !ids || !weights || !work)
+        return FP8Q_ERR_NULL;
+    if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
+    if (T < 1 || T > kMoeMaxTokens || H < 16 || H > kMoeMaxDim || (H % 16) != 0 || I < 16 ||
+        I > kMoeMaxDim || (I % 16) != 0 || E < 1 || E > kMoeMaxExperts || top_k < 1 ||
+        top_k > kMoeMaxTopK || top_k > E)
+        return FP8Q_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(w13) || !aligned16(w2) || !aligned16(y) || !aligned16(work) ||
+        !aligned4(logits) || !aligned4(s13) || !aligned4(s2) || !aligned4(ids) || !aligned4(weights))
+        return FP8Q_ERR_ALIGN;
+    const Buf bx{x, u64(T) * u64(H) * 2}, bl{logits, u64(T) * u64(E) * 4},
+        bw13{w13, u64(E) * 2 * u64(I) * u64(H)}, bs13{s13, u64(E) * 2 * weight_scale_bytes(I, H)},
+        bw2{w2, u64(E) * u64(H) * u64(I)}, bs2{s2, u64(E) * weight_scale_bytes(H, I)},
+        by{y, u64(T) * u64(H) * 2}, bi{ids, u64(T) * u64(top_k) * 4},
+        bw{weights, u64(T) * u64(top_k) * 4},
+        bk{work, u64(fp8_moe_blockwise_work_bytes(T, I, top_k))};
+    FP8Q_TRY(check_apart({bi, bw, bk}, {bx, bl, bw13, bs13, bw2, bs2, by}));
+    FP8Q_TRY(check_apart({by}, {bl, bw13, bs13, bw2, bs2}));
+    FP8Q_TRY(check_device());
+    const MoeArgs a{x, logits, w13, s13, w2, s2, y, ids, weights, work, (int)T, (int)H, (int)I,
+                    (int)E, (int)top_k, renormalize != 0};
+    return finish("fp8_moe_blockwise", launch_moe(a, dtype, (hipStream_t)stream));
+}
+
 fp8q_status fp8q_e4m3_encode_f32(const float* v, uint8_t* q, int64_t n, fp8q_stream stream)
 {
     if (!v || !q) return FP8Q_ERR_NULL;

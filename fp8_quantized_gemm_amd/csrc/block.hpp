@@ -28,4 +28,25 @@ hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* 
                              const float* sw, uint16_t* y, int M, int N, int K,
                              hipStream_t stream);
 
+// A mixture-of-experts layer for a few tokens (see moe.hip).
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxTopK = 16;
+constexpr int64_t kMoeMaxDim = 1 << 16;  // H and I
+constexpr int kMoeRoutingBytes = 8448;   // head of the workspace; the activations h follow
+struct MoeArgs {
+    const void* x;           // [T, H]
+    const float* logits;     // [T, E]
+    const uint8_t* w13;      // [E, 2, I, H]
+    const float* s13;        // [E, 2, I blocks, H blocks]
+    const uint8_t* w2;       // [E, H, I]
+    const float* s2;         // [E, H blocks, I blocks]
+    uint16_t* y;             // [T, H]
+    int* ids;                // [T, top_k]
+    float* weights;          // [T, top_k]
+    void* work;              // routing, then h[T * top_k, I] bf16
+    int T, H, I, E, top_k, renormalize;
+};
+hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t stream);
+
 }  // namespace fp8q

@@ -56,6 +56,9 @@ _SIGS = {
     "fp8_quantize_weight_blocks": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p]),
     "fp8_gemm_blockwise": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
     "fp8_linear_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
+    "fp8_moe_blockwise_work_bytes": (_i64, [_i64, _i64, _i64]),
+    "fp8_moe_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64,
+                               _i64, _i, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -388,6 +391,60 @@ def fp8_linear_blockwise(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,
         _ptr(y, "y", torch.bfloat16, (M, N), index), _ptr(q, "q", torch.uint8, (M, K), index),
         _ptr(sa, "sa", torch.float32, (kb, M), index), M, N, K, stream))
     return y, q, sa
+
+
+def fp8_moe_blockwise(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor,
+                      s13: torch.Tensor, w2: torch.Tensor, s2: torch.Tensor, top_k: int,
+                      renormalize: bool = True, y: torch.Tensor | None = None,
+                      ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                      work: torch.Tensor | None = None):
+    """A mixture-of-experts layer for a few tokens: y[t] = sum over the top_k experts e of
+    token t's logits of softmax weight * W2[e] (silu(Wg[e] x[t]) * (Wu[e] x[t])).
+
+    x [T, H] bf16/fp16 (T <= 64), logits float32 [T, E] (-inf: expert off), w13 uint8
+    [E, 2, I, H] (gate, up) and w2 uint8 [E, H, I] E4M3 codes with the block scales s13
+    and s2 that fp8_quantize_weight_blocks gives.  renormalize: weights over the chosen
+    experts instead of over all.  work is scratch (uint8, allocated when not given; its
+    size is moe_work_bytes).  Returns (y bf16 [T, H], ids int32 [T, top_k], weights
+    float32 [T, top_k])."""
+    code = _dtype_code(x)
+    if x.dim() != 2 or w13.dim() != 4 or w2.dim() != 3:
+        raise ValueError(f"expected x[T,H], w13[E,2,I,H] and w2[E,H,I], got {tuple(x.shape)}, "
+                         f"{tuple(w13.shape)} and {tuple(w2.shape)}")
+    T, H = x.shape
+    E, _, I, _ = w13.shape
+    dev = x.device
+    if y is None:
+        y = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    need = lib.fp8_moe_blockwise_work_bytes(T, I, top_k)
+    if work is None:
+        work = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif work.numel() < need:
+        raise ValueError(f"work must hold at least {need} bytes, got {work.numel()}")
+    index, stream = _where(x)
+    nb_i, nb_h = _blocks(I), _blocks(H)
+    _check("fp8_moe_blockwise", lib.fp8_moe_blockwise(
+        _ptr(x, "x", x.dtype, (T, H), index), code,
+        _ptr(logits, "logits", torch.float32, (T, E), index),
+        _ptr(w13, "w13", torch.uint8, (E, 2, I, H), index),
+        _ptr(s13, "s13", torch.float32, (E, 2, nb_i, nb_h), index),
+        _ptr(w2, "w2", torch.uint8, (E, H, I), index),
+        _ptr(s2, "s2", torch.float32, (E, nb_h, nb_i), index),
+        _ptr(y, "y", torch.bfloat16, (T, H), index),
+        _ptr(ids, "ids", torch.int32, (T, top_k), index),
+        _ptr(weights, "weights", torch.float32, (T, top_k), index),
+        _ptr(work, "work", torch.uint8, work.shape, index),
+        T, H, I, E, top_k, 1 if renormalize else 0, stream))
+    return y, ids, weights
+
+
+def moe_work_bytes(tokens: int, inter: int, top_k: int) -> int:
+    """Bytes of scratch fp8_moe_blockwise needs (0 for sizes it refuses)."""
+    return int(lib.fp8_moe_blockwise_work_bytes(tokens, inter, top_k))
 
 
 class DelayedScaling:

@@ -31,8 +31,8 @@
  *    write those bytes.  Inputs may share memory with each other.  The one
  *    exception is the y of the linear calls (fp8_linear, fp8_linear_rowwise,
  *    fp8_linear_delayed, fp8_linear_blockwise, nested_linear_fp8,
- *    nested_linear_fp8_e4m3), which may lie over their activation input (in
- *    place).
+ *    nested_linear_fp8_e4m3) and of fp8_moe_blockwise, which may lie over
+ *    their activation input (in place).
  *    A failed launch returns FP8Q_ERR_LAUNCH; faults inside a kernel surface
  *    at the caller's next synchronization, as for any HIP work.
  *  - Calls on different streams are independent (no shared mutable state).
@@ -402,6 +402,43 @@ FP8Q_API fp8q_status fp8_gemm_blockwise(const uint8_t* qa, const float* sa, cons
 FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw,
                                           const float* sw, uint16_t* y, uint8_t* q, float* sa,
                                           int64_t M, int64_t N, int64_t K, fp8q_stream stream);
+
+/*
+ * fp8_moe_blockwise - a mixture-of-experts layer for a few tokens on
+ *   block-scaled E4M3 weights: the top_k experts of each token by router
+ *   logit, a gated SiLU layer in each, and the weighted sum:
+ *
+ *   y[t] = bf16( sum_j weights[t,j] * W2[e] h[t,j] ),  e = ids[t,j],
+ *   h[t,j] = bf16( silu(Wg[e] x[t]) * (Wu[e] x[t]) ),
+ *   with fp32 accumulation; the activations are not quantized.
+ *
+ *   x[T,H]      in : bf16/fp16 activations (dtype as for fp8_quantize_act)
+ *   logits[T,E] in : fp32 router logits.  -inf switches an expert off for a
+ *                    token, NaN counts as -inf; equal logits go to the lower
+ *                    expert; +inf logits share the whole weight
+ *   w13[E,2,I,H], s13[E,2,ceil(I/128),ceil(H/128)] in: gate then up
+ *                    projection of each expert, codes and block scales as
+ *                    fp8_quantize_weight_blocks gives them for E*2 matrices
+ *   w2[E,H,I], s2[E,ceil(H/128),ceil(I/128)] in: down projection
+ *   y[T,H]      out: bf16 bit patterns; may lie over x.  A token without a
+ *                    finite-or-+inf logit gets zeros
+ *   ids[T,top_k] out: the chosen experts by descending logit, -1 where fewer
+ *                    than top_k are left
+ *   weights[T,top_k] out: softmax weights, over the chosen experts
+ *                    (renormalize != 0) or over all E (0); 0 beside an id -1
+ *   work        scratch, fp8_moe_blockwise_work_bytes(T, I, top_k) bytes,
+ *                    16-byte aligned; contents before and after the call are
+ *                    of no meaning.  Calls that may run at the same time need
+ *                    one each.
+ *   1 <= T <= 64;  16 <= H, I <= 65536, multiples of 16;  1 <= E <= 512;
+ *   1 <= top_k <= min(E, 16).  Two launches.
+ */
+FP8Q_API int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k);
+FP8Q_API fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits,
+                                       const uint8_t* w13, const float* s13, const uint8_t* w2,
+                                       const float* s2, uint16_t* y, int32_t* ids, float* weights,
+                                       void* work, int64_t T, int64_t H, int64_t I, int64_t E,
+                                       int64_t top_k, int renormalize, fp8q_stream stream);
 
 /*
  * fp8q_e4m3_encode_f32 - the device E4M3 encoder used by fp8_quantize_act,
