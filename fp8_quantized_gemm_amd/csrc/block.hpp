@@ -33,7 +33,7 @@ constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
 constexpr int64_t kMoeMaxDim = 1 << 16;  // H and I
-constexpr int kMoeRoutingBytes = 8448;   // head of the workspace; the activations h follow
+constexpr int kMoeRoutingBytes = 4096;   // head of the workspace; the activations h follow
 struct MoeArgs {
     const void* x;           // [T, H]
     const float* logits;     // [T, E]

@@ -39,18 +39,8 @@ typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
 constexpr int kMoeWaves = 16;
 constexpr int kMoeThreads = kMoeWaves * 64;
-static_assert(kMoeMaxExperts <= kMoeThreads, "one thread per expert");
-
-// The chosen (token, expert) pairs grouped by expert.  Slot s, the s-th
-// expert in ascending order that any token chose, has the pairs
-// pairs[start[s]] .. pairs[start[s + 1] - 1], each t * top_k + j, ascending.
-struct Routing {
-    int count;                                  // slots
-    int expert[kMoeMaxExperts];
-    int start[kMoeMaxExperts + 1];
-    int pairs[kMaxPairs];
-};
-static_assert(sizeof(Routing) <= kMoeRoutingBytes, "head of the workspace");
+static_assert(kMoeMaxTokens <= 64, "an expert's tokens are a 64-bit mask");
+static_assert(kMoeMaxExperts * 8 <= kMoeRoutingBytes, "masks at the head of the workspace");
 
 // 16 E4M3 codes -> 16 values of the activation's type (exact), in two operands.
 template <int DT>
@@ -151,67 +141,131 @@ __device__ __forceinline__ void route_token(const float* __restrict__ logits, in
     if (id >= 0) weight /= renormalize ? chosen : total;
 }
 
-// Groups the pairs by expert; run by the whole workgroup, ids[pairs] in LDS
-// and complete.  tmp holds one int per wave.
-__device__ __forceinline__ void group_pairs(const int* ids, int npairs, int experts, Routing& rt, int* tmp)
-{
-    const int e = threadIdx.x;
-    const int lane = e & 63, wave = e >> 6;
-    int mine = 0;
-    if (e < experts)
-        for (int p = 0; p < npairs; ++p) mine += ids[p] == e;
-    // inclusive scans over experts of (chosen, pairs), packed 16 + 16 bits
-    int scan = (mine > 0 ? 1 << 16 : 0) + mine;
+// The experts that any token chose, in ascending order: 64 experts to a word.
+template <int PER>
+struct Active {
+    uint64_t word[PER];
+    int count;
+    __device__ __forceinline__ void find(const uint64_t* masks, int experts, int lane)
+    {
+        count = 0;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(scan, d);
-        if (lane >= d) scan += o;
+        for (int i = 0; i < PER; ++i) {
+            const int e = i * 64 + lane;
+            word[i] = __ballot(e < experts && masks[e] != 0);
+            count += __popcll(word[i]);
+        }
     }
-    if (lane == 63) tmp[wave] = scan;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) scan += tmp[w];
-    if (mine > 0) {
-        const int slot = (scan >> 16) - 1;
-        const int end = scan & 0xffff;
-        rt.expert[slot] = e;
-        rt.start[slot + 1] = end;
-        int at = end - mine;
-        for (int p = 0; p < npairs; ++p)
-            if (ids[p] == e) rt.pairs[at++] = p;
+    // the slot-th of them
+    __device__ __forceinline__ int expert(int slot, int lane) const
+    {
+        int e = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int n = __popcll(word[i]);
+            if (slot >= 0 && slot < n) {
+                const bool here = (word[i] >> lane & 1) != 0 && lanes_below(word[i]) == slot;
+                e = i * 64 + __ffsll((unsigned long long)__ballot(here)) - 1;
+            }
+            slot -= n;
+        }
+        return __builtin_amdgcn_readfirstlane(e);
     }
-    if (e == kMoeThreads - 1) {
-        rt.count = scan >> 16;
-        rt.start[0] = 0;
+    // set bits of a wave-uniform mask below this lane
+    static __device__ __forceinline__ int lanes_below(uint64_t m)
+    {
+        return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
     }
-    __syncthreads();
+};
+
+// An expert's tokens, the p-th of them in lane p.
+struct Tokens {
+    int count, list;
+    __device__ __forceinline__ void find(const uint64_t* masks, int e, int lane)
+    {
+        const uint64_t v = masks[e];
+        const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+        const uint64_t m = (uint64_t)hi << 32 | lo;
+        count = __popcll(m);
+        // tokens that chose the expert go to the first lanes, the others behind them
+        const int below = Active<1>::lanes_below(m);
+        const int to = (m >> lane & 1) != 0 ? below : count + lane - below;
+        list = __builtin_amdgcn_ds_permute(to << 2, lane);
+    }
+    // the p-th token, -1 past the last
+    __device__ __forceinline__ int at(int p) const
+    {
+        const int t = __shfl(list, p & 63);
+        return p < count ? t : -1;
+    }
+};
+
+// The place j of expert e among token t's choices, as t * top_k + j.
+__device__ __forceinline__ int pair_of(const int* ids, int t, int e, int top_k)
+{
+    int p = t * top_k;
+    for (int j = 0; j < top_k; ++j)
+        if (ids[t * top_k + j] == e) p = t * top_k + j;
+    return p;
 }
 
-// ---------------------------------------------------------------- gate and up projections
-constexpr int kUpCols = 16;                 // columns of h per item
-constexpr int kUpTokens = 16;               // tokens per pass over an item's weights
+// ---------------------------------------------------------------- operand layout
+// R weight rows (8 or 4) per load instruction, 1024 / R bytes of each: lane
+// (r, g) reads unit 4 (r / R) + g of row r % R.  For R = 4 an instruction
+// covers two K blocks, the block of a lane being r / 8.
+template <int R>
+struct Layout {
+    static constexpr int kBlocks = 8 / R;                  // K blocks per load
+    int row, koff, block;                                  // within the load's K range
+    __device__ __forceinline__ explicit Layout(int lane)
+    {
+        const int r = lane & 15, g = lane >> 4;
+        row = r % R;
+        koff = (r / R * 4 + g) * 16;
+        block = r / R * 64 / kBlock;                       // of the lane's results
+    }
+    // Adds up the diagonal quadrants: lane (r, g), r < R and 4 g < R, then
+    // holds rows 4 g .. 4 g + 3 of token r.
+    static __device__ __forceinline__ float fold(float v)
+    {
+        if constexpr (R == 4) v += __shfl_xor(v, 20);
+        return v + __shfl_xor(v, 40);
+    }
+};
 
-template <int DT, int PER>
+// ---------------------------------------------------------------- gate and up projections
+// Every wave works on its own: an item is R columns of h of one expert, and
+// the wave streams their R gate and R up rows over all of K, UB blocks of
+// loads at a time, for up to MT * R tokens (a longer list takes another pass
+// over the weights).  Items are dealt out with consecutive ones on different
+// workgroups, so that few items still use every CU.
+template <int DT, int PER, int R, int MT, int UB>
 __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits,
     const uint8_t* __restrict__ w13, const float* __restrict__ s13, int* __restrict__ ids_out,
-    float* __restrict__ weights_out, Routing* __restrict__ routing, uint16_t* __restrict__ h,
+    float* __restrict__ weights_out, uint64_t* __restrict__ masks_out, uint16_t* __restrict__ h,
     int T, int H, int I, int E, int top_k, int renormalize)
 {
-    __shared__ Routing rt;
+    typedef Layout<R> L;
+    constexpr int KL = L::kBlocks * kBlock;                // K per load
+    __shared__ uint64_t masks[PER * 64];
     __shared__ int ids[kMaxPairs];
-    __shared__ int tmp[kMoeWaves];
-    __shared__ float red[kMoeWaves][8][64];  // (m-tile, gate / up, row tile) x (token, row)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, g = lane >> 4, half = r >> 3;
-    const int koff = (half * 4 + g) * 16;
+    const int r = lane & 15, g = lane >> 4;
+    const L at(lane);
 
+    if (tid < PER * 64) masks[tid] = 0;
+    __syncthreads();
     for (int t = wave; t < T; t += kMoeWaves) {
         int id;
         float weight;
         route_token<PER>(logits + (size_t)t * E, E, top_k, renormalize, lane, id, weight);
         if (lane < top_k) {
             ids[t * top_k + lane] = id;
+            // a bit of its own per token: the order of the updates does not matter
+            if (id >= 0) atomicOr(reinterpret_cast<uint32_t*>(&masks[id]) + (t >> 5), 1u << (t & 31));
             if (blockIdx.x == 0) {
                 ids_out[t * top_k + lane] = id;
                 weights_out[t * top_k + lane] = weight;
@@ -219,99 +273,93 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
         }
     }
     __syncthreads();
-    group_pairs(ids, T * top_k, E, rt, tmp);
-    if (blockIdx.x == 0) {
-        for (int i = tid; i < (int)(sizeof(Routing) / 4); i += kMoeThreads)
-            reinterpret_cast<int*>(routing)[i] = reinterpret_cast<const int*>(&rt)[i];
-    }
+    if (blockIdx.x == 0 && tid < E) masks_out[tid] = masks[tid];
+    Active<PER> active;
+    active.find(masks, E, lane);
 
-    const int nblk = (H + kBlock - 1) / kBlock;
-    const int tiles = I / kUpCols;
-    const int items = rt.count * tiles;
+    const int nblk = (H + kBlock - 1) / kBlock, nb = (I + kBlock - 1) / kBlock;
+    const int tiles = I / R;
+    const int items = active.count * tiles;
     const rsrc_t rx = make_rsrc(x, (uint32_t)(T * H * 2));
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it = wave * gridDim.x + blockIdx.x; it < items; it += kMoeWaves * gridDim.x) {
         const int slot = it / tiles;
-        const int i0 = (it - slot * tiles) * kUpCols;
-        const int e = rt.expert[slot], first = rt.start[slot], last = rt.start[slot + 1];
+        const int i0 = (it - slot * tiles) * R;
+        const int e = active.expert(slot, lane);
+        Tokens tokens;
+        tokens.find(masks, e, lane);
         const size_t row = (size_t)e * 2 * I + i0;                   // gate row; up: + I
-        const rsrc_t rg = make_rsrc(w13 + row * H, (uint32_t)(kUpCols * H));
-        const rsrc_t ru = make_rsrc(w13 + (row + I) * H, (uint32_t)(kUpCols * H));
-        const int nb = (I + kBlock - 1) / kBlock;
+        const rsrc_t rw[2] = {make_rsrc(w13 + row * H, (uint32_t)(R * H)),
+                              make_rsrc(w13 + (row + I) * H, (uint32_t)(R * H))};
         const float* const sg = s13 + ((size_t)e * 2 * nb + (i0 >> 7)) * nblk;
-        const float* const su = sg + (size_t)nb * nblk;
-        for (int p0 = first; p0 < last; p0 += kUpTokens) {
-            uint32_t xo[2];                                          // of this lane's token
+        const rsrc_t rs[2] = {make_rsrc(sg, (uint32_t)(nblk * 4)),
+                              make_rsrc(sg + (size_t)nb * nblk, (uint32_t)(nblk * 4))};
+        for (int p0 = 0; p0 < tokens.count; p0 += MT * R) {
+            uint32_t xo[MT];                                         // of this lane's token
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const int p = p0 + m * 8 + (r & 7);
-                xo[m] = p < last ? (uint32_t)(rt.pairs[p] / top_k * H + koff) * 2 : kOOB;
+            for (int m = 0; m < MT; ++m) {
+                const int t = tokens.at(p0 + m * R + at.row);
+                xo[m] = t >= 0 ? (uint32_t)(t * H + at.koff) * 2 : kOOB;
             }
-            const bool two = last - p0 > 8;
-            v4f acc[2][2][2];
+            v4f acc[MT][2];
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < 2; ++c) acc[m][c] = v4f{0.f, 0.f, 0.f, 0.f};
+            for (int k0 = 0; k0 < H; k0 += UB * KL) {
+                v4i w[UB][2], xv[UB][MT][2];
+                float s[UB][2];
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) acc[m][c][t] = v4f{0.f, 0.f, 0.f, 0.f};
-            for (int kb = wave; kb < nblk; kb += kMoeWaves) {
-                const bool in = kb * kBlock + koff < H;
-                const uint32_t off = in ? (uint32_t)((r & 7) * H + kb * kBlock + koff) : kOOB;
-                v4i w[2][2], xv[2][2];
+                for (int u = 0; u < UB; ++u) {
+                    const int k = k0 + u * KL;
+                    const uint32_t past = k + at.koff < H ? 0u : kOOB;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    w[0][t] = buf_load16<CP_NT>(rg, off + t * 8 * H);
-                    w[1][t] = buf_load16<CP_NT>(ru, off + t * 8 * H);
+                    for (int c = 0; c < 2; ++c) {
+                        w[u][c] = buf_load16<CP_NT>(rw[c], (uint32_t)(at.row * H + k + at.koff) + past);
+                        // zero past the last block
+                        s[u][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                            rs[c], (uint32_t)((k >> 7) + at.block) * 4, 0, 0));
+                    }
                 }
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const uint32_t o = in && xo[m] != kOOB ? xo[m] + kb * kBlock * 2 : kOOB;
-                    xv[m][0] = buf_load16(rx, o);
-                    xv[m][1] = buf_load16(rx, o + 16);
-                }
-                const float s[2] = {sg[kb], su[kb]};
+                for (int u = 0; u < UB; ++u) {
+                    const int k = k0 + u * KL;
+                    const uint32_t past = k + at.koff < H ? 0u : kOOB;
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    if (m == 1 && !two) break;
+                    for (int m = 0; m < MT; ++m) {
+                        // kOOB + kOOB would wrap around
+                        const uint32_t o = past != 0 || xo[m] == kOOB ? kOOB : xo[m] + (uint32_t)k * 2;
+                        xv[u][m][0] = buf_load16(rx, o);
+                        xv[u][m][1] = buf_load16(rx, o + 16);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int u = 0; u < UB; ++u)
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
 #pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            const v4f p = block_product<DT>(w[c][t], xv[m][0], xv[m][1]);
+                        for (int m = 0; m < MT; ++m) {
+                            const v4f p = block_product<DT>(w[u][c], xv[u][m][0], xv[u][m][1]);
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
-                                acc[m][c][t][q] = __builtin_fmaf(p[q], s[c], acc[m][c][t][q]);
+                                acc[m][c][q] = __builtin_fmaf(p[q], s[u][c], acc[m][c][q]);
                         }
-                }
             }
-            __syncthreads();                                         // red is free
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+            for (int m = 0; m < MT; ++m) {
+                float hv[4];
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int t = 0; t < 2; ++t)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            // the other half of the block sits 8 columns and 32 lanes away
-                            const float v = acc[m][c][t][q] + __shfl_xor(acc[m][c][t][q], 40);
-                            if (r < 8 && g < 2) red[wave][m * 4 + c * 2 + t][r * 8 + 4 * g + q] = v;
-                        }
-            __syncthreads();
-            if (tid < kUpTokens * kUpCols) {
-                const int col = tid & 15, tok = tid >> 4;
-                const int p = p0 + tok;
-                if (p < last) {
-                    float gv = 0.0f, uv = 0.0f;
-                    const int k = (tok & 7) * 8 + (col & 7), b = (tok >> 3) * 4 + (col >> 3);
-#pragma unroll
-                    for (int w = 0; w < kMoeWaves; ++w) {
-                        gv += red[w][b][k];
-                        uv += red[w][b + 2][k];
-                    }
+                for (int q = 0; q < 4; ++q) {
+                    const float gv = L::fold(acc[m][0][q]), uv = L::fold(acc[m][1][q]);
+                    hv[q] = gv / (1.0f + expf(-gv)) * uv;
+                }
+                const int t = tokens.at(p0 + m * R + at.row);
+                if (r < R && 4 * g < R && t >= 0) {
                     // bf16 has fp32's range (fp16 would overflow); its rounding, 2^-8, is that of y
-                    h[(size_t)rt.pairs[p] * I + i0 + col] =
-                        (uint16_t)f32_to_bf16_bits(gv / (1.0f + expf(-gv)) * uv);
+                    const uint32_t lo = f32_to_bf16_bits(hv[0]) | f32_to_bf16_bits(hv[1]) << 16;
+                    const uint32_t hi = f32_to_bf16_bits(hv[2]) | f32_to_bf16_bits(hv[3]) << 16;
+                    *reinterpret_cast<v2i*>(h + (size_t)pair_of(ids, t, e, top_k) * I + i0 + 4 * g) =
+                        v2i{(int)lo, (int)hi};
                 }
             }
         }
@@ -319,67 +367,97 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
 }
 
 // ---------------------------------------------------------------- down projection
+// A workgroup owns eight columns of y.  Its waves take items of kDownBlocks K
+// blocks of one expert; the next item's weights are requested before the
+// current one's products.  Each wave adds its products, weighted, to sums of
+// its own in LDS; the waves' sums are added in a fixed order at the end.
 constexpr int kDownRows = 8;                // columns of y (rows of W2) per workgroup
 constexpr int kDownBlocks = 4;              // K blocks per item
 
+template <int PER>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const uint16_t* __restrict__ h, const uint8_t* __restrict__ w2, const float* __restrict__ s2,
-    const Routing* __restrict__ routing, const float* __restrict__ weights,
-    uint16_t* __restrict__ y, int T, int H, int I, int top_k)
+    const uint64_t* __restrict__ masks_in, const int* __restrict__ ids_in,
+    const float* __restrict__ weights, uint16_t* __restrict__ y, int T, int H, int I, int E,
+    int top_k)
 {
-    __shared__ Routing rt;
+    typedef Layout<kDownRows> L;
+    __shared__ uint64_t masks[PER * 64];
+    __shared__ int ids[kMaxPairs];
     __shared__ float wt[kMaxPairs];
     extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][rows]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, g = lane >> 4, half = r >> 3;
-    const int koff = (half * 4 + g) * 16;
+    const int r = lane & 15, g = lane >> 4;
+    const L at(lane);
     const int n0 = blockIdx.x * kDownRows;
 
-    for (int i = tid; i < (int)(sizeof(Routing) / 4); i += kMoeThreads)
-        reinterpret_cast<int*>(&rt)[i] = reinterpret_cast<const int*>(routing)[i];
-    for (int i = tid; i < T * top_k; i += kMoeThreads) wt[i] = weights[i];
+    if (tid < E) masks[tid] = masks_in[tid];
+    for (int i = tid; i < T * top_k; i += kMoeThreads) {
+        ids[i] = ids_in[i];
+        wt[i] = weights[i];
+    }
     for (int i = tid; i < kMoeWaves * T * kDownRows; i += kMoeThreads) ysum[i] = 0.0f;
     __syncthreads();
+    Active<PER> active;
+    active.find(masks, E, lane);
 
     const int nblk = (I + kBlock - 1) / kBlock;
     const int chunks = (nblk + kDownBlocks - 1) / kDownBlocks;
-    const int items = rt.count * chunks;
+    const int items = active.count * chunks;
     const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * I * 2));
     float* const mine = ysum + wave * T * kDownRows;
-    for (int it = wave; it < items; it += kMoeWaves) {
+
+    v4i w[kDownBlocks];
+    float s[kDownBlocks];
+    int e = 0, kb0 = 0;
+    auto request = [&](int it) {
         const int slot = it / chunks;
-        const int kb0 = (it - slot * chunks) * kDownBlocks;
-        const int e = rt.expert[slot], first = rt.start[slot], last = rt.start[slot + 1];
+        kb0 = (it - slot * chunks) * kDownBlocks;
+        e = active.expert(slot, lane);
         const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(kDownRows * I));
         const float* const sb = s2 + ((size_t)e * ((H + kBlock - 1) / kBlock) + (n0 >> 7)) * nblk;
-        v4i w[kDownBlocks];
-        float s[kDownBlocks];
 #pragma unroll
         for (int c = 0; c < kDownBlocks; ++c) {
             const int kb = kb0 + c;
-            w[c] = buf_load16<CP_NT>(rw, kb * kBlock + koff < I
-                                             ? (uint32_t)((r & 7) * I + kb * kBlock + koff) : kOOB);
+            w[c] = buf_load16<CP_NT>(rw, (uint32_t)(at.row * I + kb * kBlock + at.koff) +
+                                             (kb * kBlock + at.koff < I ? 0u : kOOB));
             s[c] = kb < nblk ? sb[kb] : 0.0f;
         }
-        for (int p0 = first; p0 < last; p0 += 8) {
-            const int p = p0 + (r & 7);
-            const int pair = p < last ? rt.pairs[p] : -1;
+    };
+    int it = wave;
+    if (it < items) request(it);
+    while (it < items) {
+        v4i wc[kDownBlocks];
+        float sc[kDownBlocks];
+#pragma unroll
+        for (int c = 0; c < kDownBlocks; ++c) {
+            wc[c] = w[c];
+            sc[c] = s[c];
+        }
+        const int ec = e, kbc = kb0;
+        Tokens tokens;
+        tokens.find(masks, ec, lane);
+        it += kMoeWaves;
+        if (it < items) request(it);
+        for (int p0 = 0; p0 < tokens.count; p0 += kDownRows) {
+            const int t = tokens.at(p0 + at.row);
+            const int pair = t >= 0 ? pair_of(ids, t, ec, top_k) : 0;
             v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kDownBlocks; ++c) {
-                const int k = (kb0 + c) * kBlock + koff;
-                const uint32_t o = pair >= 0 && k < I ? (uint32_t)(pair * I + k) * 2 : kOOB;
-                const v4f q = block_product<DT_BF16>(w[c], buf_load16(rh, o), buf_load16(rh, o + 16));
+                const int k = (kbc + c) * kBlock + at.koff;
+                const uint32_t o = t >= 0 && k < I ? (uint32_t)(pair * I + k) * 2 : kOOB;
+                const v4f q = block_product<DT_BF16>(wc[c], buf_load16(rh, o), buf_load16(rh, o + 16));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], s[c], acc[i]);
+                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], sc[c], acc[i]);
             }
             v4f v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = acc[i] + __shfl_xor(acc[i], 40);
+            for (int i = 0; i < 4; ++i) v[i] = L::fold(acc[i]);
             // a token occurs once among an expert's pairs, so no two lanes meet
-            if (r < 8 && g < 2 && pair >= 0) {
-                v4f* const dst = reinterpret_cast<v4f*>(mine + pair / top_k * kDownRows + 4 * g);
+            if (r < kDownRows && 4 * g < kDownRows && t >= 0) {
+                v4f* const dst = reinterpret_cast<v4f*>(mine + t * kDownRows + 4 * g);
                 const float f = wt[pair];
                 v4f d = *dst;
 #pragma unroll
@@ -392,45 +470,59 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     for (int o = tid; o < T * kDownRows; o += kMoeThreads) {
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kMoeWaves; ++w) v += ysum[w * T * kDownRows + o];
+        for (int i = 0; i < kMoeWaves; ++i) v += ysum[i * T * kDownRows + o];
         y[(size_t)(o / kDownRows) * H + n0 + o % kDownRows] = (uint16_t)f32_to_bf16_bits(v);
     }
 }
 
-template <int DT, int PER>
+template <int DT, int PER, int R, int MT, int UB>
 hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
 {
     const int64_t slots = std::min<int64_t>(a.E, (int64_t)a.T * a.top_k);
-    const int64_t items = slots * (a.I / kUpCols);
+    const int64_t items = slots * (a.I / R);
     const int grid = (int)std::min<int64_t>(items, 2 * kCUs);
-    moe_up_kernel<DT, PER><<<grid, kMoeThreads, 0, stream>>>(
+    moe_up_kernel<DT, PER, R, MT, UB><<<grid, kMoeThreads, 0, stream>>>(
         static_cast<const uint16_t*>(a.x), a.logits, a.w13, a.s13, a.ids, a.weights,
-        static_cast<Routing*>(a.work),
+        static_cast<uint64_t*>(a.work),
         reinterpret_cast<uint16_t*>(static_cast<char*>(a.work) + kMoeRoutingBytes), a.T, a.H, a.I,
         a.E, a.top_k, a.renormalize);
     return hipGetLastError();
 }
 
-template <int DT>
-hipError_t launch_up_dt(const MoeArgs& a, hipStream_t stream)
+template <int PER>
+hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
-    if (a.E <= 64) return launch_up<DT, 1>(a, stream);
-    if (a.E <= 128) return launch_up<DT, 2>(a, stream);
-    if (a.E <= 256) return launch_up<DT, 4>(a, stream);
-    return launch_up<DT, 8>(a, stream);
+    const size_t lds = (size_t)kMoeWaves * a.T * kDownRows * sizeof(float);
+    moe_down_kernel<PER><<<a.H / kDownRows, kMoeThreads, lds, stream>>>(
+        reinterpret_cast<const uint16_t*>(static_cast<const char*>(a.work) + kMoeRoutingBytes), a.w2,
+        a.s2, static_cast<const uint64_t*>(a.work), a.ids, a.weights, a.y, a.T, a.H, a.I, a.E,
+        a.top_k);
+    return hipGetLastError();
+}
+
+template <int DT, int PER>
+hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
+{
+    const hipError_t e = a.T <= 4   ? launch_up<DT, PER, 4, 1, 4>(a, stream)
+                         : a.T <= 8 ? launch_up<DT, PER, 8, 1, 4>(a, stream)
+                                    : launch_up<DT, PER, 8, 2, 2>(a, stream);
+    return e == hipSuccess ? launch_down<PER>(a, stream) : e;
+}
+
+template <int DT>
+hipError_t launch_moe_dt(const MoeArgs& a, hipStream_t stream)
+{
+    if (a.E <= 64) return launch_both<DT, 1>(a, stream);
+    if (a.E <= 128) return launch_both<DT, 2>(a, stream);
+    if (a.E <= 256) return launch_both<DT, 4>(a, stream);
+    return launch_both<DT, 8>(a, stream);
 }
 
 }  // namespace
 
 hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t stream)
 {
-    hipError_t e = dtype == DT_BF16 ? launch_up_dt<DT_BF16>(a, stream) : launch_up_dt<DT_FP16>(a, stream);
-    if (e != hipSuccess) return e;
-    const size_t lds = (size_t)kMoeWaves * a.T * kDownRows * sizeof(float);
-    moe_down_kernel<<<a.H / kDownRows, kMoeThreads, lds, stream>>>(
-        reinterpret_cast<const uint16_t*>(static_cast<const char*>(a.work) + kMoeRoutingBytes), a.w2,
-        a.s2, static_cast<const Routing*>(a.work), a.weights, a.y, a.T, a.H, a.I, a.top_k);
-    return hipGetLastError();
+    return dtype == DT_BF16 ? launch_moe_dt<DT_BF16>(a, stream) : launch_moe_dt<DT_FP16>(a, stream);
 }
 
 }  // namespace fp8q
