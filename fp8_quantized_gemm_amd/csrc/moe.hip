@@ -40,7 +40,6 @@ constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
 constexpr int kMoeWaves = 16;
 constexpr int kMoeThreads = kMoeWaves * 64;
 static_assert(kMoeMaxTokens <= 64, "an expert's tokens are a 64-bit mask");
-static_assert(kMoeMaxExperts * 8 <= kMoeRoutingBytes, "masks at the head of the workspace");
 
 // 16 E4M3 codes -> 16 values of the activation's type (exact), in two operands.
 template <int DT>
@@ -142,19 +141,39 @@ __device__ __forceinline__ void route_token(const float* __restrict__ logits, in
 }
 
 // The experts that any token chose, in ascending order: 64 experts to a word.
+// first[i] is the number of pairs of the experts before expert 64 i + lane.
 template <int PER>
 struct Active {
     uint64_t word[PER];
+    int first[PER];
     int count;
     __device__ __forceinline__ void find(const uint64_t* masks, int experts, int lane)
     {
         count = 0;
+        int pairs = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = i * 64 + lane;
-            word[i] = __ballot(e < experts && masks[e] != 0);
+            const int n = e < experts ? __popcll(masks[e]) : 0;
+            word[i] = __ballot(n != 0);
             count += __popcll(word[i]);
+            int scan = n;
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const int below = __shfl_up(scan, d);
+                if (lane >= d) scan += below;
+            }
+            first[i] = pairs + scan - n;
+            pairs += __builtin_amdgcn_readlane(scan, 63);
         }
+    }
+    __device__ __forceinline__ int first_pair(int e) const
+    {
+        int p = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (e >> 6 == i) p = __builtin_amdgcn_readlane(first[i], e & 63);
+        return p;
     }
     // the slot-th of them
     __device__ __forceinline__ int expert(int slot, int lane) const
@@ -201,15 +220,6 @@ struct Tokens {
     }
 };
 
-// The place j of expert e among token t's choices, as t * top_k + j.
-__device__ __forceinline__ int pair_of(const int* ids, int t, int e, int top_k)
-{
-    int p = t * top_k;
-    for (int j = 0; j < top_k; ++j)
-        if (ids[t * top_k + j] == e) p = t * top_k + j;
-    return p;
-}
-
 // ---------------------------------------------------------------- operand layout
 // R weight rows (8 or 4) per load instruction, 1024 / R bytes of each: lane
 // (r, g) reads unit 4 (r / R) + g of row r % R.  For R = 4 an instruction
@@ -234,62 +244,125 @@ struct Layout {
     }
 };
 
+// Where column i of h stands in its row.  The down projection's lane of unit
+// u multiplies columns 16 u .. 16 u + 15 of a block with two MFMAs of eight
+// each; the first eights of all units come first, so that each of its two
+// loads reads whole 128-byte lines (with the columns in order it read 16 bytes
+// of every 32: moe_down at 64 tokens of 128 experts of 768 x 2048 58.4 us).
+// Rows are padded to whole blocks.
+__device__ __forceinline__ int h_position(int i)
+{
+    return (i & ~127) | (i & 8) << 3 | (i >> 4 & 7) << 3 | (i & 7);
+}
+__device__ __forceinline__ int h_stride(int I) { return (I + kBlock - 1) / kBlock * kBlock; }
+
+// ---------------------------------------------------------------- selection, a kernel of its own
+// One wave per token.  Used above kRouteInline tokens, where repeating the
+// selection in every workgroup of moe_up costs more than a launch.
+template <int PER>
+__global__ __launch_bounds__(64) void moe_route_kernel(const float* __restrict__ logits,
+                                                       int* __restrict__ ids,
+                                                       float* __restrict__ weights, int E,
+                                                       int top_k, int renormalize)
+{
+    const int t = blockIdx.x, lane = threadIdx.x;
+    int id;
+    float weight;
+    route_token<PER>(logits + (size_t)t * E, E, top_k, renormalize, lane, id, weight);
+    if (lane < top_k) {
+        ids[t * top_k + lane] = id;
+        weights[t * top_k + lane] = weight;
+    }
+}
+
 // ---------------------------------------------------------------- gate and up projections
-// Every wave works on its own: an item is R columns of h of one expert, and
-// the wave streams their R gate and R up rows over all of K, UB blocks of
-// loads at a time, for up to MT * R tokens (a longer list takes another pass
-// over the weights).  Items are dealt out with consecutive ones on different
-// workgroups, so that few items still use every CU.
-template <int DT, int PER, int R, int MT, int UB>
-__global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
+// Every wave works on its own: an item is RT * R columns of h of one expert,
+// and the wave streams their gate and up rows (2 RT row tiles, which share the
+// loads of x) over all of K, UB loads of each tile at a time, for up to MT * R
+// tokens (a longer list takes another pass over the weights).  Items are
+// dealt out with consecutive ones on different workgroups, so that few items
+// still use every CU.
+//
+// h and the weights it will be summed with are stored grouped by expert (the
+// p-th token of an expert at first_pair + p), so that the second kernel reads
+// an expert's rows without looking them up, and each row block by block in
+// the order of the second kernel's operands (h_position).
+//
+// With ROUTED the selection is there already (moe_route_kernel); without it
+// every workgroup makes it, and the first one stores it.
+template <int DT, int PER, int R, int RT, int MT, int UB, int WAVES, int OCC, bool ROUTED>
+__global__ __launch_bounds__(WAVES * 64) __attribute__((amdgpu_waves_per_eu(OCC)))
+void moe_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits,
-    const uint8_t* __restrict__ w13, const float* __restrict__ s13, int* __restrict__ ids_out,
-    float* __restrict__ weights_out, uint64_t* __restrict__ masks_out, uint16_t* __restrict__ h,
-    int T, int H, int I, int E, int top_k, int renormalize)
+    const uint8_t* __restrict__ w13, const float* __restrict__ s13, int* __restrict__ ids_io,
+    float* __restrict__ weights_io, uint64_t* __restrict__ masks_out,
+    float* __restrict__ pair_weights, uint16_t* __restrict__ h, int T, int H, int I, int E,
+    int top_k, int renormalize)
 {
     typedef Layout<R> L;
     constexpr int KL = L::kBlocks * kBlock;                // K per load
+    constexpr int COLS = R * RT;
     __shared__ uint64_t masks[PER * 64];
     __shared__ int ids[kMaxPairs];
+    __shared__ float wt[kMaxPairs];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r = lane & 15, g = lane >> 4;
     const L at(lane);
 
-    if (tid < PER * 64) masks[tid] = 0;
+    for (int i = tid; i < PER * 64; i += WAVES * 64) masks[i] = 0;
     __syncthreads();
-    for (int t = wave; t < T; t += kMoeWaves) {
-        int id;
-        float weight;
-        route_token<PER>(logits + (size_t)t * E, E, top_k, renormalize, lane, id, weight);
-        if (lane < top_k) {
-            ids[t * top_k + lane] = id;
-            // a bit of its own per token: the order of the updates does not matter
-            if (id >= 0) atomicOr(reinterpret_cast<uint32_t*>(&masks[id]) + (t >> 5), 1u << (t & 31));
-            if (blockIdx.x == 0) {
-                ids_out[t * top_k + lane] = id;
-                weights_out[t * top_k + lane] = weight;
+    auto choose = [&](int pair, int t, int id, float weight) {
+        ids[pair] = id;
+        wt[pair] = weight;
+        // a bit of its own per token: the order of the updates does not matter
+        if (id >= 0) atomicOr(reinterpret_cast<uint32_t*>(&masks[id]) + (t >> 5), 1u << (t & 31));
+    };
+    if constexpr (ROUTED) {
+        for (int p = tid; p < T * top_k; p += WAVES * 64) choose(p, p / top_k, ids_io[p], weights_io[p]);
+    } else {
+        for (int t = wave; t < T; t += WAVES) {
+            int id;
+            float weight;
+            route_token<PER>(logits + (size_t)t * E, E, top_k, renormalize, lane, id, weight);
+            if (lane < top_k) {
+                const int p = t * top_k + lane;
+                choose(p, t, id, weight);
+                if (blockIdx.x == 0) {
+                    ids_io[p] = id;
+                    weights_io[p] = weight;
+                }
             }
         }
     }
     __syncthreads();
-    if (blockIdx.x == 0 && tid < E) masks_out[tid] = masks[tid];
+    if (blockIdx.x == 0)
+        for (int i = tid; i < E; i += WAVES * 64) masks_out[i] = masks[i];
     Active<PER> active;
     active.find(masks, E, lane);
 
     const int nblk = (H + kBlock - 1) / kBlock, nb = (I + kBlock - 1) / kBlock;
-    const int tiles = I / R;
+    const int tiles = I / COLS;
     const int items = active.count * tiles;
     const rsrc_t rx = make_rsrc(x, (uint32_t)(T * H * 2));
-    for (int it = wave * gridDim.x + blockIdx.x; it < items; it += kMoeWaves * gridDim.x) {
+    for (int it = wave * gridDim.x + blockIdx.x; it < items; it += WAVES * gridDim.x) {
         const int slot = it / tiles;
-        const int i0 = (it - slot * tiles) * R;
+        const int i0 = (it - slot * tiles) * COLS;
         const int e = active.expert(slot, lane);
+        const int first = active.first_pair(e);
         Tokens tokens;
         tokens.find(masks, e, lane);
+        if (i0 == 0 && lane < tokens.count) {
+            // the weight of expert e among token tokens.list's choices
+            float v = 0.0f;
+            for (int j = 0; j < top_k; ++j)
+                if (ids[tokens.list * top_k + j] == e) v = wt[tokens.list * top_k + j];
+            pair_weights[first + lane] = v;
+        }
         const size_t row = (size_t)e * 2 * I + i0;                   // gate row; up: + I
-        const rsrc_t rw[2] = {make_rsrc(w13 + row * H, (uint32_t)(R * H)),
-                              make_rsrc(w13 + (row + I) * H, (uint32_t)(R * H))};
+        const rsrc_t rw[2] = {make_rsrc(w13 + row * H, (uint32_t)(COLS * H)),
+                              make_rsrc(w13 + (row + I) * H, (uint32_t)(COLS * H))};
+        // an item's columns lie in one block of 128
         const float* const sg = s13 + ((size_t)e * 2 * nb + (i0 >> 7)) * nblk;
         const rsrc_t rs[2] = {make_rsrc(sg, (uint32_t)(nblk * 4)),
                               make_rsrc(sg + (size_t)nb * nblk, (uint32_t)(nblk * 4))};
@@ -300,13 +373,15 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
                 const int t = tokens.at(p0 + m * R + at.row);
                 xo[m] = t >= 0 ? (uint32_t)(t * H + at.koff) * 2 : kOOB;
             }
-            v4f acc[MT][2];
+            v4f acc[MT][RT][2];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) acc[m][c] = v4f{0.f, 0.f, 0.f, 0.f};
+                for (int n = 0; n < RT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) acc[m][n][c] = v4f{0.f, 0.f, 0.f, 0.f};
             for (int k0 = 0; k0 < H; k0 += UB * KL) {
-                v4i w[UB][2], xv[UB][MT][2];
+                v4i w[UB][RT][2], xv[UB][MT][2];
                 float s[UB][2];
 #pragma unroll
                 for (int u = 0; u < UB; ++u) {
@@ -314,7 +389,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
                     const uint32_t past = k + at.koff < H ? 0u : kOOB;
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        w[u][c] = buf_load16<CP_NT>(rw[c], (uint32_t)(at.row * H + k + at.koff) + past);
+#pragma unroll
+                        for (int n = 0; n < RT; ++n)
+                            w[u][n][c] = buf_load16<CP_NT>(
+                                rw[c], (uint32_t)((n * R + at.row) * H + k + at.koff) + past);
                         // zero past the last block
                         s[u][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
                             rs[c], (uint32_t)((k >> 7) + at.block) * 4, 0, 0));
@@ -323,11 +401,10 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
 #pragma unroll
                 for (int u = 0; u < UB; ++u) {
                     const int k = k0 + u * KL;
-                    const uint32_t past = k + at.koff < H ? 0u : kOOB;
+                    const bool past = k + at.koff >= H;
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        // kOOB + kOOB would wrap around
-                        const uint32_t o = past != 0 || xo[m] == kOOB ? kOOB : xo[m] + (uint32_t)k * 2;
+                        const uint32_t o = past || xo[m] == kOOB ? kOOB : xo[m] + (uint32_t)k * 2;
                         xv[u][m][0] = buf_load16(rx, o);
                         xv[u][m][1] = buf_load16(rx, o + 16);
                     }
@@ -336,54 +413,57 @@ __global__ __launch_bounds__(kMoeThreads) void moe_up_kernel(
 #pragma unroll
                 for (int u = 0; u < UB; ++u)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int n = 0; n < RT; ++n)
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            const v4f p = block_product<DT>(w[u][c], xv[u][m][0], xv[u][m][1]);
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                acc[m][c][q] = __builtin_fmaf(p[q], s[u][c], acc[m][c][q]);
-                        }
+                            for (int m = 0; m < MT; ++m) {
+                                const v4f p = block_product<DT>(w[u][n][c], xv[u][m][0], xv[u][m][1]);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    acc[m][n][c][q] = __builtin_fmaf(p[q], s[u][c], acc[m][n][c][q]);
+                            }
             }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                float hv[4];
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float gv = L::fold(acc[m][0][q]), uv = L::fold(acc[m][1][q]);
-                    hv[q] = gv / (1.0f + expf(-gv)) * uv;
+                for (int n = 0; n < RT; ++n) {
+                    float hv[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float gv = L::fold(acc[m][n][0][q]), uv = L::fold(acc[m][n][1][q]);
+                        hv[q] = gv / (1.0f + expf(-gv)) * uv;
+                    }
+                    const int p = p0 + m * R + at.row;
+                    if (r < R && 4 * g < R && p < tokens.count) {
+                        // bf16 has fp32's range (fp16 would overflow); its rounding, 2^-8, is that of y
+                        const uint32_t lo = f32_to_bf16_bits(hv[0]) | f32_to_bf16_bits(hv[1]) << 16;
+                        const uint32_t hi = f32_to_bf16_bits(hv[2]) | f32_to_bf16_bits(hv[3]) << 16;
+                        *reinterpret_cast<v2i*>(h + (size_t)(first + p) * h_stride(I) +
+                                                h_position(i0 + n * R + 4 * g)) = v2i{(int)lo, (int)hi};
+                    }
                 }
-                const int t = tokens.at(p0 + m * R + at.row);
-                if (r < R && 4 * g < R && t >= 0) {
-                    // bf16 has fp32's range (fp16 would overflow); its rounding, 2^-8, is that of y
-                    const uint32_t lo = f32_to_bf16_bits(hv[0]) | f32_to_bf16_bits(hv[1]) << 16;
-                    const uint32_t hi = f32_to_bf16_bits(hv[2]) | f32_to_bf16_bits(hv[3]) << 16;
-                    *reinterpret_cast<v2i*>(h + (size_t)pair_of(ids, t, e, top_k) * I + i0 + 4 * g) =
-                        v2i{(int)lo, (int)hi};
-                }
-            }
         }
     }
 }
 
 // ---------------------------------------------------------------- down projection
 // A workgroup owns eight columns of y.  Its waves take items of kDownBlocks K
-// blocks of one expert; the next item's weights are requested before the
-// current one's products.  Each wave adds its products, weighted, to sums of
-// its own in LDS; the waves' sums are added in a fixed order at the end.
+// blocks of one expert; the next item's weights, and the rows of h of its
+// first eight tokens, are requested before the current one's products.  Each
+// wave adds its products, weighted, to sums of its own in LDS; the waves' sums
+// are added in a fixed order at the end.
 constexpr int kDownRows = 8;                // columns of y (rows of W2) per workgroup
-constexpr int kDownBlocks = 4;              // K blocks per item
+constexpr int kDownBlocks = 3;              // K blocks per item
 
 template <int PER>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const uint16_t* __restrict__ h, const uint8_t* __restrict__ w2, const float* __restrict__ s2,
-    const uint64_t* __restrict__ masks_in, const int* __restrict__ ids_in,
-    const float* __restrict__ weights, uint16_t* __restrict__ y, int T, int H, int I, int E,
-    int top_k)
+    const uint64_t* __restrict__ masks_in, const float* __restrict__ pair_weights,
+    uint16_t* __restrict__ y, int T, int H, int I, int E, int top_k)
 {
     typedef Layout<kDownRows> L;
     __shared__ uint64_t masks[PER * 64];
-    __shared__ int ids[kMaxPairs];
     __shared__ float wt[kMaxPairs];
     extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][rows]
     const int tid = threadIdx.x, lane = tid & 63;
@@ -393,10 +473,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const int n0 = blockIdx.x * kDownRows;
 
     if (tid < E) masks[tid] = masks_in[tid];
-    for (int i = tid; i < T * top_k; i += kMoeThreads) {
-        ids[i] = ids_in[i];
-        wt[i] = weights[i];
-    }
+    for (int i = tid; i < T * top_k; i += kMoeThreads) wt[i] = pair_weights[i];
     for (int i = tid; i < kMoeWaves * T * kDownRows; i += kMoeThreads) ysum[i] = 0.0f;
     __syncthreads();
     Active<PER> active;
@@ -405,65 +482,83 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const int nblk = (I + kBlock - 1) / kBlock;
     const int chunks = (nblk + kDownBlocks - 1) / kDownBlocks;
     const int items = active.count * chunks;
-    const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * I * 2));
+    const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * h_stride(I) * 2));
     float* const mine = ysum + wave * T * kDownRows;
 
-    v4i w[kDownBlocks];
-    float s[kDownBlocks];
-    int e = 0, kb0 = 0;
-    auto request = [&](int it) {
-        const int slot = it / chunks;
-        kb0 = (it - slot * chunks) * kDownBlocks;
-        e = active.expert(slot, lane);
+    // rows of h of pair p (none: zeros) in the K blocks from kb0
+    auto load_h = [&](v4i (&hv)[kDownBlocks][2], int p, bool none, int kb0) {
+#pragma unroll
+        for (int c = 0; c < kDownBlocks; ++c) {
+            const int kb = (kb0 + c) * kBlock;
+            const uint32_t o = none || kb + at.koff >= I
+                                   ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2;
+            hv[c][0] = buf_load16(rh, o);
+            hv[c][1] = buf_load16(rh, o + 128);
+        }
+    };
+    struct Stage {
+        v4i w[kDownBlocks], h[kDownBlocks][2];
+        float s[kDownBlocks];
+        int kb0, first;
+        Tokens tokens;
+    };
+    // past the last item the loads are still issued, out of range, so that
+    // the number of loads in flight, and with it the wait, is always the same
+    auto request = [&](Stage& st, int it) {
+        const uint32_t none = it < items ? 0u : kOOB;
+        const int slot = min(it, items - 1) / chunks;
+        st.kb0 = (it - slot * chunks) * kDownBlocks;
+        const int e = active.expert(slot, lane);
         const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(kDownRows * I));
         const float* const sb = s2 + ((size_t)e * ((H + kBlock - 1) / kBlock) + (n0 >> 7)) * nblk;
 #pragma unroll
         for (int c = 0; c < kDownBlocks; ++c) {
-            const int kb = kb0 + c;
-            w[c] = buf_load16<CP_NT>(rw, (uint32_t)(at.row * I + kb * kBlock + at.koff) +
-                                             (kb * kBlock + at.koff < I ? 0u : kOOB));
-            s[c] = kb < nblk ? sb[kb] : 0.0f;
+            const int kb = st.kb0 + c;
+            st.w[c] = buf_load16<CP_NT>(rw, kb * kBlock + at.koff < I
+                                                ? (uint32_t)(at.row * I + kb * kBlock + at.koff) | none : kOOB);
+            st.s[c] = sb[min(kb, nblk - 1)];
         }
+        st.first = active.first_pair(e);
+        st.tokens.find(masks, e, lane);
+        load_h(st.h, st.first + at.row, none != 0 || at.row >= st.tokens.count, st.kb0);
+        __builtin_amdgcn_sched_barrier(0);
     };
-    int it = wave;
-    if (it < items) request(it);
-    while (it < items) {
-        v4i wc[kDownBlocks];
-        float sc[kDownBlocks];
-#pragma unroll
-        for (int c = 0; c < kDownBlocks; ++c) {
-            wc[c] = w[c];
-            sc[c] = s[c];
-        }
-        const int ec = e, kbc = kb0;
-        Tokens tokens;
-        tokens.find(masks, ec, lane);
-        it += kMoeWaves;
-        if (it < items) request(it);
-        for (int p0 = 0; p0 < tokens.count; p0 += kDownRows) {
-            const int t = tokens.at(p0 + at.row);
-            const int pair = t >= 0 ? pair_of(ids, t, ec, top_k) : 0;
+    auto compute = [&](Stage& st) {
+        for (int p0 = 0; p0 < st.tokens.count; p0 += kDownRows) {
+            const int p = p0 + at.row;
+            if (p0 > 0) load_h(st.h, st.first + p, p >= st.tokens.count, st.kb0);
             v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kDownBlocks; ++c) {
-                const int k = (kbc + c) * kBlock + at.koff;
-                const uint32_t o = t >= 0 && k < I ? (uint32_t)(pair * I + k) * 2 : kOOB;
-                const v4f q = block_product<DT_BF16>(wc[c], buf_load16(rh, o), buf_load16(rh, o + 16));
+                const v4f q = block_product<DT_BF16>(st.w[c], st.h[c][0], st.h[c][1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], sc[c], acc[i]);
+                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c], acc[i]);
             }
             v4f v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = L::fold(acc[i]);
+            const int t = st.tokens.at(p);
             // a token occurs once among an expert's pairs, so no two lanes meet
             if (r < kDownRows && 4 * g < kDownRows && t >= 0) {
                 v4f* const dst = reinterpret_cast<v4f*>(mine + t * kDownRows + 4 * g);
-                const float f = wt[pair];
+                const float f = wt[st.first + p];
                 v4f d = *dst;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d[i] = __builtin_fmaf(v[i], f, d[i]);
                 *dst = d;
             }
+        }
+    };
+    Stage a, b;
+    if (wave < items) {
+        request(a, wave);
+        for (int it = wave;;) {
+            request(b, it += kMoeWaves);
+            compute(a);
+            if (it >= items) break;
+            request(a, it += kMoeWaves);
+            compute(b);
+            if (it >= items) break;
         }
     }
     __syncthreads();
@@ -475,17 +570,29 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     }
 }
 
-template <int DT, int PER, int R, int MT, int UB>
+// The workspace: the experts' token masks, the grouped weights, h.
+struct MoeWork {
+    uint64_t* masks;
+    float* weights;
+    uint16_t* h;
+    explicit MoeWork(void* p)
+        : masks(static_cast<uint64_t*>(p)),
+          weights(reinterpret_cast<float*>(static_cast<char*>(p) + kMoeMaxExperts * 8)),
+          h(reinterpret_cast<uint16_t*>(static_cast<char*>(p) + kMoeRoutingBytes))
+    {
+    }
+};
+static_assert(kMoeMaxExperts * 8 + kMaxPairs * 4 <= kMoeRoutingBytes, "head of the workspace");
+
+template <int DT, int PER, int R, int RT, int MT, int UB, int WAVES, int OCC, bool ROUTED>
 hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
 {
-    const int64_t slots = std::min<int64_t>(a.E, (int64_t)a.T * a.top_k);
-    const int64_t items = slots * (a.I / R);
-    const int grid = (int)std::min<int64_t>(items, 2 * kCUs);
-    moe_up_kernel<DT, PER, R, MT, UB><<<grid, kMoeThreads, 0, stream>>>(
-        static_cast<const uint16_t*>(a.x), a.logits, a.w13, a.s13, a.ids, a.weights,
-        static_cast<uint64_t*>(a.work),
-        reinterpret_cast<uint16_t*>(static_cast<char*>(a.work) + kMoeRoutingBytes), a.T, a.H, a.I,
-        a.E, a.top_k, a.renormalize);
+    const MoeWork work(a.work);
+    const int64_t items = std::min<int64_t>(a.E, (int64_t)a.T * a.top_k) * (a.I / (R * RT));
+    const int grid = (int)std::min<int64_t>(items, kCUs * OCC * 4 / WAVES);
+    moe_up_kernel<DT, PER, R, RT, MT, UB, WAVES, OCC, ROUTED><<<grid, WAVES * 64, 0, stream>>>(
+        static_cast<const uint16_t*>(a.x), a.logits, a.w13, a.s13, a.ids, a.weights, work.masks,
+        work.weights, work.h, a.T, a.H, a.I, a.E, a.top_k, a.renormalize);
     return hipGetLastError();
 }
 
@@ -493,19 +600,31 @@ template <int PER>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
     const size_t lds = (size_t)kMoeWaves * a.T * kDownRows * sizeof(float);
+    const MoeWork work(a.work);
     moe_down_kernel<PER><<<a.H / kDownRows, kMoeThreads, lds, stream>>>(
-        reinterpret_cast<const uint16_t*>(static_cast<const char*>(a.work) + kMoeRoutingBytes), a.w2,
-        a.s2, static_cast<const uint64_t*>(a.work), a.ids, a.weights, a.y, a.T, a.H, a.I, a.E,
-        a.top_k);
+        work.h, a.w2, a.s2, work.masks, work.weights, a.y, a.T, a.H, a.I, a.E, a.top_k);
     return hipGetLastError();
 }
+
+// Above this many tokens the selection is a kernel of its own.
+constexpr int kRouteInline = 16;
 
 template <int DT, int PER>
 hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
 {
-    const hipError_t e = a.T <= 4   ? launch_up<DT, PER, 4, 1, 4>(a, stream)
-                         : a.T <= 8 ? launch_up<DT, PER, 8, 1, 4>(a, stream)
-                                    : launch_up<DT, PER, 8, 2, 2>(a, stream);
+    hipError_t e;
+    if (a.T <= 4) {
+        e = launch_up<DT, PER, 4, 1, 1, 4, 16, 4, false>(a, stream);
+    } else if (a.T <= kRouteInline) {
+        e = launch_up<DT, PER, 8, 2, 1, 2, 16, 4, false>(a, stream);
+    } else {
+        moe_route_kernel<PER><<<a.T, 64, 0, stream>>>(a.logits, a.ids, a.weights, a.E, a.top_k,
+                                                     a.renormalize);
+        if (a.T * a.top_k <= 6 * a.E)
+            e = launch_up<DT, PER, 8, 2, 1, 2, 16, 4, true>(a, stream);
+        else
+            e = launch_up<DT, PER, 8, 2, 2, 1, 16, 4, true>(a, stream);
+    }
     return e == hipSuccess ? launch_down<PER>(a, stream) : e;
 }
 
