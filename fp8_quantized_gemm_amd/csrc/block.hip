@@ -111,16 +111,16 @@ __global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
 // ---------------------------------------------------------------- decode product (M <= 16)
 // The weight matrix is read once and bounds the time, so the loads are shaped
 // for it: a wave's load instruction reads the 128-byte lines of eight weight
-// rows, lane (r, g) = (l % 16, l / 16) the 16-byte unit 4 (r / 8) + g of row
-// r % 8.  That is also the operand layout of the product, without any
-// exchange between lanes: as the first operand of v_mfma_f32_16x16x32 the
-// eight lanes r and r + 8 of a row carry its two 64-byte halves as two
-// separate operand rows, and the activations are loaded in the same way for
-// eight tokens as the second operand.  Of the 16 x 16 results the two
-// diagonal 8 x 8 quadrants pair equal halves, and their sum is the block's
-// product; the other two are dropped.  The matrix cores have that half to
-// spare at these sizes.  A lane's four results are weight rows (4 g .. 4 g +
-// 3) % 8 for the one token r % 8, so it needs one activation scale.
+// rows, lane (r, g) = (l % 16, l / 16) the 16-byte unit 2 g + r % 2 of row r / 2,
+// so that neighbouring lanes read neighbouring bytes.  That is also the
+// operand layout of the product, without any exchange between lanes: as the
+// first operand of v_mfma_f32_16x16x32 the two lanes r of a row carry its
+// even and its odd units as two operand rows, and the activations are loaded
+// in the same way for eight tokens as the second operand.  Of the 16 x 16
+// results those that pair equal parities add up to the block's product; the
+// others are dropped.  The matrix cores have that half to spare at these
+// sizes.  A lane's results 4 g + i are weight rows 2 g + i / 2 for the one
+// token r / 2, so it needs one activation scale.
 //
 // A workgroup owns 8 * RT weight rows (RT row tiles that share the activation
 // loads); its waves interleave over the K blocks.  Tokens come in MT groups
@@ -145,16 +145,16 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
     __shared__ float red[kGbWaves][2][MT * RT][8][9];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, g = lane >> 4, half = r >> 3;
+    const int r = lane & 15, g = lane >> 4, odd = r & 1;
     const int n0 = blockIdx.x * 8 * RT;
-    const int koff = (half * 4 + g) * 16;
+    const int koff = (2 * g + odd) * 16;
     const int nblk = (K + kBlock - 1) / kBlock;
 
     const rsrc_t rw = make_rsrc(qw + (size_t)n0 * K, (uint32_t)(min(8 * RT, N - n0) * K));
     const rsrc_t ra = make_rsrc(qa, (uint32_t)(M * K));
     const rsrc_t rs = make_rsrc(sa, (uint32_t)(M * nblk * 4));
     const float* const swb = sw + (size_t)(n0 >> 7) * nblk;
-    const uint32_t off = (uint32_t)((r & 7) * K + koff);       // of row or token r % 8
+    const uint32_t off = (uint32_t)((r >> 1) * K + koff);      // of row or token r / 2
 
     v4f acc[MT][RT];
 #pragma unroll
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
                 a[u][m] = buf_load16(ra, in ? off + m * 8 * K + kb * kBlock : kOOB);
                 // tokens past M read another token's scale or zero: their results are dropped
                 s[u][m] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-                    rs, kb < nblk ? (uint32_t)((kb * M + m * 8 + (r & 7)) * 4) : kOOB, 0, 0));
+                    rs, kb < nblk ? (uint32_t)((kb * M + m * 8 + (r >> 1)) * 4) : kOOB, 0, 0));
             }
             sb[u] = kb < nblk ? swb[kb] : 0.0f;
         }
@@ -196,15 +196,14 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
             }
     }
 
-    if ((g >> 1) == half) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int t = 0; t < RT; ++t)
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    red[wave][half][m * RT + t][r & 7][(4 * g + e) & 7] = acc[m][t][e];
-    }
+            for (int e = 0; e < 2; ++e)
+                red[wave][odd][m * RT + t][r >> 1][2 * g + e] =
+                    odd ? acc[m][t][2 * e + 1] : acc[m][t][2 * e];
     __syncthreads();
     for (int o = threadIdx.x; o < MT * RT * 64; o += kGbWaves * 64) {
         const int row = o & 7, t = (o >> 3) % RT, mm = (o >> 3) / RT;     // token mm, row 8 t + row

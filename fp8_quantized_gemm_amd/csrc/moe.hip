@@ -17,11 +17,8 @@
 // (moe_down) gives each workgroup eight columns of y and all chosen experts,
 // so the weighted sum over experts needs no atomics and no third kernel.
 //
-// Both use the loads and the operand layout of gemv_block_kernel: a wave
-// reads the 128-byte lines of eight weight rows, each row's two 64-byte
-// halves become two operand rows of the MFMA, the tokens (up to eight) are
-// laid out the same way, and the two diagonal 8 x 8 quadrants of the result
-// add up to the block's product.
+// Both stream weight rows through the MFMA operand layout of Layout, a wave
+// at a time, without any exchange between lanes or waves.
 #include <math.h>
 
 #include <algorithm>
@@ -221,26 +218,52 @@ struct Tokens {
 };
 
 // ---------------------------------------------------------------- operand layout
-// R weight rows (8 or 4) per load instruction, 1024 / R bytes of each: lane
-// (r, g) reads unit 4 (r / R) + g of row r % R.  For R = 4 an instruction
-// covers two K blocks, the block of a lane being r / 8.
+// R weight rows (8 or 4) per load instruction, 1024 / R bytes of each.  The
+// Q = 16 / R lanes r of a row take Q pieces of its K range as operand rows of
+// their own, r = Q row + q, so that neighbouring lanes read neighbouring 16
+// bytes: lane (r, g) reads unit 2 g + q % 2 of K block q / 2.  (With the lanes
+// of a row eight apart every lane is in another line than the lanes beside
+// it, and a load instruction occupies the CU's cache for twice as long.)  The
+// tokens are laid out the same way, and of the 16 x 16 results those that
+// pair equal q add up to the product.
 template <int R>
 struct Layout {
+    static constexpr int Q = 16 / R;
     static constexpr int kBlocks = 8 / R;                  // K blocks per load
-    int row, koff, block;                                  // within the load's K range
+    static constexpr int kOut = R / 4;                     // results per lane after fold
+    int row, koff, block;                                  // koff, block: within the load's K range
+    int out_row;                                           // first of the lane's results
+    bool owner;                                            // one lane of Q holds them
     __device__ __forceinline__ explicit Layout(int lane)
     {
-        const int r = lane & 15, g = lane >> 4;
-        row = r % R;
-        koff = (r / R * 4 + g) * 16;
-        block = r / R * 64 / kBlock;                       // of the lane's results
+        const int r = lane & 15, g = lane >> 4, q = r % Q;
+        row = r / Q;
+        block = q / 2;
+        koff = block * kBlock + (2 * g + q % 2) * 16;
+        out_row = kOut * g;
+        owner = q == 0;
     }
-    // Adds up the diagonal quadrants: lane (r, g), r < R and 4 g < R, then
-    // holds rows 4 g .. 4 g + 3 of token r.
-    static __device__ __forceinline__ float fold(float v)
+    // Result 4 g + i of lane (r, g) is row (4 g + i) / Q with piece i % Q, for
+    // token r / Q with piece r % Q: picks and adds up the equal ones.
+    __device__ __forceinline__ void fold(const v4f& d, int lane, float (&out)[kOut]) const
     {
-        if constexpr (R == 4) v += __shfl_xor(v, 20);
-        return v + __shfl_xor(v, 40);
+        if constexpr (R == 8) {
+            out[0] = (lane & 1) != 0 ? d[1] : d[0];
+            out[1] = (lane & 1) != 0 ? d[3] : d[2];
+        } else {
+            const float lo = (lane & 1) != 0 ? d[1] : d[0], hi = (lane & 1) != 0 ? d[3] : d[2];
+            out[0] = (lane & 2) != 0 ? hi : lo;
+        }
+#pragma unroll
+        for (int i = 0; i < kOut; ++i) {
+            out[i] += dpp<0xB1>(out[i]);                   // quad_perm [1,0,3,2]
+            if constexpr (R == 4) out[i] += dpp<0x4E>(out[i]);   // quad_perm [2,3,0,1]
+        }
+    }
+    template <int CTRL>
+    static __device__ __forceinline__ float dpp(float v)
+    {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
     }
 };
 
@@ -307,7 +330,6 @@ void moe_up_kernel(
     __shared__ float wt[kMaxPairs];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, g = lane >> 4;
     const L at(lane);
 
     for (int i = tid; i < PER * 64; i += WAVES * 64) masks[i] = 0;
@@ -428,19 +450,22 @@ void moe_up_kernel(
             for (int m = 0; m < MT; ++m)
 #pragma unroll
                 for (int n = 0; n < RT; ++n) {
-                    float hv[4];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float gv = L::fold(acc[m][n][0][q]), uv = L::fold(acc[m][n][1][q]);
-                        hv[q] = gv / (1.0f + expf(-gv)) * uv;
-                    }
+                    float gv[L::kOut], uv[L::kOut];
+                    at.fold(acc[m][n][0], lane, gv);
+                    at.fold(acc[m][n][1], lane, uv);
                     const int p = p0 + m * R + at.row;
-                    if (r < R && 4 * g < R && p < tokens.count) {
+                    if (at.owner && p < tokens.count) {
+                        uint16_t* const dst = h + (size_t)(first + p) * h_stride(I) +
+                                              h_position(i0 + n * R + at.out_row);
                         // bf16 has fp32's range (fp16 would overflow); its rounding, 2^-8, is that of y
-                        const uint32_t lo = f32_to_bf16_bits(hv[0]) | f32_to_bf16_bits(hv[1]) << 16;
-                        const uint32_t hi = f32_to_bf16_bits(hv[2]) | f32_to_bf16_bits(hv[3]) << 16;
-                        *reinterpret_cast<v2i*>(h + (size_t)(first + p) * h_stride(I) +
-                                                h_position(i0 + n * R + 4 * g)) = v2i{(int)lo, (int)hi};
+                        uint32_t bits[L::kOut];
+#pragma unroll
+                        for (int q = 0; q < L::kOut; ++q)
+                            bits[q] = f32_to_bf16_bits(gv[q] / (1.0f + expf(-gv[q])) * uv[q]);
+                        if constexpr (L::kOut == 2)
+                            *reinterpret_cast<uint32_t*>(dst) = bits[0] | bits[1] << 16;
+                        else
+                            *dst = (uint16_t)bits[0];
                     }
                 }
         }
@@ -468,7 +493,6 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][rows]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int r = lane & 15, g = lane >> 4;
     const L at(lane);
     const int n0 = blockIdx.x * kDownRows;
 
@@ -534,18 +558,15 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c], acc[i]);
             }
-            v4f v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = L::fold(acc[i]);
+            float v[L::kOut];
+            at.fold(acc, lane, v);
             const int t = st.tokens.at(p);
             // a token occurs once among an expert's pairs, so no two lanes meet
-            if (r < kDownRows && 4 * g < kDownRows && t >= 0) {
-                v4f* const dst = reinterpret_cast<v4f*>(mine + t * kDownRows + 4 * g);
+            if (at.owner && t >= 0) {
+                float2* const dst = reinterpret_cast<float2*>(mine + t * kDownRows + at.out_row);
                 const float f = wt[st.first + p];
-                v4f d = *dst;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = __builtin_fmaf(v[i], f, d[i]);
-                *dst = d;
+                const float2 d = *dst;
+                *dst = make_float2(__builtin_fmaf(v[0], f, d.x), __builtin_fmaf(v[1], f, d.y));
             }
         }
     };
