@@ -597,12 +597,11 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
     return finish("fp8_linear_blockwise", e);
 }
 
-int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t E, int64_t top_k)
+int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k)
 {
-    if (T < 1 || T > kMoeMaxTokens || I < 16 || I > kMoeMaxDim || E < 1 || E > kMoeMaxExperts ||
-        top_k < 1 || top_k > kMoeMaxTopK || top_k > E)
+    if (T < 1 || T > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || I < 16 || I > kMoeMaxDim)
         return 0;
-    return moe_work_bytes(T, I, E, top_k);
+    return kMoeRoutingBytes + T * top_k * blocks_of(I) * kBlock * 2;
 }
 
 fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits, const uint8_t* w13,
@@ -626,7 +625,7 @@ fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits, con
         bw2{w2, u64(E) * u64(H) * u64(I)}, bs2{s2, u64(E) * weight_scale_bytes(H, I)},
         by{y, u64(T) * u64(H) * 2}, bi{ids, u64(T) * u64(top_k) * 4},
         bw{weights, u64(T) * u64(top_k) * 4},
-        bk{work, u64(fp8_moe_blockwise_work_bytes(T, I, E, top_k))};
+        bk{work, u64(fp8_moe_blockwise_work_bytes(T, I, top_k))};
     FP8Q_TRY(check_apart({bi, bw, bk}, {bx, bl, bw13, bs13, bw2, bs2, by}));
     FP8Q_TRY(check_apart({by}, {bl, bw13, bs13, bw2, bs2}));
     FP8Q_TRY(check_device());

@@ -138,8 +138,7 @@ __device__ __forceinline__ void route_token(const float* __restrict__ logits, in
 }
 
 // The experts that any token chose, in ascending order: 64 experts to a word.
-// first[i] is the number of token tiles of the experts before expert 64 i +
-// lane.
+// first[i] is the number of pairs of the experts before expert 64 i + lane.
 template <int PER>
 struct Active {
     uint64_t word[PER];
@@ -148,11 +147,11 @@ struct Active {
     __device__ __forceinline__ void find(const uint64_t* masks, int experts, int lane)
     {
         count = 0;
-        int tiles = 0;
+        int pairs = 0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             const int e = i * 64 + lane;
-            const int n = e < experts ? (__popcll(masks[e]) + 7) / 8 : 0;
+            const int n = e < experts ? __popcll(masks[e]) : 0;
             word[i] = __ballot(n != 0);
             count += __popcll(word[i]);
             int scan = n;
@@ -161,11 +160,11 @@ struct Active {
                 const int below = __shfl_up(scan, d);
                 if (lane >= d) scan += below;
             }
-            first[i] = tiles + scan - n;
-            tiles += __builtin_amdgcn_readlane(scan, 63);
+            first[i] = pairs + scan - n;
+            pairs += __builtin_amdgcn_readlane(scan, 63);
         }
     }
-    __device__ __forceinline__ int first_tile(int e) const
+    __device__ __forceinline__ int first_pair(int e) const
     {
         int p = 0;
 #pragma unroll
@@ -268,17 +267,17 @@ struct Layout {
     }
 };
 
-// The workspace's h: the pairs grouped by expert, an expert's tokens in tiles
-// of eight, and each tile's K blocks in the lane order of moe_down's two
-// loads, so that a load reads 1 KiB in a row: element of token `tok` of the
-// tile, column i.  (In rows of h the lanes' 16 bytes lay in eight rows:
-// moe_down at 64 tokens of 128 experts of 768 x 2048 43.8 us.)
-__device__ __forceinline__ size_t h_element(int tile, int tok, int i, int nblk)
+// Where column i of h stands in its row.  The down projection's lane of unit
+// u multiplies columns 16 u .. 16 u + 15 of a block with two MFMAs of eight
+// each; the first eights of all units come first, so that each of its two
+// loads reads whole 128-byte lines (with the columns in order it read 16 bytes
+// of every 32: moe_down at 64 tokens of 128 experts of 768 x 2048 58.4 us).
+// Rows are padded to whole blocks.
+__device__ __forceinline__ int h_position(int i)
 {
-    const int unit = i >> 4 & 7, sub = i >> 3 & 1;
-    const int lane = 2 * tok + (unit & 1) + 16 * (unit >> 1);
-    return (((size_t)tile * nblk + (i >> 7)) * 2 + sub) * 512 + lane * 8 + (i & 7);
+    return (i & ~127) | (i & 8) << 3 | (i >> 4 & 7) << 3 | (i & 7);
 }
+__device__ __forceinline__ int h_stride(int I) { return (I + kBlock - 1) / kBlock * kBlock; }
 
 // ---------------------------------------------------------------- selection, a kernel of its own
 // One wave per token.  Used above kRouteInline tokens, where repeating the
@@ -308,8 +307,9 @@ __global__ __launch_bounds__(64) void moe_route_kernel(const float* __restrict__
 // still use every CU.
 //
 // h and the weights it will be summed with are stored grouped by expert (the
-// p-th token of an expert in tile first_tile + p / 8), so that the second
-// kernel reads an expert's rows without looking them up.
+// p-th token of an expert at first_pair + p), so that the second kernel reads
+// an expert's rows without looking them up, and each row block by block in
+// the order of the second kernel's operands (h_position).
 //
 // With ROUTED the selection is there already (moe_route_kernel); without it
 // every workgroup makes it, and the first one stores it.
@@ -371,7 +371,7 @@ void moe_up_kernel(
         const int slot = it / tiles;
         const int i0 = (it - slot * tiles) * COLS;
         const int e = active.expert(slot, lane);
-        const int first = active.first_tile(e);
+        const int first = active.first_pair(e);
         Tokens tokens;
         tokens.find(masks, e, lane);
         if (i0 == 0 && lane < tokens.count) {
@@ -379,7 +379,7 @@ void moe_up_kernel(
             float v = 0.0f;
             for (int j = 0; j < top_k; ++j)
                 if (ids[tokens.list * top_k + j] == e) v = wt[tokens.list * top_k + j];
-            pair_weights[first * 8 + lane] = v;
+            pair_weights[first + lane] = v;
         }
         const size_t row = (size_t)e * 2 * I + i0;                   // gate row; up: + I
         const rsrc_t rw[2] = {make_rsrc(w13 + row * H, (uint32_t)(COLS * H)),
@@ -455,8 +455,8 @@ void moe_up_kernel(
                     at.fold(acc[m][n][1], lane, uv);
                     const int p = p0 + m * R + at.row;
                     if (at.owner && p < tokens.count) {
-                        uint16_t* const dst =
-                            h + h_element(first + p / 8, p % 8, i0 + n * R + at.out_row, nb);
+                        uint16_t* const dst = h + (size_t)(first + p) * h_stride(I) +
+                                              h_position(i0 + n * R + at.out_row);
                         // bf16 has fp32's range (fp16 would overflow); its rounding, 2^-8, is that of y
                         uint32_t bits[L::kOut];
 #pragma unroll
@@ -489,6 +489,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
 {
     typedef Layout<kDownRows> L;
     __shared__ uint64_t masks[PER * 64];
+    __shared__ float wt[kMaxPairs];
     extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][rows]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -496,6 +497,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const int n0 = blockIdx.x * kDownRows;
 
     if (tid < E) masks[tid] = masks_in[tid];
+    for (int i = tid; i < T * top_k; i += kMoeThreads) wt[i] = pair_weights[i];
     for (int i = tid; i < kMoeWaves * T * kDownRows; i += kMoeThreads) ysum[i] = 0.0f;
     __syncthreads();
     Active<PER> active;
@@ -504,31 +506,31 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const int nblk = (I + kBlock - 1) / kBlock;
     const int chunks = (nblk + kDownBlocks - 1) / kDownBlocks;
     const int items = active.count * chunks;
+    const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * h_stride(I) * 2));
     float* const mine = ysum + wave * T * kDownRows;
 
-    // the lane's part of a tile of h in the K blocks from kb0 (none: zeros)
-    auto load_h = [&](v4i (&hv)[kDownBlocks][2], int tile, bool none, int kb0) {
-        const rsrc_t rh = make_rsrc(h + ((size_t)tile * nblk + kb0) * 1024,
-                                    (uint32_t)min(kDownBlocks, nblk - kb0) * 2048);
+    // rows of h of pair p (none: zeros) in the K blocks from kb0
+    auto load_h = [&](v4i (&hv)[kDownBlocks][2], int p, bool none, int kb0) {
 #pragma unroll
         for (int c = 0; c < kDownBlocks; ++c) {
-            const uint32_t o = none || (kb0 + c) * kBlock + at.koff >= I ? kOOB : c * 2048 + lane * 16;
+            const int kb = (kb0 + c) * kBlock;
+            const uint32_t o = none || kb + at.koff >= I
+                                   ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2;
             hv[c][0] = buf_load16(rh, o);
-            hv[c][1] = buf_load16(rh, o + 1024);
+            hv[c][1] = buf_load16(rh, o + 128);
         }
     };
     struct Stage {
         v4i w[kDownBlocks], h[kDownBlocks][2];
-        float s[kDownBlocks], weight;
-        int kb0, tile;
+        float s[kDownBlocks];
+        int kb0, first;
         Tokens tokens;
     };
     // past the last item the loads are still issued, out of range, so that
     // the number of loads in flight, and with it the wait, is always the same
     auto request = [&](Stage& st, int it) {
         const uint32_t none = it < items ? 0u : kOOB;
-        it = min(it, items - 1);
-        const int slot = it / chunks;
+        const int slot = min(it, items - 1) / chunks;
         st.kb0 = (it - slot * chunks) * kDownBlocks;
         const int e = active.expert(slot, lane);
         const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(kDownRows * I));
@@ -540,19 +542,15 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
                                                 ? (uint32_t)(at.row * I + kb * kBlock + at.koff) | none : kOOB);
             st.s[c] = sb[min(kb, nblk - 1)];
         }
-        st.tile = active.first_tile(e);
+        st.first = active.first_pair(e);
         st.tokens.find(masks, e, lane);
-        load_h(st.h, st.tile, none != 0 || at.row >= st.tokens.count, st.kb0);
-        st.weight = pair_weights[st.tile * 8 + at.row];
+        load_h(st.h, st.first + at.row, none != 0 || at.row >= st.tokens.count, st.kb0);
         __builtin_amdgcn_sched_barrier(0);
     };
     auto compute = [&](Stage& st) {
         for (int p0 = 0; p0 < st.tokens.count; p0 += kDownRows) {
             const int p = p0 + at.row;
-            if (p0 > 0) {
-                load_h(st.h, st.tile + p0 / 8, p >= st.tokens.count, st.kb0);
-                st.weight = pair_weights[st.tile * 8 + p];
-            }
+            if (p0 > 0) load_h(st.h, st.first + p, p >= st.tokens.count, st.kb0);
             v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int c = 0; c < kDownBlocks; ++c) {
@@ -566,8 +564,9 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
             // a token occurs once among an expert's pairs, so no two lanes meet
             if (at.owner && t >= 0) {
                 float2* const dst = reinterpret_cast<float2*>(mine + t * kDownRows + at.out_row);
+                const float f = wt[st.first + p];
                 const float2 d = *dst;
-                *dst = make_float2(__builtin_fmaf(v[0], st.weight, d.x), __builtin_fmaf(v[1], st.weight, d.y));
+                *dst = make_float2(__builtin_fmaf(v[0], f, d.x), __builtin_fmaf(v[1], f, d.y));
             }
         }
     };
@@ -592,32 +591,24 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     }
 }
 
-// Tiles of eight tokens that the pairs can take: every chosen expert may leave
-// one partly empty.
-inline int64_t max_tiles(int64_t T, int64_t E, int64_t top_k)
-{
-    const int64_t pairs = T * top_k;
-    return std::min(pairs, E) + pairs / 8;
-}
-
-// The workspace: the experts' token masks, the weights grouped like h, h.
+// The workspace: the experts' token masks, the grouped weights, h.
 struct MoeWork {
     uint64_t* masks;
     float* weights;
     uint16_t* h;
-    MoeWork(void* p, int64_t T, int64_t E, int64_t top_k)
+    explicit MoeWork(void* p)
+        : masks(static_cast<uint64_t*>(p)),
+          weights(reinterpret_cast<float*>(static_cast<char*>(p) + kMoeMaxExperts * 8)),
+          h(reinterpret_cast<uint16_t*>(static_cast<char*>(p) + kMoeRoutingBytes))
     {
-        char* at = static_cast<char*>(p);
-        masks = reinterpret_cast<uint64_t*>(at);
-        weights = reinterpret_cast<float*>(at += kMoeMaxExperts * 8);
-        h = reinterpret_cast<uint16_t*>(at += max_tiles(T, E, top_k) * 8 * 4);
     }
 };
+static_assert(kMoeMaxExperts * 8 + kMaxPairs * 4 <= kMoeRoutingBytes, "head of the workspace");
 
 template <int DT, int PER, int R, int RT, int MT, int UB, int WAVES, int OCC, bool ROUTED>
 hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
 {
-    const MoeWork work(a.work, a.T, a.E, a.top_k);
+    const MoeWork work(a.work);
     const int64_t items = std::min<int64_t>(a.E, (int64_t)a.T * a.top_k) * (a.I / (R * RT));
     const int grid = (int)std::min<int64_t>(items, kCUs * OCC * 4 / WAVES);
     moe_up_kernel<DT, PER, R, RT, MT, UB, WAVES, OCC, ROUTED><<<grid, WAVES * 64, 0, stream>>>(
@@ -630,7 +621,7 @@ template <int PER>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
     const size_t lds = (size_t)kMoeWaves * a.T * kDownRows * sizeof(float);
-    const MoeWork work(a.work, a.T, a.E, a.top_k);
+    const MoeWork work(a.work);
     moe_down_kernel<PER><<<a.H / kDownRows, kMoeThreads, lds, stream>>>(
         work.h, a.w2, a.s2, work.masks, work.weights, a.y, a.T, a.H, a.I, a.E, a.top_k);
     return hipGetLastError();
@@ -668,13 +659,6 @@ hipError_t launch_moe_dt(const MoeArgs& a, hipStream_t stream)
 }
 
 }  // namespace
-
-int64_t moe_work_bytes(int64_t T, int64_t I, int64_t E, int64_t top_k)
-{
-    const MoeWork work(nullptr, T, E, top_k);
-    return (int64_t)reinterpret_cast<intptr_t>(work.h) +
-           max_tiles(T, E, top_k) * 8 * blocks_of(I) * kBlock * 2;
-}
 
 hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t stream)
 {

@@ -56,7 +56,7 @@ _SIGS = {
     "fp8_quantize_weight_blocks": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p]),
     "fp8_gemm_blockwise": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
     "fp8_linear_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
-    "fp8_moe_blockwise_work_bytes": (_i64, [_i64, _i64, _i64, _i64]),
+    "fp8_moe_blockwise_work_bytes": (_i64, [_i64, _i64, _i64]),
     "fp8_moe_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64,
                                _i64, _i, _p]),
 }
@@ -420,7 +420,7 @@ def fp8_moe_blockwise(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor,
         ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     if weights is None:
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
-    need = lib.fp8_moe_blockwise_work_bytes(T, I, E, top_k)
+    need = lib.fp8_moe_blockwise_work_bytes(T, I, top_k)
     if work is None:
         work = torch.empty(need, dtype=torch.uint8, device=dev)
     elif work.numel() < need:
@@ -442,9 +442,9 @@ def fp8_moe_blockwise(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor,
     return y, ids, weights
 
 
-def moe_work_bytes(tokens: int, inter: int, experts: int, top_k: int) -> int:
+def moe_work_bytes(tokens: int, inter: int, top_k: int) -> int:
     """Bytes of scratch fp8_moe_blockwise needs (0 for sizes it refuses)."""
-    return int(lib.fp8_moe_blockwise_work_bytes(tokens, inter, experts, top_k))
+    return int(lib.fp8_moe_blockwise_work_bytes(tokens, inter, top_k))
 
 
 class DelayedScaling:

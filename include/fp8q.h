@@ -426,15 +426,14 @@ FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_
  *                    than top_k are left
  *   weights[T,top_k] out: softmax weights, over the chosen experts
  *                    (renormalize != 0) or over all E (0); 0 beside an id -1
- *   work        scratch, fp8_moe_blockwise_work_bytes(T, I, E, top_k) bytes,
+ *   work        scratch, fp8_moe_blockwise_work_bytes(T, I, top_k) bytes,
  *                    16-byte aligned; contents before and after the call are
  *                    of no meaning.  Calls that may run at the same time need
  *                    one each.
  *   1 <= T <= 64;  16 <= H, I <= 65536, multiples of 16;  1 <= E <= 512;
- *   1 <= top_k <= min(E, 16).  Two launches, three above 16 tokens.
+ *   1 <= top_k <= min(E, 16).  Two launches.
  */
-FP8Q_API int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t E,
-                                               int64_t top_k);
+FP8Q_API int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k);
 FP8Q_API fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits,
                                        const uint8_t* w13, const float* s13, const uint8_t* w2,
                                        const float* s2, uint16_t* y, int32_t* ids, float* weights,

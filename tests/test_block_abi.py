@@ -101,10 +101,9 @@ def test_moe_refused_before_any_hip_call(change, status):
 
 
 def test_moe_work_bytes():
-    assert fp8q.moe_work_bytes(1, 16, 1, 1) > 32
-    assert fp8q.moe_work_bytes(64, 1024, 64, 16) >= 64 * 1024 * 16 * 2
-    for sizes in ((0, 16, 1, 1), (65, 16, 1, 1), (1, 8, 1, 1), (1, 65552, 1, 1), (1, 16, 0, 1),
-                  (1, 16, 513, 1), (1, 16, 4, 0), (1, 16, 32, 17), (1, 16, 4, 5)):
+    assert fp8q.moe_work_bytes(1, 16, 1) > 32
+    assert fp8q.moe_work_bytes(64, 1024, 16) >= 64 * 1024 * 16 * 2
+    for sizes in ((0, 16, 1), (65, 16, 1), (1, 8, 1), (1, 65552, 1), (1, 16, 0), (1, 16, 17)):
         assert fp8q.moe_work_bytes(*sizes) == 0
 
 

@@ -118,7 +118,7 @@ def test_same_result_on_streams_in_graphs_and_in_place(T, E, H, I, top_k):
     want = [t.clone() for t in fp8q.fp8_moe_blockwise(x, logits, *w, top_k)]
     guard = torch.full((T * H + 64,), 7.0, dtype=torch.bfloat16, device=DEV)
     outs = [guard[:T * H].view(T, H), torch.empty_like(want[1]), torch.empty_like(want[2])]
-    work = torch.full((fp8q.moe_work_bytes(T, I, E, top_k) + 64,), 0x5A, dtype=torch.uint8, device=DEV)
+    work = torch.full((fp8q.moe_work_bytes(T, I, top_k) + 64,), 0x5A, dtype=torch.uint8, device=DEV)
 
     def same():
         torch.cuda.synchronize()
