@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "block.hpp"
 #include "tile.hpp"
@@ -473,46 +474,46 @@ void moe_up_kernel(
 }
 
 // ---------------------------------------------------------------- down projection
-// A workgroup owns eight columns of y.  Its waves take items of kDownBlocks K
-// blocks of one expert; the next item's weights, and the rows of h of its
-// first eight tokens, are requested before the current one's products.  Each
-// wave adds its products, weighted, to sums of its own in LDS; the waves' sums
-// are added in a fixed order at the end.
-constexpr int kDownRows = 8;                // columns of y (rows of W2) per workgroup
-constexpr int kDownBlocks = 3;              // K blocks per item
+// A workgroup owns RT row tiles of eight columns of y.  Its waves take items of
+// BLOCKS K blocks of one expert; the next item's weights, and the rows of h of
+// its first eight tokens, are requested before the current one's products.
+// Each wave adds its products, weighted, to sums of its own in LDS; the waves'
+// sums are added in a fixed order at the end.
+constexpr int kDownRows = 8;                // columns of y (rows of W2) per row tile
 
-template <int PER>
+template <int PER, int RT, int BLOCKS, int CP>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const uint16_t* __restrict__ h, const uint8_t* __restrict__ w2, const float* __restrict__ s2,
     const uint64_t* __restrict__ masks_in, const float* __restrict__ pair_weights,
     uint16_t* __restrict__ y, int T, int H, int I, int E, int top_k)
 {
     typedef Layout<kDownRows> L;
+    constexpr int COLS = RT * kDownRows;
     __shared__ uint64_t masks[PER * 64];
     __shared__ float wt[kMaxPairs];
-    extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][rows]
+    extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][COLS]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const L at(lane);
-    const int n0 = blockIdx.x * kDownRows;
+    const int n0 = blockIdx.x * COLS;
 
     if (tid < E) masks[tid] = masks_in[tid];
     for (int i = tid; i < T * top_k; i += kMoeThreads) wt[i] = pair_weights[i];
-    for (int i = tid; i < kMoeWaves * T * kDownRows; i += kMoeThreads) ysum[i] = 0.0f;
+    for (int i = tid; i < kMoeWaves * T * COLS; i += kMoeThreads) ysum[i] = 0.0f;
     __syncthreads();
     Active<PER> active;
     active.find(masks, E, lane);
 
     const int nblk = (I + kBlock - 1) / kBlock;
-    const int chunks = (nblk + kDownBlocks - 1) / kDownBlocks;
+    const int chunks = (nblk + BLOCKS - 1) / BLOCKS;
     const int items = active.count * chunks;
     const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * h_stride(I) * 2));
-    float* const mine = ysum + wave * T * kDownRows;
+    float* const mine = ysum + wave * T * COLS;
 
     // rows of h of pair p (none: zeros) in the K blocks from kb0
-    auto load_h = [&](v4i (&hv)[kDownBlocks][2], int p, bool none, int kb0) {
+    auto load_h = [&](v4i (&hv)[BLOCKS][2], int p, bool none, int kb0) {
 #pragma unroll
-        for (int c = 0; c < kDownBlocks; ++c) {
+        for (int c = 0; c < BLOCKS; ++c) {
             const int kb = (kb0 + c) * kBlock;
             const uint32_t o = none || kb + at.koff >= I
                                    ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2;
@@ -521,8 +522,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
         }
     };
     struct Stage {
-        v4i w[kDownBlocks], h[kDownBlocks][2];
-        float s[kDownBlocks];
+        v4i w[BLOCKS][RT], h[BLOCKS][2];
+        float s[BLOCKS];
         int kb0, first;
         Tokens tokens;
     };
@@ -530,16 +531,20 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     // the number of loads in flight, and with it the wait, is always the same
     auto request = [&](Stage& st, int it) {
         const uint32_t none = it < items ? 0u : kOOB;
-        const int slot = min(it, items - 1) / chunks;
-        st.kb0 = (it - slot * chunks) * kDownBlocks;
+        it = min(it, items - 1);
+        const int slot = it / chunks;
+        st.kb0 = (it - slot * chunks) * BLOCKS;
         const int e = active.expert(slot, lane);
-        const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(kDownRows * I));
+        const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(COLS * I));
         const float* const sb = s2 + ((size_t)e * ((H + kBlock - 1) / kBlock) + (n0 >> 7)) * nblk;
 #pragma unroll
-        for (int c = 0; c < kDownBlocks; ++c) {
+        for (int c = 0; c < BLOCKS; ++c) {
             const int kb = st.kb0 + c;
-            st.w[c] = buf_load16<CP_NT>(rw, kb * kBlock + at.koff < I
-                                                ? (uint32_t)(at.row * I + kb * kBlock + at.koff) | none : kOOB);
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+                st.w[c][n] = buf_load16<CP>(
+                    rw, kb * kBlock + at.koff < I
+                            ? (uint32_t)((n * kDownRows + at.row) * I + kb * kBlock + at.koff) | none : kOOB);
             st.s[c] = sb[min(kb, nblk - 1)];
         }
         st.first = active.first_pair(e);
@@ -551,22 +556,26 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
         for (int p0 = 0; p0 < st.tokens.count; p0 += kDownRows) {
             const int p = p0 + at.row;
             if (p0 > 0) load_h(st.h, st.first + p, p >= st.tokens.count, st.kb0);
-            v4f acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < kDownBlocks; ++c) {
-                const v4f q = block_product<DT_BF16>(st.w[c], st.h[c][0], st.h[c][1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c], acc[i]);
-            }
-            float v[L::kOut];
-            at.fold(acc, lane, v);
             const int t = st.tokens.at(p);
-            // a token occurs once among an expert's pairs, so no two lanes meet
-            if (at.owner && t >= 0) {
-                float2* const dst = reinterpret_cast<float2*>(mine + t * kDownRows + at.out_row);
-                const float f = wt[st.first + p];
-                const float2 d = *dst;
-                *dst = make_float2(__builtin_fmaf(v[0], f, d.x), __builtin_fmaf(v[1], f, d.y));
+            const float f = t >= 0 ? wt[st.first + p] : 0.0f;
+#pragma unroll
+            for (int n = 0; n < RT; ++n) {
+                v4f acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < BLOCKS; ++c) {
+                    const v4f q = block_product<DT_BF16>(st.w[c][n], st.h[c][0], st.h[c][1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c], acc[i]);
+                }
+                float v[L::kOut];
+                at.fold(acc, lane, v);
+                // a token occurs once among an expert's pairs, so no two lanes meet
+                if (at.owner && t >= 0) {
+                    float2* const dst =
+                        reinterpret_cast<float2*>(mine + t * COLS + n * kDownRows + at.out_row);
+                    const float2 d = *dst;
+                    *dst = make_float2(__builtin_fmaf(v[0], f, d.x), __builtin_fmaf(v[1], f, d.y));
+                }
             }
         }
     };
@@ -583,11 +592,12 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
         }
     }
     __syncthreads();
-    for (int o = tid; o < T * kDownRows; o += kMoeThreads) {
+    for (int o = tid; o < T * COLS; o += kMoeThreads) {
         float v = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kMoeWaves; ++i) v += ysum[i * T * kDownRows + o];
-        y[(size_t)(o / kDownRows) * H + n0 + o % kDownRows] = (uint16_t)f32_to_bf16_bits(v);
+        for (int i = 0; i < kMoeWaves; ++i) v += ysum[i * T * COLS + o];
+        if (n0 + o % COLS < H)
+            y[(size_t)(o / COLS) * H + n0 + o % COLS] = (uint16_t)f32_to_bf16_bits(v);
     }
 }
 
@@ -617,14 +627,30 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int PER>
+template <int PER, int RT, int BLOCKS, int CP>
+hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
+{
+    constexpr int COLS = RT * kDownRows;
+    auto kern = moe_down_kernel<PER, RT, BLOCKS, CP>;
+    const size_t lds = (size_t)kMoeWaves * a.T * COLS * sizeof(float);
+    static std::atomic<uint64_t> attr_devices{0};
+    if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern),
+                                                kMoeWaves * kMoeMaxTokens * COLS * sizeof(float),
+                                                attr_devices);
+        e != hipSuccess)
+        return e;
+    const MoeWork work(a.work);
+    kern<<<(a.H + COLS - 1) / COLS, kMoeThreads, lds, stream>>>(work.h, a.w2, a.s2, work.masks,
+                                                                work.weights, a.y, a.T, a.H, a.I,
+                                                                a.E, a.top_k);
+    return hipGetLastError();
+}
+
+template <int PER, int RT, int BLOCKS>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
-    const size_t lds = (size_t)kMoeWaves * a.T * kDownRows * sizeof(float);
-    const MoeWork work(a.work);
-    moe_down_kernel<PER><<<a.H / kDownRows, kMoeThreads, lds, stream>>>(
-        work.h, a.w2, a.s2, work.masks, work.weights, a.y, a.T, a.H, a.I, a.E, a.top_k);
-    return hipGetLastError();
+    return a.I % kBlock == 0 ? launch_down_cp<PER, RT, BLOCKS, CP_NT>(a, stream)
+                             : launch_down_cp<PER, RT, BLOCKS, CP_DEFAULT>(a, stream);
 }
 
 // Above this many tokens the selection is a kernel of its own.
@@ -646,7 +672,8 @@ hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
         else
             e = launch_up<DT, PER, 8, 2, 2, 1, 16, 4, true>(a, stream);
     }
-    return e == hipSuccess ? launch_down<PER>(a, stream) : e;
+    if (e != hipSuccess) return e;
+    return a.H < 16 * kCUs ? launch_down<PER, 1, 3>(a, stream) : launch_down<PER, 2, 2>(a, stream);
 }
 
 template <int DT>
