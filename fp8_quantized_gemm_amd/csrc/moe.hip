@@ -138,6 +138,18 @@ __device__ __forceinline__ void route_token(const float* __restrict__ logits, in
     if (id >= 0) weight /= renormalize ? chosen : total;
 }
 
+// Inclusive sum over the lanes of a wave (DPP).
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr 1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);    // row_shr 2
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);    // row_shr 4
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);    // row_shr 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast15 -> rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast31 -> rows 2, 3
+    return v;
+}
+
 // The experts that any token chose, in ascending order: 64 experts to a word.
 // first[i] is the number of pairs of the experts before expert 64 i + lane.
 template <int PER>
@@ -155,12 +167,7 @@ struct Active {
             const int n = e < experts ? __popcll(masks[e]) : 0;
             word[i] = __ballot(n != 0);
             count += __popcll(word[i]);
-            int scan = n;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int below = __shfl_up(scan, d);
-                if (lane >= d) scan += below;
-            }
+            const int scan = wave_scan(n);
             first[i] = pairs + scan - n;
             pairs += __builtin_amdgcn_readlane(scan, 63);
         }
@@ -374,14 +381,6 @@ void moe_up_kernel(
         const int e = active.expert(slot, lane);
         const int first = active.first_pair(e);
         Tokens tokens;
-        tokens.find(masks, e, lane);
-        if (i0 == 0 && lane < tokens.count) {
-            // the weight of expert e among token tokens.list's choices
-            float v = 0.0f;
-            for (int j = 0; j < top_k; ++j)
-                if (ids[tokens.list * top_k + j] == e) v = wt[tokens.list * top_k + j];
-            pair_weights[first + lane] = v;
-        }
         const size_t row = (size_t)e * 2 * I + i0;                   // gate row; up: + I
         const rsrc_t rw[2] = {make_rsrc(w13 + row * H, (uint32_t)(COLS * H)),
                               make_rsrc(w13 + (row + I) * H, (uint32_t)(COLS * H))};
@@ -389,13 +388,9 @@ void moe_up_kernel(
         const float* const sg = s13 + ((size_t)e * 2 * nb + (i0 >> 7)) * nblk;
         const rsrc_t rs[2] = {make_rsrc(sg, (uint32_t)(nblk * 4)),
                               make_rsrc(sg + (size_t)nb * nblk, (uint32_t)(nblk * 4))};
-        for (int p0 = 0; p0 < tokens.count; p0 += MT * R) {
+        int p0 = 0;
+        do {                                                         // an active expert has a token
             uint32_t xo[MT];                                         // of this lane's token
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int t = tokens.at(p0 + m * R + at.row);
-                xo[m] = t >= 0 ? (uint32_t)(t * H + at.koff) * 2 : kOOB;
-            }
             v4f acc[MT][RT][2];
 #pragma unroll
             for (int m = 0; m < MT; ++m)
@@ -421,6 +416,14 @@ void moe_up_kernel(
                             rs[c], (uint32_t)((k >> 7) + at.block) * 4, 0, 0));
                     }
                 }
+                if (k0 == 0) {                                       // beside the first weights' way
+                    if (p0 == 0) tokens.find(masks, e, lane);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const int t = tokens.at(p0 + m * R + at.row);
+                        xo[m] = t >= 0 ? (uint32_t)(t * H + at.koff) * 2 : kOOB;
+                    }
+                }
 #pragma unroll
                 for (int u = 0; u < UB; ++u) {
                     const int k = k0 + u * KL;
@@ -431,6 +434,13 @@ void moe_up_kernel(
                         xv[u][m][0] = buf_load16(rx, o);
                         xv[u][m][1] = buf_load16(rx, o + 16);
                     }
+                }
+                if (i0 == 0 && k0 == 0 && p0 == 0 && lane < tokens.count) {
+                    // the weight of expert e among the choices of token tokens.list
+                    float v = 0.0f;
+                    for (int j = 0; j < top_k; ++j)
+                        if (ids[tokens.list * top_k + j] == e) v = wt[tokens.list * top_k + j];
+                    pair_weights[first + lane] = v;
                 }
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -469,7 +479,8 @@ void moe_up_kernel(
                             *dst = (uint16_t)bits[0];
                     }
                 }
-        }
+            p0 += MT * R;
+        } while (p0 < tokens.count);
     }
 }
 
@@ -663,7 +674,7 @@ hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
     if (a.T <= 4) {
         e = launch_up<DT, PER, 4, 1, 1, 4, 16, 4, false>(a, stream);
     } else if (a.T <= kRouteInline) {
-        e = launch_up<DT, PER, 8, 2, 1, 2, 16, 4, false>(a, stream);
+        e = launch_up<DT, PER, 8, 1, 1, 4, 16, 4, false>(a, stream);
     } else {
         moe_route_kernel<PER><<<a.T, 64, 0, stream>>>(a.logits, a.ids, a.weights, a.E, a.top_k,
                                                      a.renormalize);
