@@ -592,6 +592,11 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
     FP8Q_TRY(check_apart({bq, bsa}, {bx, bw, bsw, by}));
     FP8Q_TRY(check_apart({by}, {bw, bsw}));
     FP8Q_TRY(check_device());
+    // the one launch reads x while other workgroups already store y
+    if (linear_block_fused_pays(M, K) && !overlap(by, bx))
+        return finish("fp8_linear_blockwise",
+                      launch_linear_block_fused(x, dtype, qw, sw, y, q, sa, (int)M, (int)N, (int)K,
+                                                (hipStream_t)stream));
     hipError_t e = launch_quantize_blocks(x, dtype, M, K, q, sa, (hipStream_t)stream);
     if (e == hipSuccess) e = dispatch_block(q, sa, qw, sw, y, M, N, K, (hipStream_t)stream);
     return finish("fp8_linear_blockwise", e);

@@ -12,6 +12,7 @@
 // Activation scales are stored [K blocks, M]: the scales that a tile needs in
 // one K step are then contiguous.
 #include <algorithm>
+#include <atomic>
 
 #include "block.hpp"
 #include "tile.hpp"
@@ -124,7 +125,8 @@ __global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
 //
 // A workgroup owns 8 * RT weight rows (RT row tiles that share the activation
 // loads); its waves interleave over the K blocks.  Tokens come in MT groups
-// of eight.
+// of eight.  gemv_block_kernel, one workgroup per tile, serves the K that the
+// persistent kernel below does not hold.
 constexpr int kGbWaves = 16;
 constexpr int kGbUnroll = 2;
 
@@ -136,13 +138,19 @@ __device__ __forceinline__ v4f mfma_pair(const v4i& w, const v4i& a, v4f c)
     return __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(w1, a1, c, 0, 0, 0);
 }
 
+// The value of the lane beside this one (l ^ 1).
+__device__ __forceinline__ float quad_xor1(float v)
+{
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
+}
+
 template <int MT, int RT>
 __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, uint16_t* __restrict__ y, int M, int N, int K)
 {
     constexpr int U = kGbUnroll;
-    __shared__ float red[kGbWaves][2][MT * RT][8][9];
+    __shared__ float red[kGbWaves][MT * RT][8][9];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, odd = r & 1;
@@ -201,9 +209,11 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                red[wave][odd][m * RT + t][r >> 1][2 * g + e] =
-                    odd ? acc[m][t][2 * e + 1] : acc[m][t][2 * e];
+            for (int e = 0; e < 2; ++e) {
+                const float own = odd ? acc[m][t][2 * e + 1] : acc[m][t][2 * e];
+                const float sum = own + quad_xor1(own);
+                if (!odd) red[wave][m * RT + t][r >> 1][2 * g + e] = sum;
+            }
     __syncthreads();
     for (int o = threadIdx.x; o < MT * RT * 64; o += kGbWaves * 64) {
         const int row = o & 7, t = (o >> 3) % RT, mm = (o >> 3) / RT;     // token mm, row 8 t + row
@@ -211,10 +221,205 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
         if (mm >= M || n >= N) continue;
         float v = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kGbWaves; ++w)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) v += red[w][h][(mm >> 3) * RT + t][mm & 7][row];
+        for (int w = 0; w < kGbWaves; ++w) v += red[w][(mm >> 3) * RT + t][mm & 7][row];
         y[(size_t)mm * N + n] = (uint16_t)f32_to_bf16_bits(v);
+    }
+}
+
+// ---------------------------------------------------------------- persistent decode product
+// The product for K up to 16 waves * NB blocks, on at most one workgroup per
+// CU: a wave's K blocks are the same for every row tile, so its activation
+// operands and scales stay in registers and only weights stream.  The next
+// tile's weights are requested before the current tile's partial results are
+// exchanged.
+//
+// With SRC_BF16 / SRC_FP16 it is the whole of fp8_linear_blockwise: every
+// workgroup quantizes the activation into LDS first, 16 lanes to a block as in
+// quant_blocks_kernel (same codes and scales), with its first weights already
+// on the way; workgroup 0 also stores the codes and scales.  XV vectors of
+// eight values per thread.
+//
+// LDS: two buffers of partial results; with quantization also the codes, row
+// m at m * nblk * 128, 16-byte unit u of a block at u ^ (m & 7), so that the
+// eight rows of an operand read lie in different banks, and the scales
+// [nblk][M].
+//
+// Measured with replayed graphs and cold weights, M = 8, against one
+// workgroup of gemv_block_kernel per tile and a quantizer launch: N x K =
+// 12288 x 4096 12.9 against 13.1 us, M = 1 10.3 against 13.1; two workgroups
+// per CU (64 VGPRs, spills) 20 us.
+enum : int { SRC_CODES = 0, SRC_BF16 = 1, SRC_FP16 = 2 };
+
+template <int SRC, int MT, int NB, int RT, int XV>
+__global__ __launch_bounds__(kGbWaves * 64) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void gemv_block_persistent_kernel(const void* __restrict__ src, const uint8_t* __restrict__ qw,
+                                  const float* __restrict__ sw, uint16_t* __restrict__ y,
+                                  uint8_t* __restrict__ q, float* __restrict__ sa, int M, int N, int K)
+{
+    constexpr int NT = kGbWaves * 64;
+    constexpr int DT = SRC == SRC_FP16 ? DT_FP16 : DT_BF16;
+    constexpr bool kTight = NB * (RT * 4 + MT * 5 + 1) > 60;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    float(*red)[kGbWaves][MT * RT][8][9] = reinterpret_cast<float(*)[kGbWaves][MT * RT][8][9]>(lds);
+    uint8_t* const codes = lds + 2 * sizeof(red[0]);
+    const int nblk = (K + kBlock - 1) / kBlock;
+    float* const sc = reinterpret_cast<float*>(codes + M * nblk * kBlock);
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4, odd = r & 1;
+    const int unit = 2 * g + odd, koff = unit * 16;
+    const int tiles = (N + 8 * RT - 1) / (8 * RT);
+
+    v4i a[NB][MT];
+    float s[NB][MT];
+    v4i v[XV];                                 // this thread's vector of cell (tid >> 4) + 64 j
+    const int c8 = (tid & 15) * 8, cells = M * nblk;
+    if constexpr (SRC == SRC_CODES) {
+        const rsrc_t ra = make_rsrc(src, (uint32_t)(M * K));
+        const rsrc_t rs = make_rsrc(sa, (uint32_t)(M * nblk * 4));
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int kb = wave + u * kGbWaves, row = m * 8 + (r >> 1);
+                a[u][m] = buf_load16(ra, kb * kBlock + koff < K
+                                             ? (uint32_t)(row * K + kb * kBlock + koff) : kOOB);
+                // tokens past M read another token's scale or zero: their results are dropped
+                s[u][m] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                    rs, kb < nblk ? (uint32_t)((kb * M + row) * 4) : kOOB, 0, 0));
+            }
+    } else {
+        const uint16_t* const x = static_cast<const uint16_t*>(src);
+#pragma unroll
+        for (int j = 0; j < XV; ++j) {
+            const int cell = (tid >> 4) + j * (NT / 16);
+            const int m = cell / nblk, col = (cell - m * nblk) * kBlock + c8;
+            v[j] = cell < cells && col < K ? *reinterpret_cast<const v4i*>(x + (size_t)m * K + col)
+                                           : v4i{0, 0, 0, 0};
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+
+    v4i w[NB][RT];
+    float sb[NB];
+    auto load_w = [&](int t) {
+        const int n0 = t * 8 * RT;
+        const rsrc_t rw = make_rsrc(qw + (size_t)n0 * K, (uint32_t)(min(8 * RT, N - n0) * K));
+        const rsrc_t rs = make_rsrc(sw + (size_t)(n0 >> 7) * nblk, (uint32_t)(nblk * 4));
+        // the lane's offsets are computed again for each tile rather than held
+        // across the tiles (2 NB RT registers)
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        const int lk = (2 * (l >> 4) + (l & 1)) * 16;
+        const uint32_t off = (uint32_t)(((l & 15) >> 1) * K + lk);
+#pragma unroll
+        for (int u = 0; u < NB; ++u) {
+            const int kb = wave + u * kGbWaves;
+            const bool in = kb * kBlock + lk < K;
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+                w[u][n] = buf_load16<CP_NT>(rw, in ? off + n * 8 * K + kb * kBlock : kOOB);
+            // a vector load: a scalar one would hold up the prologue's LDS waits
+            sb[u] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (uint32_t)(kb * 4), 0, 0));
+            if constexpr (kTight) __builtin_amdgcn_sched_barrier(0);   // one block's offsets at a time
+        }
+    };
+    load_w(blockIdx.x);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (SRC == SRC_CODES) {
+        // wait for the operands here: left to their first use, in the loop,
+        // the wait there would cover the weights of every tile whole
+        // (12288 x 4096 11.2 against 10.0 us)
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                asm volatile("" : "+v"(a[u][m]));
+                asm volatile("" : "+v"(s[u][m]));
+            }
+    }
+
+    if constexpr (SRC != SRC_CODES) {
+#pragma unroll
+        for (int j = 0; j < XV; ++j) {
+            const int cell = (tid >> 4) + j * (NT / 16);
+            const int m = cell / nblk, kb = cell - m * nblk, col = kb * kBlock + c8;
+            const float sx = scale_from_amax(row16_max(vec_absmax<DT>(v[j])));
+            if (cell < cells) {
+                const v2i c = vec_quantize<DT>(v[j], Quotient(sx));
+                *reinterpret_cast<v2i*>(codes + (m * nblk + kb) * kBlock +
+                                        (((c8 >> 4) ^ (m & 7)) << 4) + (c8 & 8)) = c;
+                if (c8 == 0) sc[kb * M + m] = sx;
+                if (blockIdx.x == 0) {
+                    if (col < K) *reinterpret_cast<v2i*>(q + (size_t)m * K + col) = c;
+                    if (c8 == 0) sa[kb * M + m] = sx;
+                }
+            }
+        }
+        lds_barrier();
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                // past the last block the weights are zero; rows past M read
+                // the last row, and their results are dropped
+                const int kb = min(wave + u * kGbWaves, nblk - 1), row = min(m * 8 + (r >> 1), M - 1);
+                a[u][m] = *reinterpret_cast<const v4i*>(codes + (row * nblk + kb) * kBlock +
+                                                        ((unit ^ (row & 7)) << 4));
+                s[u][m] = sc[kb * M + row];
+            }
+    }
+
+    int buf = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, buf ^= 1) {
+        v4f acc[MT][RT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < RT; ++n) acc[m][n] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < NB; ++u)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float f = s[u][m] * sb[u];
+#pragma unroll
+                for (int n = 0; n < RT; ++n) {
+                    const v4f p = mfma_pair(w[u][n], a[u][m], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][n][e] = __builtin_fmaf(p[e], f, acc[m][n][e]);
+                }
+                // one block's products at a time where registers are short (the
+                // compiler would hold them all past the request below)
+                if constexpr (kTight) {
+#pragma unroll
+                    for (int n = 0; n < RT; ++n) asm volatile("" : "+v"(acc[m][n]));
+                }
+            }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + (int)gridDim.x < tiles) load_w(t + gridDim.x);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < RT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float own = odd ? acc[m][n][2 * e + 1] : acc[m][n][2 * e];
+                    const float sum = own + quad_xor1(own);
+                    if (!odd) red[buf][wave][m * RT + n][r >> 1][2 * g + e] = sum;
+                }
+        // a buffer is written again two tiles later, behind the next tile's barrier
+        lds_barrier();
+        for (int o = tid; o < MT * RT * 64; o += NT) {
+            const int row = o & 7, n = (o >> 3) % RT, m = (o >> 3) / RT;
+            const int col = (t * RT + n) * 8 + row;
+            if (m >= M || col >= N) continue;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kGbWaves; ++i) sum += red[buf][i][(m >> 3) * RT + n][m & 7][row];
+            y[(size_t)m * N + col] = (uint16_t)f32_to_bf16_bits(sum);
+        }
     }
 }
 
@@ -458,9 +663,82 @@ hipError_t launch_quantize_weight_blocks(const void* w, int dtype, int64_t batch
     return hipGetLastError();
 }
 
+namespace {
+
+// Arguments of the decode products; x is null for codes in q.
+struct DecodeArgs {
+    const void* x;
+    uint8_t* q;
+    float* sa;
+    const uint8_t* qw;
+    const float* sw;
+    uint16_t* y;
+    int M, N, K;
+};
+
+template <int SRC, int MT, int NB, int RT, int XV>
+hipError_t launch_persistent(const DecodeArgs& a, hipStream_t stream)
+{
+    auto kern = gemv_block_persistent_kernel<SRC, MT, NB, RT, XV>;
+    constexpr size_t kRed = (size_t)2 * kGbWaves * MT * RT * 72 * 4;
+    constexpr size_t kMost = kRed + (SRC == SRC_CODES ? 0 : (size_t)XV * kGbWaves * 4 * (kBlock + 4));
+    static_assert(kMost <= 160 * 1024, "LDS of one CU");
+    static std::atomic<uint64_t> attr_devices{0};
+    if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern), kMost, attr_devices);
+        e != hipSuccess)
+        return e;
+    const int64_t tiles = ((int64_t)a.N + 8 * RT - 1) / (8 * RT);
+    const size_t lds = kRed + (SRC == SRC_CODES ? 0 : (size_t)a.M * blocks_of(a.K) * (kBlock + 4));
+    kern<<<(unsigned)std::min<int64_t>(tiles, kCUs), kGbWaves * 64, lds, stream>>>(
+        SRC == SRC_CODES ? a.q : a.x, a.qw, a.sw, a.y, a.q, a.sa, a.M, a.N, a.K);
+    return hipGetLastError();
+}
+
+template <int SRC, int MT, int NB>
+hipError_t launch_nb(const DecodeArgs& a, hipStream_t stream)
+{
+    constexpr int RT = MT * NB > 8 ? 1 : 2;    // 128 VGPRs
+    if constexpr (SRC == SRC_CODES) {
+        return launch_persistent<SRC, MT, NB, RT, 1>(a, stream);
+    } else {
+        const int64_t per = ((int64_t)a.M * blocks_of(a.K) + kGbWaves * 4 - 1) / (kGbWaves * 4);
+        if (per <= 1) return launch_persistent<SRC, MT, NB, RT, 1>(a, stream);
+        if (per <= 2) return launch_persistent<SRC, MT, NB, RT, 2>(a, stream);
+        return launch_persistent<SRC, MT, NB, RT, 4>(a, stream);
+    }
+}
+
+// K blocks that the persistent kernel's largest NB covers.
+constexpr int kPersistentMaxBlocks = 6 * kGbWaves;
+
+template <int SRC, int MT>
+hipError_t launch_src(const DecodeArgs& a, hipStream_t stream)
+{
+    const int64_t nb = (blocks_of(a.K) + kGbWaves - 1) / kGbWaves;
+    if (nb <= 1) return launch_nb<SRC, MT, 1>(a, stream);
+    if (nb <= 2) return launch_nb<SRC, MT, 2>(a, stream);
+    if constexpr (SRC == SRC_CODES || MT == 1) {           // quantized here: M * blocks <= 256
+        if (nb <= 3) return launch_nb<SRC, MT, 3>(a, stream);
+        if (nb <= 4) return launch_nb<SRC, MT, 4>(a, stream);
+        if (nb <= 6) return launch_nb<SRC, MT, 6>(a, stream);
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int SRC>
+hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream)
+{
+    return a.M <= 8 ? launch_src<SRC, 1>(a, stream) : launch_src<SRC, 2>(a, stream);
+}
+
+}  // namespace
+
 hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
                              const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
 {
+    if (blocks_of(K) <= kPersistentMaxBlocks)
+        return launch_decode<SRC_CODES>({nullptr, const_cast<uint8_t*>(qa), const_cast<float*>(sa), qw,
+                                         sw, y, M, N, K}, stream);
     constexpr int RT = 2;
     const int grid = (int)(((int64_t)N + 8 * RT - 1) / (8 * RT));
     if (M <= 8)
@@ -468,6 +746,21 @@ hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* 
     else
         gemv_block_kernel<2, RT><<<grid, kGbWaves * 64, 0, stream>>>(qa, sa, qw, sw, y, M, N, K);
     return hipGetLastError();
+}
+
+bool linear_block_fused_pays(int64_t M, int64_t K)
+{
+    return M <= kGemvBlockMaxM && M * blocks_of(K) <= kFusedBlockMaxCells &&
+           blocks_of(K) <= kPersistentMaxBlocks;
+}
+
+hipError_t launch_linear_block_fused(const void* x, int dtype, const uint8_t* qw, const float* sw,
+                                     uint16_t* y, uint8_t* q, float* sa, int M, int N, int K,
+                                     hipStream_t stream)
+{
+    if (!linear_block_fused_pays(M, K)) return hipErrorInvalidValue;
+    const DecodeArgs a{x, q, sa, qw, sw, y, M, N, K};
+    return dtype == DT_BF16 ? launch_decode<SRC_BF16>(a, stream) : launch_decode<SRC_FP16>(a, stream);
 }
 
 hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* qw,

@@ -303,7 +303,8 @@ def _where(t: torch.Tensor):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError("the arguments must be CUDA (HIP) tensors")
     index = torch.cuda.current_device()
-    return index, torch.cuda.current_stream(index).cuda_stream
+    # torch.cuda.current_stream(index).cuda_stream without building a Stream object
+    return index, torch._C._cuda_getCurrentRawStream(index)
 
 
 def fp8_quantize_blocks(x: torch.Tensor, q: torch.Tensor | None = None,
