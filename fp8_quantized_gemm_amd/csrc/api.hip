@@ -557,6 +557,15 @@ hipError_t dispatch_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
                                : launch_tile_block(qa, sa, qw, sw, y, (int)M, (int)N, (int)K, st);
 }
 
+// The block-scaled kernels count rows and columns of tiles past M and N in 32
+// bits.
+constexpr int64_t kMaxBlockDim = (int64_t)1 << 30;
+fp8q_status check_block_sizes(int64_t M, int64_t N, int64_t K)
+{
+    FP8Q_TRY(check_gemm_sizes(M, N, K));
+    return M > kMaxBlockDim || N > kMaxBlockDim ? FP8Q_ERR_SHAPE : FP8Q_OK;
+}
+
 uint64_t act_scale_bytes(int64_t M, int64_t K) { return 4 * u64(blocks_of(K)) * u64(M); }
 uint64_t weight_scale_bytes(int64_t N, int64_t K) { return 4 * u64(blocks_of(N)) * u64(blocks_of(K)); }
 }  // namespace
@@ -566,7 +575,7 @@ fp8q_status fp8_gemm_blockwise(const uint8_t* qa, const float* sa, const uint8_t
                                fp8q_stream stream)
 {
     if (!qa || !sa || !qw || !sw || !y) return FP8Q_ERR_NULL;
-    FP8Q_TRY(check_gemm_sizes(M, N, K));
+    FP8Q_TRY(check_block_sizes(M, N, K));
     if (!aligned16(qa) || !aligned16(qw) || !aligned16(y) || !aligned4(sa) || !aligned4(sw))
         return FP8Q_ERR_ALIGN;
     FP8Q_TRY(check_apart({{y, u64(M) * u64(N) * 2}},
@@ -583,7 +592,7 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
 {
     if (!x || !qw || !sw || !y || !q || !sa) return FP8Q_ERR_NULL;
     if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
-    FP8Q_TRY(check_gemm_sizes(M, N, K));
+    FP8Q_TRY(check_block_sizes(M, N, K));
     if (!aligned16(x) || !aligned16(qw) || !aligned16(y) || !aligned16(q) || !aligned4(sw) ||
         !aligned4(sa))
         return FP8Q_ERR_ALIGN;

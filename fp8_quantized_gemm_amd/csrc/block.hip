@@ -427,9 +427,9 @@ void gemv_block_persistent_kernel(const void* __restrict__ src, const uint8_t* _
 // The ring-buffered tile GEMM: BM x BN outputs per workgroup, K steps of 128
 // = one block, both operands and the step's activation scales brought to LDS
 // by direct global->LDS loads, AST stages for the activations and their
-// scales, WST >= AST for the weights.  A wave's TN columns lie inside one
-// 128-row weight block (TN divides 128 and tiles start at multiples of BN),
-// so its weight scale is one scalar per step.
+// scales, WST >= AST for the weights.  Tiles start at multiples of BN, so a
+// wave's TN columns lie inside one 128-row weight block where TN divides 128,
+// and 16 of them always do: its weight scales are scalars.
 //
 // Each v_mfma_f32_16x16x128 covers exactly one block.  It starts from a zero
 // accumulator, and its four results are folded into the running sum with the
@@ -445,7 +445,10 @@ void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__
     constexpr int BK = kBlock;
     constexpr int TM = BM / WM, TN = BN / WN;
     constexpr int FM = TM / 16, FN = TN / 16;
-    static_assert(BM % 64 == 0 && 128 % TN == 0, "one weight scale per wave, whole scale loads");
+    static_assert(BM % 64 == 0, "whole scale loads");
+    // weight scales per wave: one where its columns lie in one block, else one
+    // for each 16 of them
+    constexpr int FS = kBlock % TN == 0 ? 1 : FN;
     constexpr int ASTAGE = BM * BK, WSTAGE = BN * BK;
     constexpr int ABPW = BM / 8 / NW, WBPW = BN / 8 / NW;   // 1 KiB DMA blocks per wave per step
     static_assert(ABPW * 8 * NW == BM && WBPW * 8 * NW == BN, "whole DMA blocks per wave");
@@ -455,7 +458,8 @@ void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint8_t* const a_lds = lds;
     uint8_t* const w_lds = lds + AST * ASTAGE;
-    float* const s_lds = reinterpret_cast<float*>(lds + AST * ASTAGE + WST * WSTAGE);  // AST x BM
+    // AST x (BM activation scales, then 64 slots for the weight scales)
+    float* const s_lds = reinterpret_cast<float*>(lds + AST * ASTAGE + WST * WSTAGE);
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -483,20 +487,31 @@ void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__
         const bool kin = kt < nk && kt * BK + du * 16 < K;
         return rowoff + (uint32_t)(kt * BK) + (kin ? 0u : kOOB);
     };
-    // 64 scales per wave and step; with more waves than BM / 64 some load the
-    // same ones, which keeps the wait counts of all waves equal
-    const int srow = (wave % (BM / 64)) * 64;
+    // One load of scales per wave and step: the first BM / 64 waves bring 64
+    // activation scales each, the others (with the same result) the weight
+    // scales of the tile's row blocks, so that all waves wait alike.
+    constexpr int SSTAGE = BM + 64;
+    static_assert(NW > BM / 64, "a wave for the weight scales");
+    const bool act = wave < BM / 64;
+    const int nb0 = n0 >> 7;
+    const int nbs = min((N + kBlock - 1) / kBlock - nb0, (n0 % kBlock + BN + kBlock - 1) / kBlock);
+    const float* s_at = act ? sa + m0 : sw + (size_t)nb0 * nk;     // of the next stage
+    const size_t s_step = act ? (size_t)M : 1;
+    const uint32_t s_bytes = act ? (uint32_t)(rows_m * 4) : (uint32_t)((nbs - 1) * nk + 1) * 4;
+    const int s_slot = act ? wave * 64 : BM;
+    const uint32_t soff = act ? (uint32_t)((wave * 64 + lane) * 4)
+                              : lane < nbs ? (uint32_t)(lane * nk * 4) : kOOB;
     auto dma_a = [&](int kt) {
         const uint32_t off = koff(kt);
         uint8_t* base = a_lds + (kt % AST) * ASTAGE + wave * ABPW * 1024;
 #pragma unroll
         for (int j = 0; j < ABPW; ++j)
             dma_load16(ra, base + j * 1024, (uint32_t)((wave * ABPW + j) * 8 * K) + off);
-        const int ks = min(kt, nk - 1);
-        const rsrc_t rs = make_rsrc(sa + (size_t)ks * M + m0, (uint32_t)(rows_m * 4));
+        const rsrc_t rs = make_rsrc(s_at, s_bytes);
+        s_at += kt < nk - 1 ? s_step : 0;      // stages are requested in order
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (__attribute__((address_space(3))) void*)(s_lds + (kt % AST) * BM + srow), 4,
-            (uint32_t)((srow + lane) * 4), 0, 0, 0);
+            rs, (__attribute__((address_space(3))) void*)(s_lds + (kt % AST) * SSTAGE + s_slot), 4, soff,
+            0, 0, 0);
     };
     auto dma_w = [&](int kt) {
         const uint32_t off = koff(kt);
@@ -505,15 +520,22 @@ void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__
         for (int j = 0; j < WBPW; ++j)
             dma_load16(rw, base + j * 1024, (uint32_t)((wave * WBPW + j) * 8 * K) + off);
     };
-    // a wave whose columns lie past N reads the last row block's scales
-    const int nb_last = (N - 1) >> 7;
-    const float* const swb = sw + (size_t)min((n0 + wn * TN) >> 7, nb_last) * nk;
-
     v4f acc[FM][FN];
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    // The block products of one activation fragment are folded into the sums
+    // between the MFMAs of the next one, those of a step's last fragment in
+    // the next step.
+    static_assert(FM % 2 == 0, "the last fragment's products and the first's lie apart");
+    v4f p[2][FN];
+    float f_last[FS];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) p[1][j] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < FS; ++j) f_last[j] = 0.0f;
 
     // load groups and waits as in gemm_f8_kernel: the group issued after step
     // j holds A(j + AST) (with its scales) then W(j + WST)
@@ -522,58 +544,63 @@ void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__
         if (j + AST >= 0) dma_a(j + AST);
         dma_w(j + WST);
     }
-    float swk = swb[0];
     wait_vm<ALLOW + AL + WBPW>();
+    // nothing of the scalar loads above may be pending in the loop: beside
+    // them, which return out of order, the waits on LDS reads could not count
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __syncthreads();
 
     for (int kt = 0; kt < nk; ++kt) {
         const uint8_t* As = a_lds + (kt % AST) * ASTAGE;
         const uint8_t* Ws = w_lds + (kt % WST) * WSTAGE;
-        const float* Ss = s_lds + (kt % AST) * BM + wm * TM + r;
-        const float swn = swb[min(kt + 1, nk - 1)];
+        const float* Ss = s_lds + (kt % AST) * SSTAGE;
         auto frag = [&](const uint8_t* S, int row) {
             return cat(*reinterpret_cast<const v4i*>(S + swz128(row, g)),
                        *reinterpret_cast<const v4i*>(S + swz128(row, g + 4)));
         };
-        v8i wf[FN];
+        v8i wf[FN], af[2];
+        af[0] = frag(As, wm * TM + r);
 #pragma unroll
         for (int j = 0; j < FN; ++j) wf[j] = frag(Ws, wn * TN + j * 16 + r);
-        v8i af[2];
-        af[0] = frag(As, wm * TM + r);
-        // block products of one activation fragment, folded into the sums
-        // while the next fragment's MFMAs run
-        v4f p[2][FN];
-        float f[2];
-        auto fold = [&](int i) {
+        float sa_k[FM], sw_k[FS];
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+        for (int i = 0; i < FM; ++i) sa_k[i] = Ss[wm * TM + i * 16 + r];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = __builtin_fmaf(p[i & 1][j][e], f[i & 1], acc[i][j][e]);
-            // keep the compiler from moving the sums past the end of the step
-            // (it would hold every block product until then)
+        for (int j = 0; j < FS; ++j) sw_k[j] = Ss[BM + (((n0 & 127) + wn * TN + j * 16) >> 7)];
+        auto fold = [&](int i, int j, float f) {
 #pragma unroll
-            for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(acc[i][j]));
+            for (int e = 0; e < 4; ++e)
+                acc[i][j][e] = __builtin_fmaf(p[i & 1][j][e], f, acc[i][j][e]);
         };
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             if (i + 1 < FM) af[(i + 1) & 1] = frag(As, wm * TM + (i + 1) * 16 + r);
-            f[i & 1] = Ss[i * 16] * swk;
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
+            for (int j = 0; j < FN; ++j) {
                 p[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                     wf[j], af[i & 1], v4f{0.f, 0.f, 0.f, 0.f}, WF_E4M3, WF_E4M3, 0, 0, 0, 0);
-            if (i > 0) fold(i - 1);
+                if (i > 0)
+                    fold(i - 1, j, sa_k[i - 1] * sw_k[FS == 1 ? 0 : j]);
+                else
+                    fold(FM - 1, j, f_last[FS == 1 ? 0 : j]);
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA,
+                __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);          // one fold
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
-        fold(FM - 1);
-        swk = swn;
+#pragma unroll
+        for (int j = 0; j < FS; ++j) f_last[j] = sa_k[FM - 1] * sw_k[j];
         wait_vm<ALLOW>();
         __syncthreads();                       // stage k of both rings is free
         dma_a(kt + AST);
         dma_w(kt + WST);
     }
     wait_vm<0>();                              // nothing left in flight into LDS
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            acc[FM - 1][j][e] = __builtin_fmaf(p[1][j][e], f_last[FS == 1 ? 0 : j], acc[FM - 1][j][e]);
 
     // acc[i][j][e] is output row mb + 16 i + r, column nb + 16 j + 4 g + e
     const int mb = m0 + wm * TM, nb = n0 + wn * TN;
@@ -604,7 +631,7 @@ hipError_t launch_block_tile(const uint8_t* qa, const float* sa, const uint8_t* 
                              uint16_t* y, int M, int N, int K, hipStream_t stream)
 {
     auto kern = gemm_block_kernel<BM, BN, WM, WN, AST, WST>;
-    constexpr size_t lds = ((size_t)AST * BM + (size_t)WST * BN) * 128 + (size_t)AST * BM * 4;
+    constexpr size_t lds = ((size_t)AST * BM + (size_t)WST * BN) * 128 + (size_t)AST * (BM + 64) * 4;
     static_assert(lds <= 160 * 1024, "LDS of one CU");
     static std::atomic<uint64_t> attr_devices{0};
     if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern), lds, attr_devices);

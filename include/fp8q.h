@@ -382,14 +382,15 @@ FP8Q_API fp8q_status nested_linear_fp8_e4m3(const uint16_t* a, const uint8_t* hi
  *   qa[M,K], sa[KB,M] in: activation codes and scales
  *   qw[N,K], sw[NB,KB] in: weight codes and scales
  *   y[M,N]   out: bf16 bit patterns
- *   Size rules as fp8_gemm.  M <= 16 runs the weight-streaming kernel.
+ *   1 <= M, N <= 2^30;  16 <= K <= 2^22 and K % 16 == 0.  M <= 16 runs the
+ *   weight-streaming kernel.
  *
  * fp8_linear_blockwise - fp8_quantize_blocks on the activation, then
  *   fp8_gemm_blockwise on its codes; bit-identical to the two calls made in
  *   sequence:
  *   x[M,K] in : bf16/fp16 activation;  qw[N,K], sw[NB,KB] in
  *   y[M,N] out;  q[M,K], sa[KB,M] out: the activation's codes and scales
- *   Size rules as fp8_gemm.  One launch for M <= 16, M*KB <= 256 and K <=
+ *   Size rules as fp8_gemm_blockwise.  One launch for M <= 16, M*KB <= 256 and K <=
  *   12288 unless y lies over x (which is allowed), else two.
  */
 FP8Q_API fp8q_status fp8_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols,

@@ -46,7 +46,9 @@ A2 = at(4, 2)
     ("fp8_gemm_blockwise", [A, None, C, D, E, 1, 1, 16, None], NULLP),
     ("fp8_gemm_blockwise", [A, B, C, D, E, 0, 1, 16, None], SHAPE),
     ("fp8_gemm_blockwise", [A, B, C, D, E, 1, 1, 40, None], SHAPE),
-    ("fp8_gemm_blockwise", [A, B, C, D, E, 1, 2 ** 31, 16, None], SHAPE),
+    ("fp8_gemm_blockwise", [A, B, C, D, E, 1, 2 ** 30 + 1, 16, None], SHAPE),
+    ("fp8_gemm_blockwise", [A, B, C, D, E, 2 ** 30 + 1, 1, 16, None], SHAPE),
+    ("fp8_linear_blockwise", [A, 0, B, C, D, E, F, 1, 2 ** 30 + 1, 16, None], SHAPE),
     ("fp8_gemm_blockwise", [A, B, C, D, at(4, 8), 1, 1, 16, None], ALIGN),
     ("fp8_gemm_blockwise", [A, A2, C, D, E, 1, 1, 16, None], ALIGN),
     ("fp8_gemm_blockwise", [A, B, C, D, at(0, 256), 2, 16, 256, None], OVERLAP),
