@@ -395,7 +395,6 @@ hipError_t launch_f8(const uint8_t* qa, const float* sa, const uint8_t* qw, cons
 // weights cold in HBM, medians over the Llama-7B / Qwen-32B prefill shapes.
 // 64 x 64 appears twice: a grid of at most one workgroup per CU finishes its
 // round much sooner than a full one.
-struct TileShape { int bm, bn, per_cu; float round_us; };
 constexpr TileShape kTileShapes[] = {
     {256, 256, 1, 55.8f},   // 8 waves of 128 x 64, 2 + 2 stages (128 KiB)
     {256, 192, 1, 45.3f},   // 8 waves of 128 x 48, 2 + 3 stages (136 KiB)
@@ -406,24 +405,6 @@ constexpr TileShape kTileShapes[] = {
     { 64,  64, 2, 17.0f},   // 4 waves of  32 x 32, 4 + 4 stages ( 64 KiB)
     { 64,  64, 1, 10.2f},   // the same kernel, one workgroup per CU
 };
-
-// The shape of `shapes` whose rounds of workgroups cost least; tiles may not
-// be taller than M rounded up to 64 rows.
-inline int pick_tile_shape(const TileShape* shapes, int count, int M, int N)
-{
-    const int64_t mcap = ((int64_t)M + 63) / 64 * 64;
-    int best = -1;
-    float best_us = 0.f;
-    for (int i = 0; i < count; ++i) {
-        const TileShape& t = shapes[i];
-        if (t.bm > mcap) continue;
-        const int64_t tiles = (((int64_t)M + t.bm - 1) / t.bm) * (((int64_t)N + t.bn - 1) / t.bn);
-        const int64_t slots = (int64_t)kCUs * t.per_cu;
-        const float us = (float)((tiles + slots - 1) / slots) * t.round_us;
-        if (best < 0 || us < best_us) { best = i; best_us = us; }
-    }
-    return best;
-}
 
 template <int WFMT, int OUTF>
 hipError_t launch_tile_fmt(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,

@@ -1,5 +1,6 @@
-// Device helpers shared by the LDS-tiled GEMMs: operand halves, the
-// workgroup -> tile mapping, LDS swizzles and the wait on direct-to-LDS loads.
+// Helpers shared by the LDS-tiled GEMMs: operand halves, the workgroup ->
+// tile mapping, LDS swizzles, the wait on direct-to-LDS loads and the choice of
+// a tile shape.
 #pragma once
 
 #include "common.hpp"
@@ -36,6 +37,28 @@ __device__ __forceinline__ void wait_vm()
     // s_waitcnt vmcnt(N) with expcnt and lgkmcnt left at their maxima (gfx9 encoding)
     static_assert(N_OUTSTANDING >= 0 && N_OUTSTANDING < 64, "vmcnt range");
     __builtin_amdgcn_s_waitcnt((N_OUTSTANDING & 15) | ((N_OUTSTANDING >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+// A tile shape, how many of its workgroups a CU holds, and the time of one
+// round of them.
+struct TileShape { int bm, bn, per_cu; float round_us; };
+
+// The shape of `shapes` whose rounds of workgroups cost least; tiles may not
+// be taller than M rounded up to 64 rows.
+inline int pick_tile_shape(const TileShape* shapes, int count, int M, int N)
+{
+    const int64_t mcap = ((int64_t)M + 63) / 64 * 64;
+    int best = -1;
+    float best_us = 0.f;
+    for (int i = 0; i < count; ++i) {
+        const TileShape& t = shapes[i];
+        if (t.bm > mcap) continue;
+        const int64_t tiles = (((int64_t)M + t.bm - 1) / t.bm) * (((int64_t)N + t.bn - 1) / t.bn);
+        const int64_t slots = (int64_t)kCUs * t.per_cu;
+        const float us = (float)((tiles + slots - 1) / slots) * t.round_us;
+        if (best < 0 || us < best_us) { best = i; best_us = us; }
+    }
+    return best;
 }
 
 }  // namespace fp8q
