@@ -615,7 +615,7 @@ int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k)
 {
     if (T < 1 || T > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || I < 16 || I > kMoeMaxDim)
         return 0;
-    return kMoeRoutingBytes + T * top_k * blocks_of(I) * kBlock * 2;
+    return moe_work_bytes(T, I, top_k);
 }
 
 fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits, const uint8_t* w13,

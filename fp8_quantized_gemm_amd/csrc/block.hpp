@@ -39,7 +39,6 @@ constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
 constexpr int64_t kMoeMaxDim = 1 << 16;  // H and I
-constexpr int kMoeRoutingBytes = 8192;   // head of the workspace; the activations h follow
 struct MoeArgs {
     const void* x;           // [T, H]
     const float* logits;     // [T, E]
@@ -50,9 +49,10 @@ struct MoeArgs {
     uint16_t* y;             // [T, H]
     int* ids;                // [T, top_k]
     float* weights;          // [T, top_k]
-    void* work;              // routing, then h[T * top_k, whole blocks of I] bf16
+    void* work;              // moe_work_bytes
     int T, H, I, E, top_k, renormalize;
 };
+int64_t moe_work_bytes(int64_t T, int64_t I, int64_t top_k);
 hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t stream);
 
 }  // namespace fp8q

@@ -83,6 +83,15 @@ __device__ __forceinline__ v4f block_product(const v4i& w, const v4i& x0, const 
     return Half<DT>::mfma(Half<DT>::widen(w[2], w[3]), x1, p);
 }
 
+// The same of E4M3 rows and E5M2 tokens.
+__device__ __forceinline__ v4f rest_product(const v4i& w, const v4i& x)
+{
+    const long w0 = __builtin_bit_cast(long, v2i{w[0], w[1]}), w1 = __builtin_bit_cast(long, v2i{w[2], w[3]});
+    const long x0 = __builtin_bit_cast(long, v2i{x[0], x[1]}), x1 = __builtin_bit_cast(long, v2i{x[2], x[3]});
+    const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_fp8_bf8(w0, x0, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_bf8(w1, x1, p, 0, 0, 0);
+}
+
 // ---------------------------------------------------------------- selection
 // One wave, one token: the top_k largest logits, ties to the lower index.
 // -inf switches an expert off; a NaN logit counts as -inf.  Lane j returns
@@ -285,6 +294,22 @@ __device__ __forceinline__ int h_position(int i)
 {
     return (i & ~127) | (i & 8) << 3 | (i >> 4 & 7) << 3 | (i & 7);
 }
+// Up to kRestTokens tokens the part of h that its bf16 rounding leaves out is
+// kept too, as an E5M2 code of 2^12 times it, in rows with the columns in
+// order: with bf16 alone the error of y is 1.4 times that of its own rounding
+// (bf16's 2^-8 twice), with it about that of its own rounding.  E5M2 holds
+// 2^12 rest for |h| from 2^-19 to 2^11; outside h has bf16's precision.  Above,
+// the second kernel is bound by its loads of h, and one of three more costs
+// too much.
+constexpr int kRestTokens = 8;
+constexpr float kRestScale = 0x1p12f;
+__device__ __forceinline__ uint8_t h_rest_code(float h, uint32_t bits)
+{
+    const float d = (h - bf16_bits_to_f32(bits)) * kRestScale;
+    // inf - inf, and what E5M2 would round to infinity
+    return (uint8_t)__builtin_amdgcn_cvt_pk_bf8_f32(fabsf(d) <= 57344.0f ? d : 0.0f, 0.0f, 0, false);
+}
+
 __device__ __forceinline__ int h_stride(int I) { return (I + kBlock - 1) / kBlock * kBlock; }
 
 // ---------------------------------------------------------------- selection, a kernel of its own
@@ -327,8 +352,8 @@ void moe_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits,
     const uint8_t* __restrict__ w13, const float* __restrict__ s13, int* __restrict__ ids_io,
     float* __restrict__ weights_io, uint64_t* __restrict__ masks_out,
-    float* __restrict__ pair_weights, uint16_t* __restrict__ h, int T, int H, int I, int E,
-    int top_k, int renormalize)
+    float* __restrict__ pair_weights, uint16_t* __restrict__ h, uint8_t* __restrict__ h_rest, int T,
+    int H, int I, int E, int top_k, int renormalize)
 {
     typedef Layout<R> L;
     constexpr int KL = L::kBlocks * kBlock;                // K per load
@@ -468,11 +493,19 @@ void moe_up_kernel(
                     if (at.owner && p < tokens.count) {
                         uint16_t* const dst = h + (size_t)(first + p) * h_stride(I) +
                                               h_position(i0 + n * R + at.out_row);
-                        // bf16 has fp32's range (fp16 would overflow); its rounding, 2^-8, is that of y
+                        float hv[L::kOut];
                         uint32_t bits[L::kOut];
 #pragma unroll
-                        for (int q = 0; q < L::kOut; ++q)
-                            bits[q] = f32_to_bf16_bits(gv[q] / (1.0f + expf(-gv[q])) * uv[q]);
+                        for (int q = 0; q < L::kOut; ++q) {
+                            hv[q] = gv[q] / (1.0f + expf(-gv[q])) * uv[q];
+                            bits[q] = f32_to_bf16_bits(hv[q]);
+                        }
+                        if (h_rest != nullptr) {
+                            uint8_t* const rest = h_rest + (size_t)(first + p) * h_stride(I) + i0 + n * R +
+                                                  at.out_row;
+#pragma unroll
+                            for (int q = 0; q < L::kOut; ++q) rest[q] = h_rest_code(hv[q], bits[q]);
+                        }
                         if constexpr (L::kOut == 2)
                             *reinterpret_cast<uint32_t*>(dst) = bits[0] | bits[1] << 16;
                         else
@@ -492,9 +525,10 @@ void moe_up_kernel(
 // sums are added in a fixed order at the end.
 constexpr int kDownRows = 8;                // columns of y (rows of W2) per row tile
 
-template <int PER, int RT, int BLOCKS, int CP>
+template <int PER, int RT, int BLOCKS, bool REST, int CP>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
-    const uint16_t* __restrict__ h, const uint8_t* __restrict__ w2, const float* __restrict__ s2,
+    const uint16_t* __restrict__ h, const uint8_t* __restrict__ h_rest,
+    const uint8_t* __restrict__ w2, const float* __restrict__ s2,
     const uint64_t* __restrict__ masks_in, const float* __restrict__ pair_weights,
     uint16_t* __restrict__ y, int T, int H, int I, int E, int top_k)
 {
@@ -519,21 +553,26 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const int chunks = (nblk + BLOCKS - 1) / BLOCKS;
     const int items = active.count * chunks;
     const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * h_stride(I) * 2));
+    const rsrc_t rr = make_rsrc(h_rest, (uint32_t)(T * top_k * h_stride(I)));
     float* const mine = ysum + wave * T * COLS;
 
-    // rows of h of pair p (none: zeros) in the K blocks from kb0
-    auto load_h = [&](v4i (&hv)[BLOCKS][2], int p, bool none, int kb0) {
+    // rows of h of pair p (none: zeros) in the K blocks from kb0: two operands
+    // of bf16 and, with REST, one of E5M2
+    constexpr int HV = REST ? 3 : 2;
+    auto load_h = [&](v4i (&hv)[BLOCKS][HV], int p, bool none, int kb0) {
 #pragma unroll
         for (int c = 0; c < BLOCKS; ++c) {
             const int kb = (kb0 + c) * kBlock;
-            const uint32_t o = none || kb + at.koff >= I
-                                   ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2;
+            const bool out = none || kb + at.koff >= I;
+            const uint32_t o = out ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2;
             hv[c][0] = buf_load16(rh, o);
             hv[c][1] = buf_load16(rh, o + 128);
+            if constexpr (REST)
+                hv[c][2] = buf_load16(rr, out ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff));
         }
     };
     struct Stage {
-        v4i w[BLOCKS][RT], h[BLOCKS][2];
+        v4i w[BLOCKS][RT], h[BLOCKS][HV];
         float s[BLOCKS];
         int kb0, first;
         Tokens tokens;
@@ -574,7 +613,12 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
                 v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < BLOCKS; ++c) {
-                    const v4f q = block_product<DT_BF16>(st.w[c][n], st.h[c][0], st.h[c][1]);
+                    v4f q = block_product<DT_BF16>(st.w[c][n], st.h[c][0], st.h[c][1]);
+                    if constexpr (REST) {
+                        const v4f d = rest_product(st.w[c][n], st.h[c][2]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) q[i] = __builtin_fmaf(d[i], 1.0f / kRestScale, q[i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c], acc[i]);
                 }
@@ -612,37 +656,50 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     }
 }
 
-// The workspace: the experts' token masks, the grouped weights, h.
+// The workspace: the experts' token masks, the weights grouped like h, h, and
+// up to kRestTokens tokens what its rounding left out.
 struct MoeWork {
+    static constexpr int64_t kWeightsAt = kMoeMaxExperts * 8, kHAt = kWeightsAt + kMaxPairs * 4;
+    static int64_t h_bytes(int64_t T, int64_t I, int64_t top_k)
+    {
+        return T * top_k * blocks_of(I) * kBlock * 2;
+    }
+    static int64_t bytes(int64_t T, int64_t I, int64_t top_k)
+    {
+        return kHAt + h_bytes(T, I, top_k) + (T <= kRestTokens ? h_bytes(T, I, top_k) / 2 : 0);
+    }
     uint64_t* masks;
     float* weights;
     uint16_t* h;
-    explicit MoeWork(void* p)
-        : masks(static_cast<uint64_t*>(p)),
-          weights(reinterpret_cast<float*>(static_cast<char*>(p) + kMoeMaxExperts * 8)),
-          h(reinterpret_cast<uint16_t*>(static_cast<char*>(p) + kMoeRoutingBytes))
+    uint8_t* h_rest;
+    explicit MoeWork(const MoeArgs& a)
     {
+        char* const p = static_cast<char*>(a.work);
+        masks = reinterpret_cast<uint64_t*>(p);
+        weights = reinterpret_cast<float*>(p + kWeightsAt);
+        h = reinterpret_cast<uint16_t*>(p + kHAt);
+        h_rest = a.T <= kRestTokens
+                     ? reinterpret_cast<uint8_t*>(p + kHAt + h_bytes(a.T, a.I, a.top_k)) : nullptr;
     }
 };
-static_assert(kMoeMaxExperts * 8 + kMaxPairs * 4 <= kMoeRoutingBytes, "head of the workspace");
 
 template <int DT, int PER, int R, int RT, int MT, int UB, int WAVES, int OCC, bool ROUTED>
 hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
 {
-    const MoeWork work(a.work);
+    const MoeWork work(a);
     const int64_t items = std::min<int64_t>(a.E, (int64_t)a.T * a.top_k) * (a.I / (R * RT));
     const int grid = (int)std::min<int64_t>(items, kCUs * OCC * 4 / WAVES);
     moe_up_kernel<DT, PER, R, RT, MT, UB, WAVES, OCC, ROUTED><<<grid, WAVES * 64, 0, stream>>>(
         static_cast<const uint16_t*>(a.x), a.logits, a.w13, a.s13, a.ids, a.weights, work.masks,
-        work.weights, work.h, a.T, a.H, a.I, a.E, a.top_k, a.renormalize);
+        work.weights, work.h, work.h_rest, a.T, a.H, a.I, a.E, a.top_k, a.renormalize);
     return hipGetLastError();
 }
 
-template <int PER, int RT, int BLOCKS, int CP>
+template <int PER, int RT, int BLOCKS, bool REST, int CP>
 hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
 {
     constexpr int COLS = RT * kDownRows;
-    auto kern = moe_down_kernel<PER, RT, BLOCKS, CP>;
+    auto kern = moe_down_kernel<PER, RT, BLOCKS, REST, CP>;
     const size_t lds = (size_t)kMoeWaves * a.T * COLS * sizeof(float);
     static std::atomic<uint64_t> attr_devices{0};
     if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern),
@@ -650,18 +707,21 @@ hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
                                                 attr_devices);
         e != hipSuccess)
         return e;
-    const MoeWork work(a.work);
-    kern<<<(a.H + COLS - 1) / COLS, kMoeThreads, lds, stream>>>(work.h, a.w2, a.s2, work.masks,
-                                                                work.weights, a.y, a.T, a.H, a.I,
-                                                                a.E, a.top_k);
+    const MoeWork work(a);
+    kern<<<(a.H + COLS - 1) / COLS, kMoeThreads, lds, stream>>>(work.h, work.h_rest, a.w2, a.s2,
+                                                                work.masks, work.weights, a.y, a.T,
+                                                                a.H, a.I, a.E, a.top_k);
     return hipGetLastError();
 }
 
-template <int PER, int RT, int BLOCKS>
+// Non-temporal weight loads where rows of W2 are whole 128-byte lines; else a
+// line is shared by two rows and has to stay for the second (H x I = 4096 x
+// 1392, 13 tokens: 35.5 against 32.4 us).
+template <int PER, int RT, int BLOCKS, bool REST>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
-    return a.I % kBlock == 0 ? launch_down_cp<PER, RT, BLOCKS, CP_NT>(a, stream)
-                             : launch_down_cp<PER, RT, BLOCKS, CP_DEFAULT>(a, stream);
+    return a.I % kBlock == 0 ? launch_down_cp<PER, RT, BLOCKS, REST, CP_NT>(a, stream)
+                             : launch_down_cp<PER, RT, BLOCKS, REST, CP_DEFAULT>(a, stream);
 }
 
 // Above this many tokens the selection is a kernel of its own.
@@ -684,7 +744,11 @@ hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
             e = launch_up<DT, PER, 8, 2, 2, 1, 16, 4, true>(a, stream);
     }
     if (e != hipSuccess) return e;
-    return a.H < 16 * kCUs ? launch_down<PER, 1, 3>(a, stream) : launch_down<PER, 2, 2>(a, stream);
+    if (a.T <= kRestTokens) return launch_down<PER, 1, 2, true>(a, stream);
+    // two row tiles share the loads of h where that leaves a workgroup per CU
+    // (4096 x 1392, 13 tokens: 32.8 -> 27.2 us)
+    return a.H < 16 * kCUs ? launch_down<PER, 1, 3, false>(a, stream)
+                           : launch_down<PER, 2, 2, false>(a, stream);
 }
 
 template <int DT>
@@ -697,6 +761,8 @@ hipError_t launch_moe_dt(const MoeArgs& a, hipStream_t stream)
 }
 
 }  // namespace
+
+int64_t moe_work_bytes(int64_t T, int64_t I, int64_t top_k) { return MoeWork::bytes(T, I, top_k); }
 
 hipError_t launch_moe(const MoeArgs& a, int dtype, hipStream_t stream)
 {
