@@ -536,7 +536,8 @@ fp8q_status fp8_quantize_weight_blocks(const void* w, int dtype, int64_t batch, 
     if (!w || !q || !scale) return FP8Q_ERR_NULL;
     if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
     if (batch < 1 || rows < 1 || rows > kMaxDim || cols < 16 || (cols % 16) != 0 || cols > kMaxK ||
-        rows > ((int64_t)1 << 40) / cols || batch > ((int64_t)1 << 40) / (rows * cols))
+        rows > ((int64_t)1 << 40) / cols || batch > ((int64_t)1 << 40) / (rows * cols) ||
+        batch > kMaxDim / (blocks_of(rows) * blocks_of(cols)))
         return FP8Q_ERR_SHAPE;
     if (!aligned16(w) || !aligned16(q) || !aligned4(scale)) return FP8Q_ERR_ALIGN;
     const uint64_t n = u64(batch) * u64(rows) * u64(cols);

@@ -40,6 +40,8 @@ A2 = at(4, 2)
     ("fp8_quantize_weight_blocks", [A, 0, 1, 0, 16, B, C, None], SHAPE),
     ("fp8_quantize_weight_blocks", [A, 0, 1, 1, 8, B, C, None], SHAPE),
     ("fp8_quantize_weight_blocks", [A, 0, 2 ** 40, 1, 16, B, C, None], SHAPE),
+    ("fp8_quantize_weight_blocks", [A, 0, 2 ** 31, 1, 16, B, C, None], SHAPE),
+    ("fp8_quantize_weight_blocks", [A, 0, 2 ** 30, 1, 256, B, C, None], SHAPE),
     ("fp8_quantize_weight_blocks", [A, 0, 1, 1, 16, at(1, 8), C, None], ALIGN),
     ("fp8_quantize_weight_blocks", [A, 0, 2, 130, 128, B, at(1, 2 * 130 * 128 - 4), None], OVERLAP),
     # fp8_gemm_blockwise(qa, sa, qw, sw, y, M, N, K)

@@ -99,7 +99,7 @@ def _gemm(qa, sa, qw, sw):
     return out[:M * N].reshape(M, N)
 
 
-SHAPES = [(1, 1, 16), (1, 37, 160), (1, 300, 4096), (2, 129, 272), (7, 1000, 1040), (8, 16, 128),
+SHAPES = [(1, 1, 16), (1, 37, 160), (8, 100, 12304), (16, 40, 16400), (12, 8200, 2064), (5, 33, 8192), (1, 300, 4096), (2, 129, 272), (7, 1000, 1040), (8, 16, 128),
           (9, 257, 144), (15, 515, 11008), (16, 640, 4096), (17, 64, 272), (33, 129, 112),
           (64, 1, 16), (65, 200, 1040), (129, 257, 4096), (300, 515, 272), (513, 300, 528),
           (700, 1028, 1296)]
@@ -133,6 +133,25 @@ def test_random_within_bound(M, N, K):
     assert np.all(off <= 0), f"{(off > 0).sum()} outside, worst by {off.max()}"
 
 
+# one size for each tile shape of the larger products (128 x 64, 128 x 128, 64 x 64 twice per
+# CU, 128 x 192, 128 x 256, 256 x 192, 256 x 256), with ragged edges in M, N and K
+@pytest.mark.parametrize("M,N,K", [(257, 4100, 272), (333, 6100, 272), (64, 16400, 272),
+                                   (500, 8200, 400), (1100, 6100, 272), (1000, 8200, 272),
+                                   (1100, 10000, 272)])
+def test_each_tile_shape_within_bound(M, N, K):
+    x = synth.activation(M, K, seed=synth.seed_for("tx", M, N, K), outliers=True)
+    w = synth.normal((N, K), 0.02, "fp16", seed=synth.seed_for("tw", M, N, K), device=DEV)
+    qa, sa = ref.quantize_blocks(synth.bits(x), oracle.BF16)
+    qw, sw = (host(t) for t in fp8q.fp8_quantize_weight_blocks(w))
+    say("blockwise tile", M, N, K)
+    y = oracle.bf16_decode(_gemm(qa, sa, qw, sw)).astype(np.float64).reshape(M, N)
+    rng = np.random.Generator(np.random.PCG64(M + N))
+    cols = np.unique(np.concatenate([rng.integers(0, N, 400), np.arange(N - 300, N)]))
+    want, ab = ref.gemm(qa, sa, qw, sw, cols)
+    off = np.abs(y[:, cols] - want) - ref.gemm_tolerance(want, ab, K)
+    assert np.all(off <= 0), f"{(off > 0).sum()} outside, worst by {off.max()}"
+
+
 # ------------------------------------------------------------------ linear
 LINEAR = [(1, 4096, 4096), (1, 37, 160), (3, 515, 1040), (8, 2048, 4096), (11, 300, 5120),
           (16, 4100, 2064), (17, 257, 272), (200, 640, 4096), (600, 515, 1040)]
@@ -157,6 +176,19 @@ def test_linear_equals_quantize_and_gemm(M, N, K, dtype):
     _same_bits(q, want_q)
     _same_bits(s, want_s)
     assert torch.equal(y.view(torch.int16), y0.view(torch.int16))
+
+
+def test_linear_infinite_and_nan_activations_stay_in_their_row():
+    """A row with an infinity or a NaN is outside the contract; the others are as without it."""
+    M, N, K = 6, 300, 1040
+    x, qw, sw = _linear_inputs(M, N, K, "bf16")
+    want = fp8q.fp8_linear_blockwise(x, qw, sw)[0].clone()
+    x[1, 17] = float("inf")
+    x[4, 1030] = float("nan")
+    say("linear_blockwise inf / nan rows")
+    y = fp8q.fp8_linear_blockwise(x, qw, sw)[0]
+    keep = [0, 2, 3, 5]
+    assert torch.equal(y[keep], want[keep])
 
 
 @pytest.mark.parametrize("M,K", [(1, 4096), (5, 1040), (40, 512)])
