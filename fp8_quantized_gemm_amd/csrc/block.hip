@@ -725,10 +725,9 @@ hipError_t launch_persistent(const DecodeArgs& a, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int SRC, int MT, int NB>
-hipError_t launch_nb(const DecodeArgs& a, hipStream_t stream)
+template <int SRC, int MT, int NB, int RT>
+hipError_t launch_rt(const DecodeArgs& a, hipStream_t stream)
 {
-    constexpr int RT = MT * NB > 8 ? 1 : 2;    // 128 VGPRs
     if constexpr (SRC == SRC_CODES) {
         return launch_persistent<SRC, MT, NB, RT, 1>(a, stream);
     } else {
@@ -737,6 +736,24 @@ hipError_t launch_nb(const DecodeArgs& a, hipStream_t stream)
         if (per <= 2) return launch_persistent<SRC, MT, NB, RT, 2>(a, stream);
         return launch_persistent<SRC, MT, NB, RT, 4>(a, stream);
     }
+}
+
+template <int SRC, int MT, int NB>
+hipError_t launch_nb(const DecodeArgs& a, hipStream_t stream)
+{
+    // Tiles of 16 rows, two row tiles that share the activation operands,
+    // where registers allow; of 8 rows where that leaves the busiest CU at
+    // least a tenth fewer rows (5120 x 8192, M = 1 and 16: 10.4 -> 9.5 and 12.1
+    // -> 10.4 us; 22016 x 4096, 88 against 96 rows, M = 16: 18.2 against 18.8).
+    constexpr int RT = MT * NB > 8 ? 1 : 2;    // 128 VGPRs
+    if constexpr (RT == 2) {
+        auto busiest = [&](int64_t rows) {
+            const int64_t tiles = (a.N + rows - 1) / rows;
+            return (tiles + kCUs - 1) / kCUs * rows;
+        };
+        if (busiest(8) * 10 <= busiest(16) * 9) return launch_rt<SRC, MT, NB, 1>(a, stream);
+    }
+    return launch_rt<SRC, MT, NB, RT>(a, stream);
 }
 
 // K blocks that the persistent kernel's largest NB covers.

@@ -120,7 +120,13 @@ def test_small_integers_bit_exact(M, N, K):
     assert np.array_equal(y, oracle.bf16_encode(want.astype(np.float32)).reshape(M, N))
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES)
+# tiles of 16 rows of the decode kernel (N just below 4096), each number of K blocks per wave,
+# one and two groups of tokens
+DECODE = [(1, 4090, 1040), (3, 4094, 2064), (2, 4090, 6000), (8, 4096, 8192), (6, 4090, 11008),
+          (16, 4090, 2048), (9, 4091, 4096), (11, 4090, 8192), (13, 4090, 12288), (1, 4090, 12304)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES + DECODE)
 def test_random_within_bound(M, N, K):
     x = synth.activation(M, K, seed=synth.seed_for("bx", M, N, K), outliers=True)
     w = synth.normal((N, K), 0.02, "fp16", seed=synth.seed_for("bw", M, N, K))
@@ -153,7 +159,7 @@ def test_each_tile_shape_within_bound(M, N, K):
 
 
 # ------------------------------------------------------------------ linear
-LINEAR = [(1, 4096, 4096), (1, 37, 160), (3, 515, 1040), (8, 2048, 4096), (11, 300, 5120),
+LINEAR = [(1, 4096, 4096), (1, 4090, 11008), (2, 4090, 8192), (4, 4090, 6000), (1, 37, 160), (3, 515, 1040), (8, 2048, 4096), (11, 300, 5120),
           (16, 4100, 2064), (17, 257, 272), (200, 640, 4096), (600, 515, 1040)]
 
 
