@@ -1,5 +1,5 @@
 // A mixture-of-experts layer for a few tokens on block-scaled FP8 weights, in
-// two kernels.
+// two kernels up to 16 tokens and three above.
 //
 //   ids[t, j], weights[t, j]: the top_k experts of token t by logit and their
 //     softmax weights;
@@ -12,10 +12,11 @@
 // need no quantization pass between the two products.
 //
 // The first kernel (moe_up) repeats the selection in every workgroup: T * E
-// logits are a few KiB, and a launch of its own would cost more.  It then
-// deals (expert, 16 columns of h) items out to the workgroups.  The second
-// (moe_down) gives each workgroup eight columns of y and all chosen experts,
-// so the weighted sum over experts needs no atomics and no third kernel.
+// logits are a few KiB, and up to kRouteInline tokens a launch of its own
+// (moe_route_kernel) would cost more.  It then deals items, some columns of
+// one expert's h, out to the waves.  The second (moe_down) gives each
+// workgroup 8 or 16 columns of y and all chosen experts, so the weighted sum
+// over experts needs no atomics and no kernel of its own.
 //
 // Both stream weight rows through the MFMA operand layout of Layout, a wave
 // at a time, without any exchange between lanes or waves.
@@ -724,9 +725,26 @@ hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
                              : launch_down_cp<PER, RT, BLOCKS, REST, CP_DEFAULT>(a, stream);
 }
 
-// Above this many tokens the selection is a kernel of its own.
+// Above this many tokens the selection is a kernel of its own: repeating it in
+// every workgroup grows with T, its launch does not (32 tokens, 6 of 64
+// experts, 2048 x 1408: 101 us repeated, 94 us with the kernel; 16 tokens, 4
+// of 32, 4096 x 1392: 92.5 repeated, 101 with it).
 constexpr int kRouteInline = 16;
 
+// moe_up's items.  A wave holds R tokens' columns of R weight rows at once, RT
+// such row tiles and MT token tiles (Layout: smaller R means longer runs of K).
+//   R = 4 up to four tokens (1 token, 6 of 64, 2048 x 1408: 19.0 us a call,
+//     19.7 with 8; 4 of 32, 4096 x 1392: 24.5 against 26.7).
+//   Two row tiles share the loads of x wherever that leaves an item for every
+//     wave (64 tokens, 6 of 64: 109.7 against 117.9 with one); with fewer
+//     items the second tile idles waves (24 tokens, 4 of 32, 4096 x 1392: 114
+//     against 102; 32 tokens, 2 of 8, 4096 x 1408: 51.1 against 39.7).
+//   Two token tiles, which read an expert's rows once for 16 tokens, where an
+//     expert has on average more than 3 tokens (one row tile: 4), so that many
+//     have more than 8 (64 tokens, 6 of 64: 122 -> 109.7; 8 of 128, 2048 x
+//     768: 115 -> 111; with 2 tokens each, 32 of 8 of 128: 94.2 -> 95.2; one
+//     row tile, 48 of 4 of 32: 130 -> 123, 24: 102 -> 108).
+// UB, the K steps in flight, is what 128 registers hold.
 template <int DT, int PER>
 hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
 {
@@ -738,10 +756,18 @@ hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
     } else {
         moe_route_kernel<PER><<<a.T, 64, 0, stream>>>(a.logits, a.ids, a.weights, a.E, a.top_k,
                                                      a.renormalize);
-        if (a.T * a.top_k <= 6 * a.E)
-            e = launch_up<DT, PER, 8, 2, 1, 2, 16, 4, true>(a, stream);
-        else
-            e = launch_up<DT, PER, 8, 2, 2, 1, 16, 4, true>(a, stream);
+        const int pairs = a.T * a.top_k;
+        if ((int64_t)std::min(a.E, pairs) * (a.I / 16) < kCUs * kMoeWaves) {
+            if (pairs <= 4 * a.E)
+                e = launch_up<DT, PER, 8, 1, 1, 4, 16, 4, true>(a, stream);
+            else
+                e = launch_up<DT, PER, 8, 1, 2, 2, 16, 4, true>(a, stream);
+        } else {
+            if (pairs <= 3 * a.E)
+                e = launch_up<DT, PER, 8, 2, 1, 2, 16, 4, true>(a, stream);
+            else
+                e = launch_up<DT, PER, 8, 2, 2, 1, 16, 4, true>(a, stream);
+        }
     }
     if (e != hipSuccess) return e;
     if (a.T <= kRestTokens) return launch_down<PER, 1, 2, true>(a, stream);

@@ -60,6 +60,17 @@ def test_layer_within_bound(T, E, H, I, top_k, dtype, renormalize):
     _check(*_inputs(T, E, H, I, dtype), top_k, renormalize)
 
 
+# Enough (expert, columns) items for two row tiles each: few tokens an expert and many.
+@pytest.mark.parametrize("T,E,H,I,top_k,dtype", [
+    (20, 128, 144, 528, 8, "bf16"),
+    (64, 128, 144, 528, 8, "fp16"),
+    (64, 40, 272, 1680, 3, "bf16"),
+])
+def test_layer_with_many_items(T, E, H, I, top_k, dtype):
+    say("moe many items", T, E, H, I, top_k, dtype)
+    _check(*_inputs(T, E, H, I, dtype), top_k, True)
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_masked_and_tied_logits(renormalize):
     T, E, H, I, top_k = 12, 70, 144, 144, 6
