@@ -614,7 +614,8 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
 
 int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k)
 {
-    if (T < 1 || T > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || I < 16 || I > kMoeMaxDim)
+    if (T < 1 || T > kMoeMaxTokens || top_k < 1 || top_k > kMoeMaxTopK || I < 16 ||
+        I > kMoeMaxDim || (I % 16) != 0)
         return 0;
     return moe_work_bytes(T, I, top_k);
 }

@@ -423,7 +423,8 @@ def fp8_moe_blockwise(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor,
         weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     need = lib.fp8_moe_blockwise_work_bytes(T, I, top_k)
     if work is None:
-        work = torch.empty(need, dtype=torch.uint8, device=dev)
+        # never empty: sizes that need is 0 for are refused below, as sizes
+        work = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif work.numel() < need:
         raise ValueError(f"work must hold at least {need} bytes, got {work.numel()}")
     index, stream = _where(x)

@@ -415,7 +415,9 @@ FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_
  *
  *   y[t] = bf16( sum_j weights[t,j] * W2[e] h[t,j] ),  e = ids[t,j],
  *   h[t,j] = bf16( silu(Wg[e] x[t]) * (Wu[e] x[t]) ),
- *   with fp32 accumulation; the activations are not quantized.
+ *   with fp32 accumulation; the activations are not quantized.  Up to 8 tokens
+ *   what the rounding of h leaves out is kept as well, so that the rounding of
+ *   y is the error that remains (for |h| from 2^-19 to 2^11).
  *
  *   x[T,H]      in : bf16/fp16 activations (dtype as for fp8_quantize_act)
  *   logits[T,E] in : fp32 router logits.  -inf switches an expert off for a
@@ -436,7 +438,8 @@ FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_
  *                    of no meaning.  Calls that may run at the same time need
  *                    one each.
  *   1 <= T <= 64;  16 <= H, I <= 65536, multiples of 16;  1 <= E <= 512;
- *   1 <= top_k <= min(E, 16).  Two launches.
+ *   1 <= top_k <= min(E, 16).  Two launches, three above 16 tokens.
+ *   fp8_moe_blockwise_work_bytes gives 0 for sizes that the call refuses.
  */
 FP8Q_API int64_t fp8_moe_blockwise_work_bytes(int64_t T, int64_t I, int64_t top_k);
 FP8Q_API fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits,

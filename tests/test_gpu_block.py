@@ -232,3 +232,40 @@ def test_linear_on_another_stream_and_in_a_graph(M, N, K):
         for o, w in zip(outs, want):
             assert torch.equal(o.view(torch.uint8), w.view(torch.uint8)), f"replay {rep}"
     del g
+
+
+@pytest.mark.parametrize("M", [1, 16, 40])
+def test_weights_past_32_bits(M):
+    """The last rows of a weight of more than 2^32 bytes, against the same rows alone."""
+    K, tail = 4112, 512
+    N = (1 << 20) + tail
+    assert (N - tail) * K > 1 << 32
+    say("block past 32 bits", M)
+    w = synth.normal((tail, K), 0.05, "bf16", seed=77, device=DEV)
+    qt, st = fp8q.fp8_quantize_weight_blocks(w)
+    qw = torch.zeros((N, K), dtype=torch.uint8, device=DEV)
+    sw = torch.ones((N // 128, st.shape[1]), dtype=torch.float32, device=DEV)
+    qw[-tail:], sw[-(tail // 128):] = qt, st
+    x = synth.activation(M, K, seed=78, outliers=True, device=DEV)
+    y, q, s = fp8q.fp8_linear_blockwise(x, qw, sw)
+    torch.cuda.synchronize()
+    want, ab = ref.gemm(host(q), host(s), host(qt), host(st))
+    got = y[:, -tail:].double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= ref.gemm_tolerance(want, ab, K))
+    assert torch.all(y[:, :-tail] == 0)
+
+
+def test_quantizers_past_32_bits():
+    """Values more than 2^32 elements into the matrix, against the same rows alone."""
+    K, tail = 4112, 256
+    N = (1 << 20) + tail
+    say("quantizers past 32 bits")
+    x = torch.zeros((N, K), dtype=torch.bfloat16, device=DEV)
+    x[-tail:] = synth.normal((tail, K), 1.0, "bf16", seed=79, device=DEV)
+    for f, rows in ((fp8q.fp8_quantize_blocks, None), (fp8q.fp8_quantize_weight_blocks, 2)):
+        q, s = f(x)
+        qt, st = f(x[-tail:].contiguous())
+        torch.cuda.synchronize()
+        assert torch.equal(q[-tail:], qt)
+        assert torch.equal(s[:, -tail:], st) if rows is None else torch.equal(s[-rows:], st)
+        assert not q[:-tail].any()

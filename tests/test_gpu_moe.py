@@ -181,3 +181,70 @@ def test_block_path_of_a_layer():
     want, ab = ref.gemm(host(q), host(s), host(qo), host(so))
     assert np.all(np.abs(a.double().cpu().numpy() - want) <= ref.gemm_tolerance(want, ab, H))
     _check(a.cpu(), logits, *w, top_k, True)
+
+
+def test_refused_sizes():
+    """Sizes outside the limits are refused as sizes, also where no buffer is passed."""
+    say("moe refusals")
+    for T, E, H, I, top_k in ((65, 4, 128, 128, 2), (2, 4, 128, 128, 5), (1, 20, 128, 128, 17),
+                              (1, 513, 16, 16, 1), (1, 4, 24, 128, 2), (1, 4, 128, 24, 2)):
+        nb = lambda n: (n + 127) // 128
+        zeros = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype, device=DEV)
+        with pytest.raises(RuntimeError, match="size out of range"):
+            fp8q.fp8_moe_blockwise(zeros(T, H, dtype=torch.bfloat16), zeros(T, E),
+                                   zeros(E, 2, I, H, dtype=torch.uint8), zeros(E, 2, nb(I), nb(H)),
+                                   zeros(E, H, I, dtype=torch.uint8), zeros(E, nb(H), nb(I)), top_k)
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a work buffer of its own."""
+    T, E, H, I, top_k = 24, 32, 1024, 272, 4
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    x, logits, *w = _inputs(T, E, H, I)
+    x2, logits2, *_ = _inputs(T, E, H, I, seed=1)
+    ins = [(x.to(DEV), torch.from_numpy(logits).to(DEV)), (x2.to(DEV), torch.from_numpy(logits2).to(DEV))]
+    want = [[t.clone() for t in fp8q.fp8_moe_blockwise(*i, *w, top_k)] for i in ins]
+    outs = [[torch.empty_like(t) for t in v] for v in want]
+    works = [torch.empty(fp8q.moe_work_bytes(T, I, top_k), dtype=torch.uint8, device=DEV) for _ in ins]
+    torch.cuda.synchronize()
+    say("moe two streams")
+    for _ in range(10):
+        for side, i, o, k in zip(sides, ins, outs, works):
+            with torch.cuda.stream(side):
+                fp8q.fp8_moe_blockwise(*i, *w, top_k, True, *o, work=k)
+    torch.cuda.synchronize()
+    for o, v in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, v))
+
+
+def test_weights_past_32_bits():
+    """The last of 512 experts lies more than 2^32 bytes into its array."""
+    E, H, I = 512, 4096, 1040
+    assert (E - 1) * 2 * I * H > 1 << 32
+    x, _, w13, s13, w2, s2 = _inputs(3, 1, H, I)
+    say("moe past 32 bits")
+    all13 = torch.zeros((E, 2, I, H), dtype=torch.uint8, device=DEV)
+    all2 = torch.zeros((E, H, I), dtype=torch.uint8, device=DEV)
+    sc13, sc2 = s13.repeat(E, 1, 1, 1), s2.repeat(E, 1, 1)
+    all13[-1], all2[-1] = w13[0], w2[0]
+    logits = torch.zeros((3, E), device=DEV)
+    logits[:, -1] = 5.0
+    y, ids, _ = fp8q.fp8_moe_blockwise(x.to(DEV), logits, all13, sc13, all2, sc2, 1)
+    one, _, _ = fp8q.fp8_moe_blockwise(x.to(DEV), logits[:, -1:].contiguous(), w13, s13, w2, s2, 1)
+    torch.cuda.synchronize()
+    assert torch.all(ids == E - 1) and torch.equal(y, one) and torch.any(one != 0)
+
+
+@pytest.mark.parametrize("T", [4, 8, 15, 40])
+def test_infinite_and_nan_tokens_stay_in_their_row(T):
+    E, H, I, top_k = 6, 272, 144, 2
+    x, logits, *w = _inputs(T, E, H, I)
+    x, logits = x.to(DEV), torch.from_numpy(logits).to(DEV)
+    say("moe inf and nan", T)
+    clean, _, _ = fp8q.fp8_moe_blockwise(x, logits, *w, top_k)
+    x[1], x[2, 5] = float("nan"), float("inf")
+    y, _, _ = fp8q.fp8_moe_blockwise(x, logits, *w, top_k)
+    torch.cuda.synchronize()
+    keep = [t for t in range(T) if t not in (1, 2)]
+    assert torch.equal(y[keep], clean[keep])
+    assert torch.isnan(y[1].float()).all() and not torch.isfinite(y[2].float()).any()
