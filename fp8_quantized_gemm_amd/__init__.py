@@ -1,5 +1,6 @@
-"""fp8_quantized_gemm_amd: FP8 E4M3 per-tensor-scaled linear layers and the
-NestedFP dual-precision GEMM for AMD MI355X (gfx950).
+"""fp8_quantized_gemm_amd: FP8 E4M3 linear layers (per-tensor, per-row or block
+scales), a mixture-of-experts layer on block-scaled weights and the NestedFP
+dual-precision GEMM for AMD MI355X (gfx950).
 
 The compute lives in ``libfp8q.so`` (hand-written HIP kernels behind a C ABI,
 declared in ``include/fp8q.h``).  ``fp8_quantized_gemm_amd.fp8q`` is the thin
