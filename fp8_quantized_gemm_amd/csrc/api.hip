@@ -603,7 +603,7 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
     FP8Q_TRY(check_apart({by}, {bw, bsw}));
     FP8Q_TRY(check_device());
     // the one launch reads x while other workgroups already store y
-    if (linear_block_fused_pays(M, K) && !overlap(by, bx))
+    if (linear_block_fused_pays(M, N, K) && !overlap(by, bx))
         return finish("fp8_linear_blockwise",
                       launch_linear_block_fused(x, dtype, qw, sw, y, q, sa, (int)M, (int)N, (int)K,
                                                 (hipStream_t)stream));

@@ -796,17 +796,24 @@ hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* 
     return hipGetLastError();
 }
 
-bool linear_block_fused_pays(int64_t M, int64_t K)
+// Every workgroup reads and quantizes the whole activation, which grows with
+// its blocks, while a launch of its own for that costs the same always: up to
+// 192 blocks one launch is as fast or faster (K = 4096, M = 3: N = 2048 4.6
+// against 6.2 us, 16384 13.2 against 15.6; M = 6: N = 6144 8.7 both, 12288 11.8
+// against 12.7), with 256 only under a long stream of weights (M = 8: N =
+// 2048 6.9 against 6.2, 16384 15.4 against 15.3, 22016 19.9 against 20.1).
+bool linear_block_fused_pays(int64_t M, int64_t N, int64_t K)
 {
-    return M <= kGemvBlockMaxM && M * blocks_of(K) <= kFusedBlockMaxCells &&
-           blocks_of(K) <= kPersistentMaxBlocks;
+    const int64_t cells = M * blocks_of(K);
+    return M <= kGemvBlockMaxM && blocks_of(K) <= kPersistentMaxBlocks &&
+           cells <= (N * K > (int64_t)1 << 26 ? kFusedBlockMaxCells : kFusedBlockMaxCells * 3 / 4);
 }
 
 hipError_t launch_linear_block_fused(const void* x, int dtype, const uint8_t* qw, const float* sw,
                                      uint16_t* y, uint8_t* q, float* sa, int M, int N, int K,
                                      hipStream_t stream)
 {
-    if (!linear_block_fused_pays(M, K)) return hipErrorInvalidValue;
+    if (!linear_block_fused_pays(M, N, K)) return hipErrorInvalidValue;
     const DecodeArgs a{x, q, sa, qw, sw, y, M, N, K};
     return dtype == DT_BF16 ? launch_decode<SRC_BF16>(a, stream) : launch_decode<SRC_FP16>(a, stream);
 }

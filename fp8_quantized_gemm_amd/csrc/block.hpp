@@ -26,7 +26,7 @@ hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* 
                              hipStream_t stream);
 // Quantizer and product in one launch, taken where linear_block_fused_pays.
 constexpr int kFusedBlockMaxCells = 256; // 1 x 128 blocks of the activation
-bool linear_block_fused_pays(int64_t M, int64_t K);
+bool linear_block_fused_pays(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_block_fused(const void* x, int dtype, const uint8_t* qw, const float* sw,
                                      uint16_t* y, uint8_t* q, float* sa, int M, int N, int K,
                                      hipStream_t stream);

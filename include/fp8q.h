@@ -393,8 +393,9 @@ FP8Q_API fp8q_status nested_linear_fp8_e4m3(const uint16_t* a, const uint8_t* hi
  *   sequence:
  *   x[M,K] in : bf16/fp16 activation;  qw[N,K], sw[NB,KB] in
  *   y[M,N] out;  q[M,K], sa[KB,M] out: the activation's codes and scales
- *   Size rules as fp8_gemm_blockwise.  One launch for M <= 16, M*KB <= 256 and K <=
- *   12288 unless y lies over x (which is allowed), else two.
+ *   Size rules as fp8_gemm_blockwise.  One launch for M <= 16, K <= 12288 and
+ *   M*KB <= 192 (256 where N*K > 2^26), unless y lies over x (which is allowed),
+ *   else two.
  */
 FP8Q_API fp8q_status fp8_quantize_blocks(const void* x, int dtype, int64_t rows, int64_t cols,
                                          uint8_t* q, float* scale, fp8q_stream stream);

@@ -160,7 +160,8 @@ def test_each_tile_shape_within_bound(M, N, K):
 
 # ------------------------------------------------------------------ linear
 LINEAR = [(1, 4096, 4096), (1, 4090, 11008), (2, 4090, 8192), (4, 4090, 6000), (1, 37, 160), (3, 515, 1040), (8, 2048, 4096), (11, 300, 5120),
-          (16, 4100, 2064), (17, 257, 272), (200, 640, 4096), (600, 515, 1040)]
+          (16, 4100, 2064), (5, 2048, 4096), (9, 300, 2320), (10, 515, 2048), (8, 16400, 4096),
+          (16, 32784, 2048), (17, 257, 272), (200, 640, 4096), (600, 515, 1040)]
 
 
 def _linear_inputs(M, N, K, dtype):
