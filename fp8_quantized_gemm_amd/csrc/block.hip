@@ -128,9 +128,9 @@ __global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
 // A workgroup owns 8 * RT weight rows (RT row tiles that share the activation
 // loads); its waves interleave over the K blocks.  Tokens come in MT groups
 // of eight.  gemv_block_kernel, one workgroup per tile, serves the K that the
-// persistent kernel below does not hold.
+// persistent kernel below does not hold, and products of more tokens that are
+// too small to fill the chip with LDS tiles (launch_tile_block).
 constexpr int kGbWaves = 16;
-constexpr int kGbUnroll = 2;
 
 __device__ __forceinline__ v4f mfma_pair(const v4i& w, const v4i& a, v4f c)
 {
@@ -146,23 +146,24 @@ __device__ __forceinline__ float quad_xor1(float v)
     return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xf, 0xf, true));
 }
 
-template <int MT, int RT>
+template <int MT, int RT, int U>
 __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, uint16_t* __restrict__ y, int M, int N, int K)
 {
-    constexpr int U = kGbUnroll;
-    __shared__ float red[kGbWaves][MT * RT][8][9];
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    float(*red)[MT * RT][8][9] = reinterpret_cast<float(*)[MT * RT][8][9]>(lds);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4, odd = r & 1;
-    const int n0 = blockIdx.x * 8 * RT;
+    const int n0 = blockIdx.x * 8 * RT, m0 = blockIdx.y * 8 * MT;
+    const int rows = min(8 * MT, M - m0);
     const int koff = (2 * g + odd) * 16;
     const int nblk = (K + kBlock - 1) / kBlock;
 
     const rsrc_t rw = make_rsrc(qw + (size_t)n0 * K, (uint32_t)(min(8 * RT, N - n0) * K));
-    const rsrc_t ra = make_rsrc(qa, (uint32_t)(M * K));
-    const rsrc_t rs = make_rsrc(sa, (uint32_t)(M * nblk * 4));
+    const rsrc_t ra = make_rsrc(qa + (size_t)m0 * K, (uint32_t)(rows * K));
+    const rsrc_t rs = make_rsrc(sa + m0, (uint32_t)(((nblk - 1) * M + rows) * 4));
     const float* const swb = sw + (size_t)(n0 >> 7) * nblk;
     const uint32_t off = (uint32_t)((r >> 1) * K + koff);      // of row or token r / 2
 
@@ -185,7 +186,7 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 a[u][m] = buf_load16(ra, in ? off + m * 8 * K + kb * kBlock : kOOB);
-                // tokens past M read another token's scale or zero: their results are dropped
+                // tokens past the last read another token's scale or zero: their results are dropped
                 s[u][m] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(
                     rs, kb < nblk ? (uint32_t)((kb * M + m * 8 + (r >> 1)) * 4) : kOOB, 0, 0));
             }
@@ -220,11 +221,11 @@ __global__ __launch_bounds__(kGbWaves * 64) void gemv_block_kernel(
     for (int o = threadIdx.x; o < MT * RT * 64; o += kGbWaves * 64) {
         const int row = o & 7, t = (o >> 3) % RT, mm = (o >> 3) / RT;     // token mm, row 8 t + row
         const int n = n0 + t * 8 + row;
-        if (mm >= M || n >= N) continue;
+        if (mm >= rows || n >= N) continue;
         float v = 0.0f;
 #pragma unroll
         for (int w = 0; w < kGbWaves; ++w) v += red[w][(mm >> 3) * RT + t][mm & 7][row];
-        y[(size_t)mm * N + n] = (uint16_t)f32_to_bf16_bits(v);
+        y[(size_t)(m0 + mm) * N + n] = (uint16_t)f32_to_bf16_bits(v);
     }
 }
 
@@ -696,6 +697,8 @@ hipError_t launch_quantize_weight_blocks(const void* w, int dtype, int64_t batch
 
 namespace {
 
+int64_t div_up(int64_t n, int64_t d) { return (n + d - 1) / d; }
+
 // Arguments of the decode products; x is null for codes in q.
 struct DecodeArgs {
     const void* x;
@@ -773,6 +776,21 @@ hipError_t launch_src(const DecodeArgs& a, hipStream_t stream)
     return hipErrorInvalidValue;
 }
 
+template <int MT, int RT, int U>
+hipError_t launch_gemv(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
+                       uint16_t* y, int M, int N, int K, hipStream_t stream)
+{
+    auto kern = gemv_block_kernel<MT, RT, U>;
+    constexpr size_t lds = sizeof(float) * kGbWaves * MT * RT * 8 * 9;
+    static std::atomic<uint64_t> attr_devices{0};
+    if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern), lds, attr_devices);
+        e != hipSuccess)
+        return e;
+    const dim3 grid((unsigned)div_up(N, 8 * RT), (unsigned)div_up(M, 8 * MT));
+    kern<<<grid, kGbWaves * 64, lds, stream>>>(qa, sa, qw, sw, y, M, N, K);
+    return hipGetLastError();
+}
+
 template <int SRC>
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream)
 {
@@ -787,13 +805,8 @@ hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* 
     if (blocks_of(K) <= kPersistentMaxBlocks)
         return launch_decode<SRC_CODES>({nullptr, const_cast<uint8_t*>(qa), const_cast<float*>(sa), qw,
                                          sw, y, M, N, K}, stream);
-    constexpr int RT = 2;
-    const int grid = (int)(((int64_t)N + 8 * RT - 1) / (8 * RT));
-    if (M <= 8)
-        gemv_block_kernel<1, RT><<<grid, kGbWaves * 64, 0, stream>>>(qa, sa, qw, sw, y, M, N, K);
-    else
-        gemv_block_kernel<2, RT><<<grid, kGbWaves * 64, 0, stream>>>(qa, sa, qw, sw, y, M, N, K);
-    return hipGetLastError();
+    return M <= 8 ? launch_gemv<1, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream)
+                  : launch_gemv<2, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
 }
 
 // Every workgroup reads and quantizes the whole activation, which grows with
@@ -836,6 +849,18 @@ constexpr TileShape kBlockShapes[] = {
 hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
                              const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
 {
+    // Few outputs: the tiles leave most CUs idle and walk K step by step, so the
+    // decode kernel, whose 16 waves share K, takes them wherever its workgroups
+    // of 32 tokens by 16 or 32 columns are at most one per CU (N x K = 4096 x
+    // 4096, M = 32: 13.1 -> 7.5 us, M = 64: 13.9 -> 10.2; 4096 x 11008, M = 32:
+    // 28.8 -> 17.2, M = 64: 31.4 -> 21.4; 8192 x 4096, M = 32: 13.7 -> 11.8; in
+    // two rounds it loses: 5120 x 5120, M = 32, 16 columns: 16.6 against 16.3,
+    // 12288 x 4096, 32 columns: 20.5 against 16.7).
+    const int64_t groups = div_up(M, 32);
+    if (groups * div_up(N, 16) <= kCUs)
+        return launch_gemv<4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
+    if (groups * div_up(N, 32) <= kCUs)
+        return launch_gemv<4, 4, 1>(qa, sa, qw, sw, y, M, N, K, stream);
     switch (pick_tile_shape(kBlockShapes, sizeof(kBlockShapes) / sizeof(kBlockShapes[0]), M, N)) {
     case 0: return launch_block_tile<256, 256, 2, 4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
     case 1: return launch_block_tile<256, 192, 2, 4, 2, 3>(qa, sa, qw, sw, y, M, N, K, stream);

@@ -385,7 +385,8 @@ FP8Q_API fp8q_status nested_linear_fp8_e4m3(const uint16_t* a, const uint8_t* hi
  *   qa[M,K], sa[KB,M] in: activation codes and scales
  *   qw[N,K], sw[NB,KB] in: weight codes and scales
  *   y[M,N]   out: bf16 bit patterns
- *   1 <= M, N <= 2^30;  16 <= K <= 2^22 and K % 16 == 0.  M <= 16 runs the
+ *   1 <= M, N <= 2^30;  16 <= K <= 2^22 and K % 16 == 0.  M <= 16, and larger M with
+ *   few outputs (M/32 * N/32 <= 256, rounded up), runs the
  *   weight-streaming kernel.
  *
  * fp8_linear_blockwise - fp8_quantize_blocks on the activation, then

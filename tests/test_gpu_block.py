@@ -126,7 +126,14 @@ DECODE = [(1, 4090, 1040), (3, 4094, 2064), (2, 4090, 6000), (8, 4096, 8192), (6
           (16, 4090, 2048), (9, 4091, 4096), (11, 4090, 8192), (13, 4090, 12288), (1, 4090, 12304)]
 
 
-@pytest.mark.parametrize("M,N,K", SHAPES + DECODE)
+# more tokens than a decode step on few columns: 16 and 32 columns a workgroup, one and
+# several groups of 32 tokens, long K, and one column more than they take
+FEW = [(17, 4096, 1040), (32, 4090, 2320), (33, 2047, 272), (64, 1000, 16400), (250, 500, 528),
+       (2100, 40, 400), (8192, 16, 144), (31, 8190, 400), (64, 4081, 1296), (200, 1170, 272),
+       (4000, 64, 272), (64, 4097, 272)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES + DECODE + FEW)
 def test_random_within_bound(M, N, K):
     x = synth.activation(M, K, seed=synth.seed_for("bx", M, N, K), outliers=True)
     w = synth.normal((N, K), 0.02, "fp16", seed=synth.seed_for("bw", M, N, K))
