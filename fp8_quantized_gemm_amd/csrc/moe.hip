@@ -15,7 +15,7 @@
 // logits are a few KiB, and up to kRouteInline tokens a launch of its own
 // (moe_route_kernel) would cost more.  It then deals items, some columns of
 // one expert's h, out to the waves.  The second (moe_down) gives each
-// workgroup 8 or 16 columns of y and all chosen experts, so the weighted sum
+// workgroup 8 to 32 columns of y and all chosen experts, so the weighted sum
 // over experts needs no atomics and no kernel of its own.
 //
 // Both stream weight rows through the MFMA operand layout of Layout, a wave
@@ -536,6 +536,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
 {
     typedef Layout<kDownRows> L;
     constexpr int COLS = RT * kDownRows;
+    // weight scales: one where the columns lie in one block of 128, else one a tile
+    constexpr int FS = kBlock % COLS == 0 ? 1 : RT;
     __shared__ uint64_t masks[PER * 64];
     __shared__ float wt[kMaxPairs];
     extern __shared__ __attribute__((aligned(16))) float ysum[];   // [waves][T][COLS]
@@ -575,7 +577,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     };
     struct Stage {
         v4i w[BLOCKS][RT], h[BLOCKS][HV];
-        float s[BLOCKS];
+        float s[BLOCKS][FS];
         int kb0, first;
         Tokens tokens;
     };
@@ -587,8 +589,12 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
         const int slot = it / chunks;
         st.kb0 = (it - slot * chunks) * BLOCKS;
         const int e = active.expert(slot, lane);
-        const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(COLS * I));
-        const float* const sb = s2 + ((size_t)e * ((H + kBlock - 1) / kBlock) + (n0 >> 7)) * nblk;
+        const rsrc_t rw = make_rsrc(w2 + ((size_t)e * H + n0) * I, (uint32_t)(min(COLS, H - n0) * I));
+        const float* sb[FS];
+#pragma unroll
+        for (int n = 0; n < FS; ++n)
+            sb[n] = s2 + ((size_t)e * ((H + kBlock - 1) / kBlock) + (min(n0 + n * kDownRows, H - 1) >> 7)) *
+                             nblk;
 #pragma unroll
         for (int c = 0; c < BLOCKS; ++c) {
             const int kb = st.kb0 + c;
@@ -597,7 +603,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
                 st.w[c][n] = buf_load16<CP>(
                     rw, kb * kBlock + at.koff < I
                             ? (uint32_t)((n * kDownRows + at.row) * I + kb * kBlock + at.koff) | none : kOOB);
-            st.s[c] = sb[min(kb, nblk - 1)];
+#pragma unroll
+            for (int n = 0; n < FS; ++n) st.s[c][n] = sb[n][min(kb, nblk - 1)];
         }
         st.first = active.first_pair(e);
         st.tokens.find(masks, e, lane);
@@ -622,7 +629,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
                         for (int i = 0; i < 4; ++i) q[i] = __builtin_fmaf(d[i], 1.0f / kRestScale, q[i]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c], acc[i]);
+                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c][FS == 1 ? 0 : n], acc[i]);
                 }
                 float v[L::kOut];
                 at.fold(acc, lane, v);
@@ -771,11 +778,22 @@ hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
         }
     }
     if (e != hipSuccess) return e;
-    if (a.T <= kRestTokens) return launch_down<PER, 1, 2, true>(a, stream);
-    // two row tiles share the loads of h where that leaves a workgroup per CU
-    // (4096 x 1392, 13 tokens: 32.8 -> 27.2 us)
-    return a.H < 16 * kCUs ? launch_down<PER, 1, 3, false>(a, stream)
-                           : launch_down<PER, 2, 2, false>(a, stream);
+    // moe_down's row tiles of eight columns, which share the loads of h: as many
+    // as leave at most one workgroup per CU (1024 columns of h, 4 of 16 experts,
+    // 8 / 40 tokens, microseconds a call: H = 2048 one 24.8 / 35.9, two 26.6 /
+    // 38.4; 2560 one 34.9 / 53.4, two 29.4 / 43.8; 4096 one 46.0 / 64.3, two 41.1
+    // / 58.8; 5120 two 49.2 / 83.1, three 43.2 / 72.8; 8192 three 77.2 / 106.6,
+    // four 70.8 / 93.6).  K blocks an item: what 128 registers hold; with two
+    // tiles two blocks of bf16 fit as well and take as long as one.
+    const bool rest = a.T <= kRestTokens;
+    const int per_cu = (a.H + kDownRows * kCUs - 1) / (kDownRows * kCUs);
+    if (per_cu <= 1)
+        return rest ? launch_down<PER, 1, 2, true>(a, stream) : launch_down<PER, 1, 3, false>(a, stream);
+    if (per_cu <= 2)
+        return rest ? launch_down<PER, 2, 1, true>(a, stream) : launch_down<PER, 2, 1, false>(a, stream);
+    if (per_cu <= 3)
+        return rest ? launch_down<PER, 3, 1, true>(a, stream) : launch_down<PER, 3, 1, false>(a, stream);
+    return rest ? launch_down<PER, 4, 1, true>(a, stream) : launch_down<PER, 4, 1, false>(a, stream);
 }
 
 template <int DT>

@@ -71,6 +71,23 @@ def test_layer_with_many_items(T, E, H, I, top_k, dtype):
     _check(*_inputs(T, E, H, I, dtype), top_k, True)
 
 
+# Widths of the second kernel's two, three and four row tiles, with and without the rest of h,
+# rows of W2 of whole and of partial lines, ends inside a tile.
+@pytest.mark.parametrize("T,E,H,I,top_k,dtype", [
+    (3, 4, 2064, 144, 2, "bf16"),
+    (20, 6, 4096, 256, 3, "fp16"),
+    (8, 4, 4112, 128, 2, "bf16"),
+    (17, 5, 6128, 272, 2, "bf16"),
+    (1, 300, 6160, 16, 4, "bf16"),
+    (64, 3, 8176, 144, 2, "fp16"),
+    (64, 260, 6160, 16, 2, "bf16"),
+    (6, 2, 9232, 256, 1, "bf16"),
+])
+def test_layer_of_each_width(T, E, H, I, top_k, dtype):
+    say("moe width", T, E, H, I, top_k, dtype)
+    _check(*_inputs(T, E, H, I, dtype), top_k, True)
+
+
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_masked_and_tied_logits(renormalize):
     T, E, H, I, top_k = 12, 70, 144, 144, 6
