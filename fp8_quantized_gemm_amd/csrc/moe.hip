@@ -20,6 +20,7 @@
 //
 // Both stream weight rows through the MFMA operand layout of Layout, a wave
 // at a time, without any exchange between lanes or waves.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -82,15 +83,6 @@ __device__ __forceinline__ v4f block_product(const v4i& w, const v4i& x0, const 
 {
     const v4f p = Half<DT>::mfma(Half<DT>::widen(w[0], w[1]), x0, v4f{0.f, 0.f, 0.f, 0.f});
     return Half<DT>::mfma(Half<DT>::widen(w[2], w[3]), x1, p);
-}
-
-// The same of E4M3 rows and E5M2 tokens.
-__device__ __forceinline__ v4f rest_product(const v4i& w, const v4i& x)
-{
-    const long w0 = __builtin_bit_cast(long, v2i{w[0], w[1]}), w1 = __builtin_bit_cast(long, v2i{w[2], w[3]});
-    const long x0 = __builtin_bit_cast(long, v2i{x[0], x[1]}), x1 = __builtin_bit_cast(long, v2i{x[2], x[3]});
-    const v4f p = __builtin_amdgcn_mfma_f32_16x16x32_fp8_bf8(w0, x0, v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
-    return __builtin_amdgcn_mfma_f32_16x16x32_fp8_bf8(w1, x1, p, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------- selection
@@ -296,20 +288,40 @@ __device__ __forceinline__ int h_position(int i)
 {
     return (i & ~127) | (i & 8) << 3 | (i >> 4 & 7) << 3 | (i & 7);
 }
-// Up to kRestTokens tokens the part of h that its bf16 rounding leaves out is
-// kept too, as an E5M2 code of 2^12 times it, in rows with the columns in
-// order: with bf16 alone the error of y is 1.4 times that of its own rounding
-// (bf16's 2^-8 twice), with it about that of its own rounding.  E5M2 holds
-// 2^12 rest for |h| from 2^-19 to 2^11; outside h has bf16's precision.  Above,
-// the second kernel is bound by its loads of h, and one of three more costs
-// too much.
-constexpr int kRestTokens = 8;
-constexpr float kRestScale = 0x1p12f;
-__device__ __forceinline__ uint8_t h_rest_code(float h, uint32_t bits)
+// h is kept in fp16 with a power of two for every four columns of a pair, the
+// exponent of the largest of them (which the stored values bring to [1, 2)):
+// two bytes a value, as in bf16, with 2^-11 instead of 2^-8 lost, over fp32's
+// whole range.  moe_down brings a block's values to its largest exponent.  In
+// bf16 the error of y is 1.4 times that of its own rounding, in this form 1.01
+// times.  64 tokens, 8 of 128 experts, 2048 x 768 take 115 us a call, 110 with
+// bf16 alone.  Two bf16 values for each h, the second for what the first
+// leaves out, lose less still, but moe_down is bound by its reads of h from
+// the L2: 129 us.
+constexpr int kHGroup = 4;
+
+// The exponents of a pair, a byte a group: those of a 16-column unit in the
+// `blocks` (1 to 3) K blocks that moe_down takes at a time stand together, so
+// that a lane reads them at once and the lanes of a token read neighbouring
+// bytes (a load for each block: 64 tokens, 6 of 64 experts, 2048 x 1408 120
+// against 116 us).  The room for them is that of three blocks, the most.
+__host__ __device__ constexpr int exp_slot(int blocks) { return blocks == 3 ? 16 : 4 * blocks; }
+__host__ __device__ constexpr int exp_stride(int I) { return ((I + kBlock - 1) / kBlock + 2) / 3 * 8 * exp_slot(3); }
+__device__ __forceinline__ int exp_position(int i, int blocks)
 {
-    const float d = (h - bf16_bits_to_f32(bits)) * kRestScale;
-    // inf - inf, and what E5M2 would round to infinity
-    return (uint8_t)__builtin_amdgcn_cvt_pk_bf8_f32(fabsf(d) <= 57344.0f ? d : 0.0f, 0.0f, 0, false);
+    const int kb = i / kBlock, item = kb / blocks;
+    return (item * 8 + (i >> 4 & 7)) * exp_slot(blocks) + (kb - item * blocks) * 4 + (i >> 2 & 3);
+}
+
+// The larger of the values here and in the lane 16 (32) away.
+__device__ __forceinline__ uint32_t max_xor16(uint32_t v)
+{
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return max((uint32_t)p[0], (uint32_t)p[1]);
+}
+__device__ __forceinline__ uint32_t max_xor32(uint32_t v)
+{
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return max((uint32_t)p[0], (uint32_t)p[1]);
 }
 
 __device__ __forceinline__ int h_stride(int I) { return (I + kBlock - 1) / kBlock * kBlock; }
@@ -354,8 +366,8 @@ void moe_up_kernel(
     const uint16_t* __restrict__ x, const float* __restrict__ logits,
     const uint8_t* __restrict__ w13, const float* __restrict__ s13, int* __restrict__ ids_io,
     float* __restrict__ weights_io, uint64_t* __restrict__ masks_out,
-    float* __restrict__ pair_weights, uint16_t* __restrict__ h, uint8_t* __restrict__ h_rest, int T,
-    int H, int I, int E, int top_k, int renormalize)
+    float* __restrict__ pair_weights, uint16_t* __restrict__ h, uint8_t* __restrict__ h_exp, int T,
+    int H, int I, int E, int top_k, int renormalize, int down_blocks)
 {
     typedef Layout<R> L;
     constexpr int KL = L::kBlocks * kBlock;                // K per load
@@ -491,27 +503,29 @@ void moe_up_kernel(
                     float gv[L::kOut], uv[L::kOut];
                     at.fold(acc[m][n][0], lane, gv);
                     at.fold(acc[m][n][1], lane, uv);
-                    const int p = p0 + m * R + at.row;
+                    float hv[L::kOut], largest = 0.0f;
+#pragma unroll
+                    for (int q = 0; q < L::kOut; ++q) {
+                        hv[q] = gv[q] / (1.0f + expf(-gv[q])) * uv[q];
+                        largest = fmaxf(largest, fabsf(hv[q]));      // passes over a NaN
+                    }
+                    // a group's columns are 4 / kOut lanes 16 apart
+                    uint32_t top = max_xor16(__float_as_uint(largest));
+                    if constexpr (L::kOut == 1) top = max_xor32(top);
+                    const int exponent = max((int)(top >> 23), 1);
+                    const int p = p0 + m * R + at.row, i = i0 + n * R + at.out_row;
                     if (at.owner && p < tokens.count) {
-                        uint16_t* const dst = h + (size_t)(first + p) * h_stride(I) +
-                                              h_position(i0 + n * R + at.out_row);
-                        float hv[L::kOut];
+                        uint16_t* const dst = h + (size_t)(first + p) * h_stride(I) + h_position(i);
                         uint32_t bits[L::kOut];
 #pragma unroll
-                        for (int q = 0; q < L::kOut; ++q) {
-                            hv[q] = gv[q] / (1.0f + expf(-gv[q])) * uv[q];
-                            bits[q] = f32_to_bf16_bits(hv[q]);
-                        }
-                        if (h_rest != nullptr) {
-                            uint8_t* const rest = h_rest + (size_t)(first + p) * h_stride(I) + i0 + n * R +
-                                                  at.out_row;
-#pragma unroll
-                            for (int q = 0; q < L::kOut; ++q) rest[q] = h_rest_code(hv[q], bits[q]);
-                        }
+                        for (int q = 0; q < L::kOut; ++q)
+                            bits[q] = f32_to_f16_bits(__builtin_ldexpf(hv[q], 127 - exponent));
                         if constexpr (L::kOut == 2)
                             *reinterpret_cast<uint32_t*>(dst) = bits[0] | bits[1] << 16;
                         else
                             *dst = (uint16_t)bits[0];
+                        if (at.out_row % kHGroup == 0)
+                            h_exp[(first + p) * exp_stride(I) + exp_position(i, down_blocks)] = (uint8_t)exponent;
                     }
                 }
             p0 += MT * R;
@@ -527,9 +541,9 @@ void moe_up_kernel(
 // sums are added in a fixed order at the end.
 constexpr int kDownRows = 8;                // columns of y (rows of W2) per row tile
 
-template <int PER, int RT, int BLOCKS, bool REST, int CP>
+template <int PER, int RT, int BLOCKS, int CP>
 __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
-    const uint16_t* __restrict__ h, const uint8_t* __restrict__ h_rest,
+    const uint16_t* __restrict__ h, const uint8_t* __restrict__ h_exp,
     const uint8_t* __restrict__ w2, const float* __restrict__ s2,
     const uint64_t* __restrict__ masks_in, const float* __restrict__ pair_weights,
     uint16_t* __restrict__ y, int T, int H, int I, int E, int top_k)
@@ -557,26 +571,61 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     const int chunks = (nblk + BLOCKS - 1) / BLOCKS;
     const int items = active.count * chunks;
     const rsrc_t rh = make_rsrc(h, (uint32_t)(T * top_k * h_stride(I) * 2));
-    const rsrc_t rr = make_rsrc(h_rest, (uint32_t)(T * top_k * h_stride(I)));
+    const rsrc_t re = make_rsrc(h_exp, (uint32_t)(T * top_k * exp_stride(I)));
     float* const mine = ysum + wave * T * COLS;
 
-    // rows of h of pair p (none: zeros) in the K blocks from kb0: two operands
-    // of bf16 and, with REST, one of E5M2
-    constexpr int HV = REST ? 3 : 2;
-    auto load_h = [&](v4i (&hv)[BLOCKS][HV], int p, bool none, int kb0) {
+    struct Rows {
+        v4i v[BLOCKS][2];
+        uint32_t e[BLOCKS];
+    };
+    // rows of h of pair p (none: zeros) in the K blocks from kb0, as stored:
+    // two operands and the exponents of their four groups.  What is not there
+    // is moved out of range by an addition, not by a branch.
+    auto load_h = [&](Rows& rows, int p, bool none, int kb0) {
+        const uint32_t past = none ? kOOB : 0u;
 #pragma unroll
         for (int c = 0; c < BLOCKS; ++c) {
             const int kb = (kb0 + c) * kBlock;
-            const bool out = none || kb + at.koff >= I;
-            const uint32_t o = out ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2;
-            hv[c][0] = buf_load16(rh, o);
-            hv[c][1] = buf_load16(rh, o + 128);
-            if constexpr (REST)
-                hv[c][2] = buf_load16(rr, out ? kOOB : (uint32_t)(p * h_stride(I) + kb + at.koff));
+            const uint32_t o = (uint32_t)(p * h_stride(I) + kb + at.koff / 2) * 2 +
+                               (kb + at.koff < I ? past : kOOB);
+            rows.v[c][0] = buf_load16(rh, o);
+            rows.v[c][1] = buf_load16(rh, o + 128);
+        }
+        const uint32_t o = (uint32_t)(p * exp_stride(I) + (kb0 / BLOCKS * 8 + at.koff / 16) * exp_slot(BLOCKS)) + past;
+        if constexpr (BLOCKS == 1) {
+            rows.e[0] = __builtin_amdgcn_raw_buffer_load_b32(re, o, 0, 0);
+        } else if constexpr (BLOCKS == 2) {
+            const auto e = __builtin_amdgcn_raw_buffer_load_b64(re, o, 0, 0);
+            rows.e[0] = e[0], rows.e[1] = e[1];
+        } else {
+            const auto e = __builtin_amdgcn_raw_buffer_load_b96(re, o, 0, 0);
+            rows.e[0] = e[0], rows.e[1] = e[1], rows.e[2] = e[2];
         }
     };
+    // brings the values of block c to the largest exponent among a token's
+    // lanes, and returns the power of two they then lack
+    auto align_h = [&](Rows& rows, int c, int kb0) {
+        // none are stored past the last column
+        const uint32_t e = (kb0 + c) * kBlock + at.koff < I ? rows.e[c] : 0u;
+        const int e4[4] = {(int)(e & 255), (int)(e >> 8 & 255), (int)(e >> 16 & 255), (int)(e >> 24)};
+        uint32_t top = (uint32_t)max(max(e4[0], e4[1]), max(e4[2], e4[3]));
+        top = max(top, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xf, 0xf, true));
+        top = max_xor32(max_xor16(top));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const _Float16 f = __builtin_amdgcn_ldexph((_Float16)1.0f, e4[i] - (int)top);
+            v4i& v = rows.v[c][i / 2];
+#pragma unroll
+            for (int j = i % 2 * 2; j < i % 2 * 2 + 2; ++j) {
+                const int two = v[j];          // (a bit cast of v[j] itself reads v[0])
+                v[j] = __builtin_bit_cast(int, __builtin_bit_cast(v2h, two) * v2h{f, f});
+            }
+        }
+        return (int)top - 127;
+    };
     struct Stage {
-        v4i w[BLOCKS][RT], h[BLOCKS][HV];
+        v4i w[BLOCKS][RT];
+        Rows h;
         float s[BLOCKS][FS];
         int kb0, first;
         Tokens tokens;
@@ -617,19 +666,19 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
             if (p0 > 0) load_h(st.h, st.first + p, p >= st.tokens.count, st.kb0);
             const int t = st.tokens.at(p);
             const float f = t >= 0 ? wt[st.first + p] : 0.0f;
+            int lack[BLOCKS];
+#pragma unroll
+            for (int c = 0; c < BLOCKS; ++c) lack[c] = align_h(st.h, c, st.kb0);
 #pragma unroll
             for (int n = 0; n < RT; ++n) {
                 v4f acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int c = 0; c < BLOCKS; ++c) {
-                    v4f q = block_product<DT_BF16>(st.w[c][n], st.h[c][0], st.h[c][1]);
-                    if constexpr (REST) {
-                        const v4f d = rest_product(st.w[c][n], st.h[c][2]);
+                    const v4f q = block_product<DT_FP16>(st.w[c][n], st.h.v[c][0], st.h.v[c][1]);
+                    float f = __builtin_ldexpf(st.s[c][FS == 1 ? 0 : n], lack[c]);
+                    f = f > FLT_MAX ? FLT_MAX : f;       // a zero product stays zero
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) q[i] = __builtin_fmaf(d[i], 1.0f / kRestScale, q[i]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], st.s[c][FS == 1 ? 0 : n], acc[i]);
+                    for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(q[i], f, acc[i]);
                 }
                 float v[L::kOut];
                 at.fold(acc, lane, v);
@@ -665,8 +714,8 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
     }
 }
 
-// The workspace: the experts' token masks, the weights grouped like h, h, and
-// up to kRestTokens tokens what its rounding left out.
+// The workspace: the experts' token masks, the weights grouped like h, h and
+// its exponents.
 struct MoeWork {
     static constexpr int64_t kWeightsAt = kMoeMaxExperts * 8, kHAt = kWeightsAt + kMaxPairs * 4;
     static int64_t h_bytes(int64_t T, int64_t I, int64_t top_k)
@@ -675,22 +724,38 @@ struct MoeWork {
     }
     static int64_t bytes(int64_t T, int64_t I, int64_t top_k)
     {
-        return kHAt + h_bytes(T, I, top_k) + (T <= kRestTokens ? h_bytes(T, I, top_k) / 2 : 0);
+        return kHAt + h_bytes(T, I, top_k) + T * top_k * exp_stride((int)I);
     }
     uint64_t* masks;
     float* weights;
     uint16_t* h;
-    uint8_t* h_rest;
+    uint8_t* h_exp;
     explicit MoeWork(const MoeArgs& a)
     {
         char* const p = static_cast<char*>(a.work);
         masks = reinterpret_cast<uint64_t*>(p);
         weights = reinterpret_cast<float*>(p + kWeightsAt);
         h = reinterpret_cast<uint16_t*>(p + kHAt);
-        h_rest = a.T <= kRestTokens
-                     ? reinterpret_cast<uint8_t*>(p + kHAt + h_bytes(a.T, a.I, a.top_k)) : nullptr;
+        h_exp = reinterpret_cast<uint8_t*>(p + kHAt + h_bytes(a.T, a.I, a.top_k));
     }
 };
+
+// moe_down's row tiles of eight columns, which share the loads of h: as many
+// as leave at most one workgroup per CU (1024 columns of h, 4 of 16 experts,
+// 8 / 40 tokens, microseconds a call: H = 2048 one 24.8 / 35.9, two 26.6 /
+// 38.4; 2560 one 34.9 / 53.4, two 29.4 / 43.8; 4096 one 46.0 / 64.3, two 41.1
+// / 58.8; 5120 two 49.2 / 83.1, three 43.2 / 72.8; 8192 three 77.2 / 106.6,
+// four 70.8 / 93.6), four at most.
+inline int down_tiles(const MoeArgs& a)
+{
+    return std::min((a.H + kDownRows * kCUs - 1) / (kDownRows * kCUs), 4);
+}
+// Its K blocks an item: with one row tile what 128 registers hold, except
+// where the items are few (one token, 8 of 128, 2048 x 768: 16.5 against 16.8
+// us with three; 64 tokens 120 against 116); else one (two of them with two
+// tiles: 4096 x 1408, 2 of 8 experts, one token 14.6 -> 15.2, 64 tokens 63.5
+// -> 64.4).
+inline int down_blocks(const MoeArgs& a) { return down_tiles(a) > 1 ? 1 : a.T <= 4 ? 2 : 3; }
 
 template <int DT, int PER, int R, int RT, int MT, int UB, int WAVES, int OCC, bool ROUTED>
 hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
@@ -700,15 +765,15 @@ hipError_t launch_up(const MoeArgs& a, hipStream_t stream)
     const int grid = (int)std::min<int64_t>(items, kCUs * OCC * 4 / WAVES);
     moe_up_kernel<DT, PER, R, RT, MT, UB, WAVES, OCC, ROUTED><<<grid, WAVES * 64, 0, stream>>>(
         static_cast<const uint16_t*>(a.x), a.logits, a.w13, a.s13, a.ids, a.weights, work.masks,
-        work.weights, work.h, work.h_rest, a.T, a.H, a.I, a.E, a.top_k, a.renormalize);
+        work.weights, work.h, work.h_exp, a.T, a.H, a.I, a.E, a.top_k, a.renormalize, down_blocks(a));
     return hipGetLastError();
 }
 
-template <int PER, int RT, int BLOCKS, bool REST, int CP>
+template <int PER, int RT, int BLOCKS, int CP>
 hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
 {
     constexpr int COLS = RT * kDownRows;
-    auto kern = moe_down_kernel<PER, RT, BLOCKS, REST, CP>;
+    auto kern = moe_down_kernel<PER, RT, BLOCKS, CP>;
     const size_t lds = (size_t)kMoeWaves * a.T * COLS * sizeof(float);
     static std::atomic<uint64_t> attr_devices{0};
     if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern),
@@ -717,7 +782,7 @@ hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
         e != hipSuccess)
         return e;
     const MoeWork work(a);
-    kern<<<(a.H + COLS - 1) / COLS, kMoeThreads, lds, stream>>>(work.h, work.h_rest, a.w2, a.s2,
+    kern<<<(a.H + COLS - 1) / COLS, kMoeThreads, lds, stream>>>(work.h, work.h_exp, a.w2, a.s2,
                                                                 work.masks, work.weights, a.y, a.T,
                                                                 a.H, a.I, a.E, a.top_k);
     return hipGetLastError();
@@ -726,11 +791,11 @@ hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
 // Non-temporal weight loads where rows of W2 are whole 128-byte lines; else a
 // line is shared by two rows and has to stay for the second (H x I = 4096 x
 // 1392, 13 tokens: 35.5 against 32.4 us).
-template <int PER, int RT, int BLOCKS, bool REST>
+template <int PER, int RT, int BLOCKS>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
-    return a.I % kBlock == 0 ? launch_down_cp<PER, RT, BLOCKS, REST, CP_NT>(a, stream)
-                             : launch_down_cp<PER, RT, BLOCKS, REST, CP_DEFAULT>(a, stream);
+    return a.I % kBlock == 0 ? launch_down_cp<PER, RT, BLOCKS, CP_NT>(a, stream)
+                             : launch_down_cp<PER, RT, BLOCKS, CP_DEFAULT>(a, stream);
 }
 
 // Above this many tokens the selection is a kernel of its own: repeating it in
@@ -778,22 +843,12 @@ hipError_t launch_both(const MoeArgs& a, hipStream_t stream)
         }
     }
     if (e != hipSuccess) return e;
-    // moe_down's row tiles of eight columns, which share the loads of h: as many
-    // as leave at most one workgroup per CU (1024 columns of h, 4 of 16 experts,
-    // 8 / 40 tokens, microseconds a call: H = 2048 one 24.8 / 35.9, two 26.6 /
-    // 38.4; 2560 one 34.9 / 53.4, two 29.4 / 43.8; 4096 one 46.0 / 64.3, two 41.1
-    // / 58.8; 5120 two 49.2 / 83.1, three 43.2 / 72.8; 8192 three 77.2 / 106.6,
-    // four 70.8 / 93.6).  K blocks an item: what 128 registers hold; with two
-    // tiles two blocks of bf16 fit as well and take as long as one.
-    const bool rest = a.T <= kRestTokens;
-    const int per_cu = (a.H + kDownRows * kCUs - 1) / (kDownRows * kCUs);
-    if (per_cu <= 1)
-        return rest ? launch_down<PER, 1, 2, true>(a, stream) : launch_down<PER, 1, 3, false>(a, stream);
-    if (per_cu <= 2)
-        return rest ? launch_down<PER, 2, 1, true>(a, stream) : launch_down<PER, 2, 1, false>(a, stream);
-    if (per_cu <= 3)
-        return rest ? launch_down<PER, 3, 1, true>(a, stream) : launch_down<PER, 3, 1, false>(a, stream);
-    return rest ? launch_down<PER, 4, 1, true>(a, stream) : launch_down<PER, 4, 1, false>(a, stream);
+    switch (down_tiles(a)) {
+    case 1: return down_blocks(a) == 2 ? launch_down<PER, 1, 2>(a, stream) : launch_down<PER, 1, 3>(a, stream);
+    case 2: return launch_down<PER, 2, 1>(a, stream);
+    case 3: return launch_down<PER, 3, 1>(a, stream);
+    default: return launch_down<PER, 4, 1>(a, stream);
+    }
 }
 
 template <int DT>

@@ -416,10 +416,10 @@ FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_
  *   logit, a gated SiLU layer in each, and the weighted sum:
  *
  *   y[t] = bf16( sum_j weights[t,j] * W2[e] h[t,j] ),  e = ids[t,j],
- *   h[t,j] = bf16( silu(Wg[e] x[t]) * (Wu[e] x[t]) ),
- *   with fp32 accumulation; the activations are not quantized.  Up to 8 tokens
- *   what the rounding of h leaves out is kept as well, so that the rounding of
- *   y is the error that remains (for |h| from 2^-19 to 2^11).
+ *   h[t,j] = silu(Wg[e] x[t]) * (Wu[e] x[t]),
+ *   with fp32 accumulation; the activations are not quantized, and h is kept in
+ *   fp16 with a power of two for every four columns (relative error 2^-11 over
+ *   fp32's range), so that the rounding of y is nearly all the error.
  *
  *   x[T,H]      in : bf16/fp16 activations (dtype as for fp8_quantize_act)
  *   logits[T,E] in : fp32 router logits.  -inf switches an expert off for a
