@@ -36,16 +36,18 @@ __device__ __forceinline__ float row16_max(float v)
 // 16 lanes own a 1 x 128 block, 8 values each, and keep it in registers
 // between its amax and its codes.  Cells (row, K block) are numbered row
 // first within chunks of RT rows, so that the scales of a chunk, stored
-// [K blocks, rows], are written next to each other.
+// [K blocks, rows], are written next to each other.  A row of the grid has
+// chunks_x chunks of per_chunk workgroups.
 constexpr int kQbThreads = 256;
 constexpr int kQbUnroll = 2;
 template <int DT, int RT>
 __global__ __launch_bounds__(kQbThreads) void quant_blocks_kernel(
-    const uint16_t* __restrict__ x, int64_t rows, int cols, int kblocks, int per_chunk,
+    const uint16_t* __restrict__ x, int64_t rows, int cols, int kblocks, int per_chunk, int chunks_x,
     uint8_t* __restrict__ q, float* __restrict__ scale)
 {
-    const int64_t chunk = blockIdx.x / per_chunk;
-    const int part = blockIdx.x - (int)(chunk * per_chunk);
+    const int chunk_x = blockIdx.x / per_chunk;
+    const int part = blockIdx.x - chunk_x * per_chunk;
+    const int64_t chunk = (int64_t)blockIdx.y * chunks_x + chunk_x;
     const int c8 = (threadIdx.x & 15) * 8;
     const int cell0 = part * (kQbThreads / 16) * kQbUnroll + (threadIdx.x >> 4);
     v4i v[kQbUnroll];
@@ -78,11 +80,12 @@ __global__ __launch_bounds__(kQbThreads) void quant_blocks_kernel(
 constexpr int kQwThreads = 256;
 template <int DT>
 __global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
-    const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int nblocks, int kblocks,
+    const uint16_t* __restrict__ w, int64_t rows, int64_t cols, int64_t cells, int nblocks, int kblocks,
     uint8_t* __restrict__ q, float* __restrict__ scale)
 {
     __shared__ float lds[kQwThreads / 64];
-    const int64_t cell = blockIdx.x;
+    const int64_t cell = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (cell >= cells) return;
     const int64_t bn = cell / kblocks;                   // batch * nblocks + row block
     const int kb = (int)(cell - bn * kblocks);
     const int64_t batch = bn / nblocks;
@@ -472,10 +475,11 @@ void gemm_block_kernel(const uint8_t* __restrict__ qa, const float* __restrict__
     const int wm = wave / WN, wn = wave % WN;
     const int r = lane & 15, g = lane >> 4;
 
-    const int tiles_m = (int)(((int64_t)M + BM - 1) / BM);
-    const int bid = xcd_remap(blockIdx.x, gridDim.x);
-    const int m0 = (bid % tiles_m) * BM;
-    const int n0 = (bid / tiles_m) * BN;
+    const uint32_t tiles_m = ((uint32_t)M + BM - 1) / BM, tiles_n = ((uint32_t)N + BN - 1) / BN;
+    const uint32_t bid = blockIdx.y * gridDim.x + xcd_remap(blockIdx.x, gridDim.x);
+    if (bid >= tiles_m * tiles_n) return;              // in the last of several rows of workgroups
+    const int m0 = (int)(bid % tiles_m) * BM;
+    const int n0 = (int)(bid / tiles_m) * BN;
     const int rows_m = min(BM, M - m0);
     const rsrc_t ra = make_rsrc(qa + (size_t)m0 * K, (uint32_t)(rows_m * K));
     const rsrc_t rw = make_rsrc(qw + (size_t)n0 * K, (uint32_t)(min(BN, N - n0) * K));
@@ -642,9 +646,10 @@ hipError_t launch_block_tile(const uint8_t* qa, const float* sa, const uint8_t* 
     if (const hipError_t e = set_lds_limit_once(reinterpret_cast<const void*>(kern), lds, attr_devices);
         e != hipSuccess)
         return e;
-    const int64_t grid = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    kern<<<(int)grid, WM * WN * 64, lds, stream>>>(qa, sa, qw, sw, y, M, N, K);
+    const int64_t tiles = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
+    if (tiles > 0x7fffffff) return hipErrorInvalidValue;     // y is larger than any memory
+    const int64_t gx = std::min(tiles, max_groups(WM * WN * 64)), gy = (tiles + gx - 1) / gx;
+    kern<<<dim3((unsigned)gx, (unsigned)gy), WM * WN * 64, lds, stream>>>(qa, sa, qw, sw, y, M, N, K);
     return hipGetLastError();
 }
 
@@ -654,11 +659,13 @@ hipError_t launch_quant_blocks_rt(const void* x, int64_t rows, int64_t cols, uin
 {
     const int64_t kblocks = blocks_of(cols);
     const int64_t cells = kblocks * RT, per_wg = kQbThreads / 16 * kQbUnroll;
-    const int64_t per_chunk = (cells + per_wg - 1) / per_wg;
-    const int64_t grid = per_chunk * ((rows + RT - 1) / RT);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    quant_blocks_kernel<DT, RT><<<(int)grid, kQbThreads, 0, stream>>>(
-        static_cast<const uint16_t*>(x), rows, (int)cols, (int)kblocks, (int)per_chunk, q, scale);
+    const int64_t per_chunk = (cells + per_wg - 1) / per_wg, chunks = (rows + RT - 1) / RT;
+    const int64_t chunks_x = std::min(chunks, max_groups(kQbThreads) / per_chunk);
+    const int64_t gy = (chunks + chunks_x - 1) / chunks_x;
+    if (gy > kMaxGroupRows) return hipErrorInvalidValue;
+    quant_blocks_kernel<DT, RT><<<dim3((unsigned)(per_chunk * chunks_x), (unsigned)gy), kQbThreads, 0, stream>>>(
+        static_cast<const uint16_t*>(x), rows, (int)cols, (int)kblocks, (int)per_chunk, (int)chunks_x, q,
+        scale);
     return hipGetLastError();
 }
 
@@ -683,15 +690,17 @@ hipError_t launch_quantize_weight_blocks(const void* w, int dtype, int64_t batch
                                          int64_t cols, uint8_t* q, float* scale, hipStream_t stream)
 {
     const int64_t nb = blocks_of(rows), kb = blocks_of(cols);
-    const int64_t grid = batch * nb * kb;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    const int64_t cells = batch * nb * kb;
+    const int64_t gx = std::min(cells, max_groups(kQwThreads)), gy = (cells + gx - 1) / gx;
+    if (gy > kMaxGroupRows) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)gx, (unsigned)gy);
     const auto* x = static_cast<const uint16_t*>(w);
     if (dtype == DT_BF16)
-        quant_weight_blocks_kernel<DT_BF16><<<(int)grid, kQwThreads, 0, stream>>>(
-            x, rows, cols, (int)nb, (int)kb, q, scale);
+        quant_weight_blocks_kernel<DT_BF16><<<grid, kQwThreads, 0, stream>>>(
+            x, rows, cols, cells, (int)nb, (int)kb, q, scale);
     else
-        quant_weight_blocks_kernel<DT_FP16><<<(int)grid, kQwThreads, 0, stream>>>(
-            x, rows, cols, (int)nb, (int)kb, q, scale);
+        quant_weight_blocks_kernel<DT_FP16><<<grid, kQwThreads, 0, stream>>>(
+            x, rows, cols, cells, (int)nb, (int)kb, q, scale);
     return hipGetLastError();
 }
 

@@ -529,6 +529,12 @@ inline hipError_t set_lds_limit_once(const void* kern, size_t lds, std::atomic<u
     return e;
 }
 
+// The workgroups one dimension of a launch takes: HIP counts its threads along
+// x in 32 bits, and of 2^32 and more it runs only what the lower bits say,
+// without an error.  Kernels with more workgroups take rows of them along y.
+constexpr int64_t max_groups(int threads) { return (((int64_t)1 << 32) - 1) / threads; }
+constexpr int64_t kMaxGroupRows = 65535;
+
 // Row-contiguous decode path for M <= kRowkMaxM (see linear.hip).
 constexpr int kRowkMaxM = 2;
 // Largest M*K the fused decode linear quantizes in LDS.
