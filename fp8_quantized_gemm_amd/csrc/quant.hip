@@ -506,11 +506,12 @@ constexpr int kRowVec = 4;
 
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void quant_rows_kernel(
-    const uint16_t* __restrict__ x, int64_t cols, uint8_t* __restrict__ q,
+    const uint16_t* __restrict__ x, int64_t rows, int64_t cols, uint8_t* __restrict__ q,
     float* __restrict__ scale, float* __restrict__ amax_out)
 {
     __shared__ float lds[kRowThreads / 64];
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    if (row >= rows) return;
     const int nvec = (int)(cols >> 3);                     // cols % 16 == 0
     const v4i* xv = reinterpret_cast<const v4i*>(x + row * cols);
     v2i* qv = reinterpret_cast<v2i*>(q + row * cols);
@@ -617,10 +618,12 @@ hipError_t launch_quantize_rows(const void* x, int dtype, int64_t rows, int64_t 
 {
     if (rows < 1 || rows > 0x7fffffff || cols < 16 || (cols & 15) != 0) return hipErrorInvalidValue;
     const uint16_t* xs = static_cast<const uint16_t*>(x);
+    const int64_t gx = std::min(rows, max_groups(kRowThreads));
+    const dim3 grid((unsigned)gx, (unsigned)((rows + gx - 1) / gx));
     if (dtype == DT_BF16)
-        quant_rows_kernel<DT_BF16><<<(unsigned)rows, kRowThreads, 0, stream>>>(xs, cols, q, scale, amax);
+        quant_rows_kernel<DT_BF16><<<grid, kRowThreads, 0, stream>>>(xs, rows, cols, q, scale, amax);
     else
-        quant_rows_kernel<DT_FP16><<<(unsigned)rows, kRowThreads, 0, stream>>>(xs, cols, q, scale, amax);
+        quant_rows_kernel<DT_FP16><<<grid, kRowThreads, 0, stream>>>(xs, rows, cols, q, scale, amax);
     return hipGetLastError();
 }
 
