@@ -385,7 +385,7 @@ hipError_t launch_f8(const uint8_t* qa, const float* sa, const uint8_t* qw, cons
         e != hipSuccess)
         return e;
     const int64_t grid = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > max_groups(WM * WN * 64)) return hipErrorInvalidConfiguration;
     kern<<<(int)grid, WM * WN * 64, lds, stream>>>(qa, sa, qw, sw, y, M, N, K, rowscale);
     return hipGetLastError();
 }
@@ -448,7 +448,7 @@ hipError_t launch_n16(const uint16_t* a, const uint8_t* hi, const uint8_t* lo, u
         e != hipSuccess)
         return e;
     const int64_t grid = (((int64_t)M + BM - 1) / BM) * (((int64_t)N + BN - 1) / BN);
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (grid > max_groups(WM * WN * 64)) return hipErrorInvalidConfiguration;
     kern<<<(int)grid, WM * WN * 64, lds, stream>>>(a, hi, lo, y, M, N, K);
     return hipGetLastError();
 }

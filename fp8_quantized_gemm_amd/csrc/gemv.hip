@@ -519,7 +519,9 @@ hipError_t launch_gemv_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw
 {
     const int64_t tiles = ((int64_t)N + 15) / 16;
     const dim3 block(kGemvWaves * 64), grid((unsigned)tiles);
-    if (wfmt == WF_E4M3 && outf == OUT_BF16 && tiles >= kGemvPairedTiles)
+    const bool paired = wfmt == WF_E4M3 && outf == OUT_BF16 && tiles >= kGemvPairedTiles;
+    if ((paired ? (tiles + 1) / 2 : tiles) > max_groups(kGemvWaves * 64)) return hipErrorInvalidConfiguration;
+    if (paired)
         gemv_f8_kernel<WF_E4M3, OUT_BF16, kGemvWaves, 1, CP_NT, 2>
             <<<dim3((unsigned)((tiles + 1) / 2)), block, 0, stream>>>(qa, sa, qw, sw, y, M, N, K, rowscale);
     else if (wfmt == WF_E4M3 && outf == OUT_BF16)
@@ -604,6 +606,7 @@ hipError_t launch_gemv_nested16(const uint16_t* a, const uint8_t* hi, const uint
                                 uint16_t* y, int M, int N, int K, int sp, hipStream_t stream)
 {
     const dim3 grid((unsigned)(((int64_t)N + 15) / 16)), block(kNestedWaves * 64);
+    if (grid.x > max_groups(kNestedWaves * 64)) return hipErrorInvalidConfiguration;
     if (sp == SP_E4M3)
         gemv_nested16_kernel<kNestedWaves, kNestedUnroll, CP_NT, SP_E4M3>
             <<<grid, block, 0, stream>>>(a, hi, lo, y, M, N, K);

@@ -592,6 +592,7 @@ hipError_t launch_rowk_fp8(const uint8_t* qa, const float* sa, const uint8_t* qw
 hipError_t launch_rowk_nested16(const uint16_t* a, const uint8_t* hi, const uint8_t* lo,
                                 uint16_t* y, int M, int N, int K, int sp, hipStream_t stream)
 {
+    if (rowk_grid(N) > max_groups(kThreads)) return hipErrorInvalidConfiguration;
     auto go = [&](auto mr, auto spc) {
         rowk_nested16_kernel<decltype(mr)::value, kRows, kUnroll, CP_NT, decltype(spc)::value>
             <<<rowk_grid(N), kThreads, 0, stream>>>(a, hi, lo, y, N, K);

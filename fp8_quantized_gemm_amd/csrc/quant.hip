@@ -675,7 +675,7 @@ hipError_t launch_quantize_kv(const void* x, int dtype, int64_t T, int64_t H, in
     const int64_t tpw = std::max<int64_t>(1, std::min<int64_t>(((int64_t)1 << 31) / dv, 8192 / D));
     const int64_t C64 = (T + tpw - 1) / tpw;
     const int64_t grid = H * C64;
-    if (C64 > 0x7fffffff || grid > 0x7fffffff) return hipErrorInvalidValue;
+    if (C64 > 0x7fffffff || grid > max_groups(kBigThreads)) return hipErrorInvalidConfiguration;
     const int C = (int)C64;
     // the partial maxima live in q until the quantization pass (H*C*4 <= T*H*D)
     float* part = reinterpret_cast<float*>(q);
@@ -687,9 +687,8 @@ hipError_t launch_quantize_kv(const void* x, int dtype, int64_t T, int64_t H, in
     // quantization: token-major for 256 .. 2048 vectors per token (two tokens
     // per workgroup), else head-major like the partial maxima
     const int64_t VT = H * dv;
-    if (VT >= kBigThreads && VT <= 8 * kBigThreads) {
+    if (VT >= kBigThreads && VT <= 8 * kBigThreads && (T + 1) / 2 <= max_groups(kBigThreads)) {
         const int64_t g2 = (T + 1) / 2;
-        if (g2 > 0x7fffffff) return hipErrorInvalidValue;
         auto go = [&](auto rpt) {
             constexpr int R = decltype(rpt)::value;
             if (dtype == DT_BF16)

@@ -33,7 +33,9 @@
  *    fp8_linear_delayed, fp8_linear_blockwise, nested_linear_fp8,
  *    nested_linear_fp8_e4m3) and of fp8_moe_blockwise, which may lie over
  *    their activation input (in place).
- *    A failed launch returns FP8Q_ERR_LAUNCH; faults inside a kernel surface
+ *    A failed launch returns FP8Q_ERR_LAUNCH, as does a product of so many
+ *    rows or columns (2^26 and more) that its kernel would have 2^32 threads
+ *    (the block-scaled product takes all sizes); faults inside a kernel surface
  *    at the caller's next synchronization, as for any HIP work.
  *  - Calls on different streams are independent (no shared mutable state).
  */
