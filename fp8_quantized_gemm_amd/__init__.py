@@ -14,7 +14,7 @@ _API = (
     "fp8_quantize_rows", "fp8_gemm_rowwise", "fp8_linear_rowwise",
     # a scale per block of 128: quantizers, GEMM, quantize + GEMM
     "fp8_quantize_blocks", "fp8_quantize_weight_blocks", "fp8_gemm_blockwise",
-    "fp8_linear_blockwise",
+    "fp8_linear_blockwise", "gemm_blockwise_kernel",
     # mixture-of-experts layer on block-scaled weights
     "fp8_moe_blockwise", "moe_work_bytes",
     # delayed scaling with an amax history

@@ -550,14 +550,6 @@ fp8q_status fp8_quantize_weight_blocks(const void* w, int dtype, int64_t batch, 
 }
 
 namespace {
-// The block-scaled product, dispatched on M like the FP8 GEMM.
-hipError_t dispatch_block(const uint8_t* qa, const float* sa, const uint8_t* qw, const float* sw,
-                          uint16_t* y, int64_t M, int64_t N, int64_t K, hipStream_t st)
-{
-    return M <= kGemvBlockMaxM ? launch_gemv_block(qa, sa, qw, sw, y, (int)M, (int)N, (int)K, st)
-                               : launch_tile_block(qa, sa, qw, sw, y, (int)M, (int)N, (int)K, st);
-}
-
 // The block-scaled kernels count rows and columns of tiles past M and N in 32
 // bits.
 constexpr int64_t kMaxBlockDim = (int64_t)1 << 30;
@@ -584,7 +576,13 @@ fp8q_status fp8_gemm_blockwise(const uint8_t* qa, const float* sa, const uint8_t
                           {qw, u64(N) * u64(K)}, {sw, weight_scale_bytes(N, K)}}));
     FP8Q_TRY(check_device());
     return finish("fp8_gemm_blockwise",
-                  dispatch_block(qa, sa, qw, sw, y, M, N, K, (hipStream_t)stream));
+                  launch_product_block(qa, sa, qw, sw, y, (int)M, (int)N, (int)K,
+                                       (hipStream_t)stream));
+}
+
+const char* fp8_gemm_blockwise_kernel(int64_t M, int64_t N, int64_t K)
+{
+    return check_block_sizes(M, N, K) == FP8Q_OK ? product_block_kernel((int)M, (int)N, (int)K) : "";
 }
 
 fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, const float* sw,
@@ -608,7 +606,8 @@ fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw, co
                       launch_linear_block_fused(x, dtype, qw, sw, y, q, sa, (int)M, (int)N, (int)K,
                                                 (hipStream_t)stream));
     hipError_t e = launch_quantize_blocks(x, dtype, M, K, q, sa, (hipStream_t)stream);
-    if (e == hipSuccess) e = dispatch_block(q, sa, qw, sw, y, M, N, K, (hipStream_t)stream);
+    if (e == hipSuccess)
+        e = launch_product_block(q, sa, qw, sw, y, (int)M, (int)N, (int)K, (hipStream_t)stream);
     return finish("fp8_linear_blockwise", e);
 }
 

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
     if (threadIdx.x == 0) scale[cell] = s;
 }
 
-// ---------------------------------------------------------------- decode product (M <= 16)
+// ---------------------------------------------------------------- weight-streaming product
 // The weight matrix is read once and bounds the time, so the loads are shaped
 // for it: a wave's load instruction reads the 128-byte lines of eight weight
 // rows, lane (r, g) = (l % 16, l / 16) the 16-byte unit 2 g + r % 2 of row r / 2,
@@ -132,7 +132,7 @@ __global__ __launch_bounds__(kQwThreads) void quant_weight_blocks_kernel(
 // loads); its waves interleave over the K blocks.  Tokens come in MT groups
 // of eight.  gemv_block_kernel, one workgroup per tile, serves the K that the
 // persistent kernel below does not hold, and products of more tokens that are
-// too small to fill the chip with LDS tiles (launch_tile_block).
+// too small to fill the chip with LDS tiles (pick_product).
 constexpr int kGbWaves = 16;
 
 __device__ __forceinline__ v4f mfma_pair(const v4i& w, const v4i& a, v4f c)
@@ -431,7 +431,7 @@ void gemv_block_persistent_kernel(const void* __restrict__ src, const uint8_t* _
     }
 }
 
-// ---------------------------------------------------------------- tile product (M > 16)
+// ---------------------------------------------------------------- tile product
 // The ring-buffered tile GEMM: BM x BN outputs per workgroup, K steps of 128
 // = one block, both operands and the step's activation scales brought to LDS
 // by direct global->LDS loads, AST stages for the activations and their
@@ -808,16 +808,6 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream)
 
 }  // namespace
 
-hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
-                             const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
-{
-    if (blocks_of(K) <= kPersistentMaxBlocks)
-        return launch_decode<SRC_CODES>({nullptr, const_cast<uint8_t*>(qa), const_cast<float*>(sa), qw,
-                                         sw, y, M, N, K}, stream);
-    return M <= 8 ? launch_gemv<1, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream)
-                  : launch_gemv<2, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
-}
-
 // Every workgroup reads and quantizes the whole activation, which grows with
 // its blocks, while a launch of its own for that costs the same always: up to
 // 192 blocks one launch is as fast or faster (K = 4096, M = 3: N = 2048 4.6
@@ -827,7 +817,7 @@ hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* 
 bool linear_block_fused_pays(int64_t M, int64_t N, int64_t K)
 {
     const int64_t cells = M * blocks_of(K);
-    return M <= kGemvBlockMaxM && blocks_of(K) <= kPersistentMaxBlocks &&
+    return M <= kDecodeBlockMaxM && blocks_of(K) <= kPersistentMaxBlocks &&
            cells <= (N * K > (int64_t)1 << 26 ? kFusedBlockMaxCells : kFusedBlockMaxCells * 3 / 4);
 }
 
@@ -855,28 +845,60 @@ constexpr TileShape kBlockShapes[] = {
     { 64,  64, 1, 11.0f},   // the same kernel, one workgroup per CU
 };
 
-hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
-                             const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
+namespace {
+
+// The kernel of a product.  Up to 16 tokens the weights are streamed, by the
+// persistent kernel as far as its K blocks reach.  More tokens on few outputs
+// are streamed too: LDS tiles leave most CUs idle there and walk K step by
+// step, so the streaming kernel, whose 16 waves share K, takes them wherever
+// its workgroups of 32 tokens by 16 or 32 columns are at most one per CU (N x
+// K = 4096 x 4096, M = 32: 13.1 -> 7.5 us, M = 64: 13.9 -> 10.2; 4096 x 11008,
+// M = 32: 28.8 -> 17.2, M = 64: 31.4 -> 21.4; 8192 x 4096, M = 32: 13.7 -> 11.8;
+// in two rounds it loses: 5120 x 5120, M = 32, 16 columns: 16.6 against 16.3,
+// 12288 x 4096, 32 columns: 20.5 against 16.7).  All others take a tile.
+enum Product : int { PERSISTENT, STREAM_8X16, STREAM_16X16, STREAM_32X16, STREAM_32X32, TILES };
+constexpr int kTileShapes = sizeof(kBlockShapes) / sizeof(kBlockShapes[0]);
+int pick_product(int M, int N, int K)
 {
-    // Few outputs: the tiles leave most CUs idle and walk K step by step, so the
-    // decode kernel, whose 16 waves share K, takes them wherever its workgroups
-    // of 32 tokens by 16 or 32 columns are at most one per CU (N x K = 4096 x
-    // 4096, M = 32: 13.1 -> 7.5 us, M = 64: 13.9 -> 10.2; 4096 x 11008, M = 32:
-    // 28.8 -> 17.2, M = 64: 31.4 -> 21.4; 8192 x 4096, M = 32: 13.7 -> 11.8; in
-    // two rounds it loses: 5120 x 5120, M = 32, 16 columns: 16.6 against 16.3,
-    // 12288 x 4096, 32 columns: 20.5 against 16.7).
+    if (M <= kDecodeBlockMaxM) {
+        if (blocks_of(K) <= kPersistentMaxBlocks) return PERSISTENT;
+        return M <= 8 ? STREAM_8X16 : STREAM_16X16;
+    }
     const int64_t groups = div_up(M, 32);
-    if (groups * div_up(N, 16) <= kCUs)
-        return launch_gemv<4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
-    if (groups * div_up(N, 32) <= kCUs)
-        return launch_gemv<4, 4, 1>(qa, sa, qw, sw, y, M, N, K, stream);
-    switch (pick_tile_shape(kBlockShapes, sizeof(kBlockShapes) / sizeof(kBlockShapes[0]), M, N)) {
-    case 0: return launch_block_tile<256, 256, 2, 4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
-    case 1: return launch_block_tile<256, 192, 2, 4, 2, 3>(qa, sa, qw, sw, y, M, N, K, stream);
-    case 2: return launch_block_tile<128, 256, 2, 4, 3, 3>(qa, sa, qw, sw, y, M, N, K, stream);
-    case 3: return launch_block_tile<128, 192, 2, 4, 3, 4>(qa, sa, qw, sw, y, M, N, K, stream);
-    case 4: return launch_block_tile<128, 128, 2, 4, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
-    case 5: return launch_block_tile<128, 64, 4, 2, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
+    if (groups * div_up(N, 16) <= kCUs) return STREAM_32X16;
+    if (groups * div_up(N, 32) <= kCUs) return STREAM_32X32;
+    return TILES + pick_tile_shape(kBlockShapes, kTileShapes, M, N);
+}
+
+}  // namespace
+
+const char* product_block_kernel(int M, int N, int K)
+{
+    static_assert(kTileShapes == 8, "a name for each");
+    constexpr const char* names[TILES + kTileShapes] = {
+        "persistent", "streaming 8x16", "streaming 16x16", "streaming 32x16", "streaming 32x32",
+        "tile 256x256", "tile 256x192", "tile 128x256", "tile 128x192", "tile 128x128", "tile 128x64",
+        "tile 64x64", "tile 64x64"};
+    return names[pick_product(M, N, K)];
+}
+
+hipError_t launch_product_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                                const float* sw, uint16_t* y, int M, int N, int K, hipStream_t stream)
+{
+    switch (pick_product(M, N, K)) {
+    case PERSISTENT:
+        return launch_decode<SRC_CODES>({nullptr, const_cast<uint8_t*>(qa), const_cast<float*>(sa), qw,
+                                         sw, y, M, N, K}, stream);
+    case STREAM_8X16: return launch_gemv<1, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
+    case STREAM_16X16: return launch_gemv<2, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
+    case STREAM_32X16: return launch_gemv<4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
+    case STREAM_32X32: return launch_gemv<4, 4, 1>(qa, sa, qw, sw, y, M, N, K, stream);
+    case TILES + 0: return launch_block_tile<256, 256, 2, 4, 2, 2>(qa, sa, qw, sw, y, M, N, K, stream);
+    case TILES + 1: return launch_block_tile<256, 192, 2, 4, 2, 3>(qa, sa, qw, sw, y, M, N, K, stream);
+    case TILES + 2: return launch_block_tile<128, 256, 2, 4, 3, 3>(qa, sa, qw, sw, y, M, N, K, stream);
+    case TILES + 3: return launch_block_tile<128, 192, 2, 4, 3, 4>(qa, sa, qw, sw, y, M, N, K, stream);
+    case TILES + 4: return launch_block_tile<128, 128, 2, 4, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
+    case TILES + 5: return launch_block_tile<128, 64, 4, 2, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
     default: return launch_block_tile<64, 64, 2, 2, 4, 4>(qa, sa, qw, sw, y, M, N, K, stream);
     }
 }

@@ -18,21 +18,19 @@ hipError_t launch_quantize_weight_blocks(const void* w, int dtype, int64_t batch
                                          hipStream_t stream);
 
 // The product of block-scaled codes, sa[K blocks, M] and sw[N blocks, K
-// blocks], M <= kGemvBlockMaxM on the weight-streaming kernel, larger M on
-// the MFMA tile kernel.
-constexpr int kGemvBlockMaxM = 16;
-hipError_t launch_gemv_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
-                             const float* sw, uint16_t* y, int M, int N, int K,
-                             hipStream_t stream);
+// blocks], on the kernel that product_block_kernel names: weight streaming up
+// to kDecodeBlockMaxM tokens and for few outputs, LDS tiles else.
+constexpr int kDecodeBlockMaxM = 16;
+hipError_t launch_product_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
+                                const float* sw, uint16_t* y, int M, int N, int K,
+                                hipStream_t stream);
+const char* product_block_kernel(int M, int N, int K);
 // Quantizer and product in one launch, taken where linear_block_fused_pays.
 constexpr int kFusedBlockMaxCells = 256; // 1 x 128 blocks of the activation
 bool linear_block_fused_pays(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear_block_fused(const void* x, int dtype, const uint8_t* qw, const float* sw,
                                      uint16_t* y, uint8_t* q, float* sa, int M, int N, int K,
                                      hipStream_t stream);
-hipError_t launch_tile_block(const uint8_t* qa, const float* sa, const uint8_t* qw,
-                             const float* sw, uint16_t* y, int M, int N, int K,
-                             hipStream_t stream);
 
 // A mixture-of-experts layer for a few tokens (see moe.hip).
 constexpr int kMoeMaxTokens = 64;

@@ -55,6 +55,7 @@ _SIGS = {
     "fp8_quantize_blocks": (_i, [_p, _i, _i64, _i64, _p, _p, _p]),
     "fp8_quantize_weight_blocks": (_i, [_p, _i, _i64, _i64, _i64, _p, _p, _p]),
     "fp8_gemm_blockwise": (_i, [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
+    "fp8_gemm_blockwise_kernel": (ctypes.c_char_p, [_i64, _i64, _i64]),
     "fp8_linear_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _i64, _i64, _i64, _p]),
     "fp8_moe_blockwise_work_bytes": (_i64, [_i64, _i64, _i64]),
     "fp8_moe_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64,
@@ -369,6 +370,11 @@ def fp8_gemm_blockwise(qa: torch.Tensor, sa: torch.Tensor, qw: torch.Tensor, sw:
         _ptr(sw, "sw", torch.float32, (_blocks(N), kb), index),
         _ptr(y, "y", torch.bfloat16, (M, N), index), M, N, K, stream))
     return y
+
+
+def gemm_blockwise_kernel(m: int, n: int, k: int) -> str:
+    """Name of the kernel that fp8_gemm_blockwise runs for these sizes, "" for sizes it refuses."""
+    return lib.fp8_gemm_blockwise_kernel(m, n, k).decode()
 
 
 def fp8_linear_blockwise(x: torch.Tensor, qw: torch.Tensor, sw: torch.Tensor,

@@ -408,6 +408,10 @@ FP8Q_API fp8q_status fp8_quantize_weight_blocks(const void* w, int dtype, int64_
 FP8Q_API fp8q_status fp8_gemm_blockwise(const uint8_t* qa, const float* sa, const uint8_t* qw,
                                         const float* sw, uint16_t* y, int64_t M, int64_t N,
                                         int64_t K, fp8q_stream stream);
+/* Name of the kernel that fp8_gemm_blockwise runs for these sizes ("persistent", "streaming
+ * 32x16", "tile 128x64", ...: tokens by columns), for profiles and tests; "" for sizes that it
+ * refuses.  A host function; the names may change. */
+FP8Q_API const char* fp8_gemm_blockwise_kernel(int64_t M, int64_t N, int64_t K);
 FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_t* qw,
                                           const float* sw, uint16_t* y, uint8_t* q, float* sa,
                                           int64_t M, int64_t N, int64_t K, fp8q_stream stream);
