@@ -3,6 +3,7 @@ that the GPU tests reach every one of them."""
 import pytest
 
 import test_gpu_block
+import test_gpu_block_tiles
 from fp8_quantized_gemm_amd import fp8q
 
 STREAMING = ["persistent", "streaming 8x16", "streaming 16x16", "streaming 32x16", "streaming 32x32"]
@@ -28,3 +29,11 @@ def test_gpu_tests_reach_every_kernel():
     lists = test_gpu_block.SHAPES + test_gpu_block.DECODE + test_gpu_block.FEW
     reached = {fp8q.gemm_blockwise_kernel(*size) for size in lists}
     assert reached >= set(STREAMING)
+
+
+def test_gpu_tests_run_every_tile_over_many_steps():
+    assert set(test_gpu_block_tiles.SIZES.values()) == set(TILES)
+    for (M, N), kernel in test_gpu_block_tiles.SIZES.items():
+        for K in test_gpu_block_tiles.DEPTHS:
+            assert fp8q.gemm_blockwise_kernel(M, N, K) == kernel
+    assert max(test_gpu_block_tiles.DEPTHS) >= 20 * 128
