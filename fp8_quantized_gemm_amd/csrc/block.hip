@@ -812,8 +812,12 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t stream)
 // its blocks, while a launch of its own for that costs the same always: up to
 // 192 blocks one launch is as fast or faster (K = 4096, M = 3: N = 2048 4.6
 // against 6.2 us, 16384 13.2 against 15.6; M = 6: N = 6144 8.7 both, 12288 11.8
-// against 12.7), with 256 only under a long stream of weights (M = 8: N =
-// 2048 6.9 against 6.2, 16384 15.4 against 15.3, 22016 19.9 against 20.1).
+// against 12.7).  With up to 256 it loses on few weights with many tokens (M =
+// 15, 4096 x 2048: 6.9 against 6.2; M = 13, 8192 x 2048: 7.8 against 7.6) and
+// wins under a long stream of them (above 2^26: M = 4, 16384 x 8064 24.2 against
+// 25.1; M = 7, 22016 x 4096 18.8 against 19.4; M = 12, 32768 x 2304 17.9 against
+// 18.5), the more the fewer blocks: all 256 are on a par (M = 8, K = 4096: N =
+// 16640 17.8 against 16.6, 20480 18.0 against 18.4, 27648 22.7 both).
 bool linear_block_fused_pays(int64_t M, int64_t N, int64_t K)
 {
     const int64_t cells = M * blocks_of(K);
@@ -832,7 +836,7 @@ hipError_t launch_linear_block_fused(const void* x, int dtype, const uint8_t* qw
 
 // Tile shapes of the block-scaled product and the measured time of one round
 // of their workgroups at K = 4096 (512 x 12288, and 333 x 4100 for the small
-// ones), picked like those of the FP8 GEMM.  256 x 128 took 41.9 us, more than
+// ones, three sets of operands in turn), picked like those of the FP8 GEMM.  256 x 128 took 41.9 us, more than
 // 128 x 256 for the same work.
 constexpr TileShape kBlockShapes[] = {
     {256, 256, 1, 58.6f},   // 8 waves of 128 x 64, 2 + 2 stages (130 KiB)

@@ -281,8 +281,8 @@ struct Layout {
 // u multiplies columns 16 u .. 16 u + 15 of a block with two MFMAs of eight
 // each; the first eights of all units come first, so that each of its two
 // loads reads whole 128-byte lines (with the columns in order it read 16 bytes
-// of every 32: moe_down at 64 tokens of 128 experts of 768 x 2048 58.4 us,
-// so 43.8).
+// of every 32: moe_down at 64 tokens of 128 experts of 768 x 2048, with h in
+// bf16, 58.4 us, so 43.8).
 // Rows are padded to whole blocks.
 __device__ __forceinline__ int h_position(int i)
 {
@@ -742,10 +742,10 @@ struct MoeWork {
 
 // moe_down's row tiles of eight columns, which share the loads of h: as many
 // as leave at most one workgroup per CU (1024 columns of h, 4 of 16 experts,
-// 8 / 40 tokens, microseconds a call: H = 2048 one 24.8 / 35.9, two 26.6 /
-// 38.4; 2560 one 34.9 / 53.4, two 29.4 / 43.8; 4096 one 46.0 / 64.3, two 41.1
-// / 58.8; 5120 two 49.2 / 83.1, three 43.2 / 72.8; 8192 three 77.2 / 106.6,
-// four 70.8 / 93.6), four at most.
+// 8 / 40 tokens, microseconds a call: H = 2048 one 26.0 / 37.9, two 27.1 /
+// 41.7; 2560 one 37.7 / 57.3, two 30.6 / 47.8; 4096 one 48.3 / 68.5, two 41.2
+// / 58.9; 5120 two 54.9 / 80.8, three 49.2 / 68.4; 8192 three 81.6 / 112,
+// four 72.9 / 95.1), four at most.
 inline int down_tiles(const MoeArgs& a)
 {
     return std::min((a.H + kDownRows * kCUs - 1) / (kDownRows * kCUs), 4);
@@ -789,8 +789,8 @@ hipError_t launch_down_cp(const MoeArgs& a, hipStream_t stream)
 }
 
 // Non-temporal weight loads where rows of W2 are whole 128-byte lines; else a
-// line is shared by two rows and has to stay for the second (H x I = 4096 x
-// 1392, 13 tokens: 35.5 against 32.4 us).
+// line is shared by two rows and has to stay for the second (4 of 32 experts
+// of 4096 x 1392, 13 tokens: 96.3 against 91.4 us a call).
 template <int PER, int RT, int BLOCKS>
 hipError_t launch_down(const MoeArgs& a, hipStream_t stream)
 {
