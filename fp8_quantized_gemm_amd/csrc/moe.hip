@@ -750,11 +750,11 @@ inline int down_tiles(const MoeArgs& a)
 {
     return std::min((a.H + kDownRows * kCUs - 1) / (kDownRows * kCUs), 4);
 }
-// Its K blocks an item: with one row tile what 128 registers hold, except
-// where the items are few (one token, 8 of 128, 2048 x 768: 16.5 against 16.8
-// us with three; 64 tokens 120 against 116); else one (two of them with two
-// tiles: 4096 x 1408, 2 of 8 experts, one token 14.6 -> 15.2, 64 tokens 63.5
-// -> 64.4).
+// Its K blocks an item.  With one row tile three, what 128 registers hold,
+// but two up to four tokens, where the items are few (one token, 8 of 128, 2048
+// x 768: two 16.5, three 16.8 us; 64 tokens 120 and 116).  With more row tiles
+// one (4096 x 1408, 2 of 8 experts, one token: one 14.6, two 15.2; 64 tokens
+// 63.5 and 64.4).
 inline int down_blocks(const MoeArgs& a) { return down_tiles(a) > 1 ? 1 : a.T <= 4 ? 2 : 3; }
 
 template <int DT, int PER, int R, int RT, int MT, int UB, int WAVES, int OCC, bool ROUTED>
