@@ -289,15 +289,19 @@ __device__ __forceinline__ int h_position(int i)
     return (i & ~127) | (i & 8) << 3 | (i >> 4 & 7) << 3 | (i & 7);
 }
 // h is kept in fp16 with a power of two for every four columns of a pair, the
-// exponent of the largest of them (which the stored values bring to [1, 2)):
-// two bytes a value, as in bf16, with 2^-11 instead of 2^-8 lost, over fp32's
-// whole range.  moe_down brings a block's values to its largest exponent.  In
-// bf16 the error of y is 1.4 times that of its own rounding, in this form 1.01
-// times.  64 tokens, 8 of 128 experts, 2048 x 768 take 115 us a call, 110 with
+// exponent of the largest of them: two bytes a value, as in bf16, with 2^-11
+// instead of 2^-8 lost, over fp32's whole range.  The stored values bring the
+// largest of the four to [2^kHStored, 2^(kHStored + 1)), and moe_down the largest
+// of a block to [2^kHTop, 2^(kHTop + 1)), the top of fp16 but one binade for
+// the rounding.  Values far below those are subnormal or gone: with half of kHTop
+// on either side (the factors are fp16 too) they are off by less than 2^-31 of
+// the block's largest.  In bf16 the error of y is 1.4 times that of its own
+// rounding, in this form 1.01 times.  64 tokens, 8 of 128 experts, 2048 x 768 take 115 us a call, 110 with
 // bf16 alone.  Two bf16 values for each h, the second for what the first
 // leaves out, lose less still, but moe_down is bound by its reads of h from
 // the L2: 129 us.
 constexpr int kHGroup = 4;
+constexpr int kHStored = 7, kHTop = 14;
 
 // The exponents of a pair, a byte a group: those of a 16-column unit in the
 // `blocks` (1 to 3) K blocks that moe_down takes at a time stand together, so
@@ -519,7 +523,7 @@ void moe_up_kernel(
                         uint32_t bits[L::kOut];
 #pragma unroll
                         for (int q = 0; q < L::kOut; ++q)
-                            bits[q] = f32_to_f16_bits(__builtin_ldexpf(hv[q], 127 - exponent));
+                            bits[q] = f32_to_f16_bits(__builtin_ldexpf(hv[q], 127 + kHStored - exponent));
                         if constexpr (L::kOut == 2)
                             *reinterpret_cast<uint32_t*>(dst) = bits[0] | bits[1] << 16;
                         else
@@ -613,7 +617,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
         top = max_xor32(max_xor16(top));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const _Float16 f = __builtin_amdgcn_ldexph((_Float16)1.0f, e4[i] - (int)top);
+            const _Float16 f = __builtin_amdgcn_ldexph((_Float16)(1 << (kHTop - kHStored)), e4[i] - (int)top);
             v4i& v = rows.v[c][i / 2];
 #pragma unroll
             for (int j = i % 2 * 2; j < i % 2 * 2 + 2; ++j) {
@@ -621,7 +625,7 @@ __global__ __launch_bounds__(kMoeThreads) void moe_down_kernel(
                 v[j] = __builtin_bit_cast(int, __builtin_bit_cast(v2h, two) * v2h{f, f});
             }
         }
-        return (int)top - 127;
+        return (int)top - 127 - kHTop;
     };
     struct Stage {
         v4i w[BLOCKS][RT];

@@ -425,7 +425,8 @@ FP8Q_API fp8q_status fp8_linear_blockwise(const void* x, int dtype, const uint8_
  *   h[t,j] = silu(Wg[e] x[t]) * (Wu[e] x[t]),
  *   with fp32 accumulation; the activations are not quantized, and h is kept in
  *   fp16 with a power of two for every four columns (relative error 2^-11 over
- *   fp32's range), so that the rounding of y is nearly all the error.
+ *   fp32's range, and 2^-31 of the largest |h| in its block of 128 columns),
+ *   so that the rounding of y is nearly all the error.
  *
  *   x[T,H]      in : bf16/fp16 activations (dtype as for fp8_quantize_act)
  *   logits[T,E] in : fp32 router logits.  -inf switches an expert off for a

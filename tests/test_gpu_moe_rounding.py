@@ -51,10 +51,10 @@ def _reference(x, logits, w13, s13, w2, s2, top_k):
     """y in 64 bits, how far a bf16 result may be from it, and y with h rounded to bf16.
 
     As block_ref.moe, but for h: an fp16 value with a power of two per four columns is off by at
-    most 2^-11 of itself where it is normal.  Columns below 2^-14 of the largest of their four are
-    subnormal (the largest is scaled to [1, 2), subnormals are 2^-24 apart), and once more those
-    below 2^-14 of the largest of their block, to whose power of two all are brought: 2^-25 of
-    that largest each."""
+    most 2^-11 of itself where it is normal.  The largest of the four is scaled to [2^7, 2^8), so
+    one that is subnormal (they are 2^-24 apart) is off by 2^-32 of the largest.  Brought to the power of
+    two of their block's largest, which comes to [2^14, 2^15), subnormals are off by 2^-39 of it; four
+    columns below 2^-31 of it are lost.  Together less than 2^-31 of the block's largest."""
     T, H = x.shape
     I = w2.shape[2]
     ids, weights, woff = ref.route(logits, top_k, True)
@@ -73,7 +73,7 @@ def _reference(x, logits, w13, s13, w2, s2, top_k):
         dh = dh + (2.0 ** -11 + 2.0 ** -20) * (np.abs(h) + dh)
         starts = np.arange(0, I, ref.B)
         top = np.maximum.reduceat(np.abs(h) + dh, starts, axis=1)
-        dh = dh + 2.0 ** -24 * np.repeat(top, ref.B, axis=1)[:, :I]
+        dh = dh + 2.0 ** -31 * np.repeat(top, ref.B, axis=1)[:, :I]
         w, dw = weights[t, j][:, None], woff[t, j][:, None]
         y[t] += w * (h @ wd.T)
         rough[t] += w * (_bf16(h) @ wd.T)
@@ -116,6 +116,30 @@ def test_low_bits_of_h_are_kept(T, E, H, I, top_k, exponent, dtype):
     say("moe low bits of h", T, E, H, I, top_k, exponent, dtype)
     got, _, _ = fp8q.fp8_moe_blockwise(xd.to(DEV), f32(logits), to_dev_u8(w[0]), f32(w[1]),
                                        to_dev_u8(w[2]), f32(w[3]), top_k)
+    bad = np.abs(got.double().cpu().numpy() - y) - off
+    assert np.all(bad <= 0), f"{(bad > 0).sum()} outside, worst by {bad.max()}"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,H,I", [(3, 272, 400), (12, 272, 400), (40, 2064, 272), (64, 512, 272)])
+def test_small_columns_beside_large_ones(T, H, I):
+    """A quarter of the columns of h are 2^17 times the others, and no row of W2 takes them: the
+    small ones keep their precision beside them."""
+    x, logits, w13, s13, w2, s2 = _case(T, 3, H, I, 2, 0, 5)
+    w13[:, 1, :, 3] = 0
+    w13[:, 1, :, H // 2] = 0x01                                    # 2^-9
+    w13[:, 1, ::4, H // 2] = 0x78                                  # 2^8
+    d = np.zeros((H, I), np.float32)
+    small = np.array([i for i in range(I) if i % 4])
+    np.add.at(d, (small % H, small), 1.0)
+    np.add.at(d, (small % H, (small + 36) // 4 * 4 % I + small % 4), -1.0)
+    w2[:] = oracle.e4m3_encode(d).reshape(1, H, I)
+    y, off, rough = _reference(x.astype(np.float64), logits, w13, s13, w2, s2, 2)
+    assert (np.abs(rough - y) > off).any()
+    f32 = lambda a: torch.from_numpy(a).to(DEV)
+    say("moe small beside large", T, H, I)
+    got, _, _ = fp8q.fp8_moe_blockwise(torch.from_numpy(x).to(torch.bfloat16).to(DEV), f32(logits),
+                                       to_dev_u8(w13), f32(s13), to_dev_u8(w2), f32(s2), 2)
     bad = np.abs(got.double().cpu().numpy() - y) - off
     assert np.all(bad <= 0), f"{(bad > 0).sum()} outside, worst by {bad.max()}"
 
