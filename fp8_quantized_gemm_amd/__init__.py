@@ -21,6 +21,8 @@ _API = (
     "DelayedScaling", "fp8_quantize_act_delayed", "fp8_linear_delayed",
     # FP8 KV-cache quantizer (one scale per head)
     "fp8_quantize_kv",
+    # paged FP8 KV cache: appending with rotation, attention
+    "fp8_kv_append", "fp8_paged_attention", "paged_attention_work", "paged_attention_work_bytes",
     # NestedFP: byte split, FP16 and FP8 modes
     "nested_split", "nested_rebuild_fp16", "nested_gemm_fp16", "nested_gemm_fp8",
     "nested_linear_fp8",

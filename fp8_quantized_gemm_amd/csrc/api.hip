@@ -3,6 +3,7 @@
 // GEMV) and the MFMA tile kernels (M > 16), and launch on the caller's stream.  No device memory is allocated and no host
 // synchronization happens in any call.
 #include <atomic>
+#include <cfloat>
 #include <cstdio>
 #include <cstring>
 
@@ -12,6 +13,7 @@
 #include "block.hpp"
 #include "common.hpp"
 #include "fp8q.h"
+#include "paged.hpp"
 
 using namespace fp8q;
 
@@ -647,6 +649,153 @@ fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* logits, con
     const MoeArgs a{x, logits, w13, s13, w2, s2, y, ids, weights, work, (int)T, (int)H, (int)I,
                     (int)E, (int)top_k, renormalize != 0};
     return finish("fp8_moe_blockwise", launch_moe(a, dtype, (hipStream_t)stream));
+}
+
+namespace {
+// Rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void* p;
+    uint64_t rows, width, stride;
+    Buf span() const { return Buf{p, p ? (rows - 1) * stride + width : 0}; }
+};
+
+// Rows of one stride may lie between each other, like q, k and v of one
+// projection; others must have spans apart.
+bool overlap(const Rows& a, const Rows& b)
+{
+    if (!overlap(a.span(), b.span())) return false;
+    if (a.stride != b.stride) return true;
+    const uintptr_t ab = reinterpret_cast<uintptr_t>(a.p), bb = reinterpret_cast<uintptr_t>(b.p);
+    const uint64_t d = ab < bb ? (bb - ab) % a.stride : (a.stride - (ab - bb) % a.stride) % a.stride;
+    return d < a.width || d + b.width > a.stride;        // b begins d bytes into a row of a
+}
+
+struct PagedBufs {
+    Buf k, v, ks, vs, table, start, lens;
+};
+PagedBufs paged_bufs(const fp8q_kv_cache& c, const fp8q_kv_batch& s)
+{
+    const uint64_t cells = u64(c.pages) * u64(c.kv_heads), codes = cells * u64(c.page_size) * u64(c.head_dim);
+    return PagedBufs{{c.k, codes}, {c.v, codes}, {c.k_scale, 4 * cells}, {c.v_scale, 4 * cells},
+                     {s.page_table, 4 * u64(s.seqs) * u64(s.table_width)},
+                     {s.q_start, 4 * (u64(s.seqs) + 1)}, {s.kv_lens, 4 * u64(s.seqs)}};
+}
+
+bool paged_head_dim_ok(int64_t D) { return D >= 16 && D <= kMaxHeadDim && D % 16 == 0; }
+
+fp8q_status check_paged(const fp8q_kv_cache* c, const fp8q_kv_batch* s)
+{
+    if (!c || !s || !c->k || !c->v || !c->k_scale || !c->v_scale || !s->page_table || !s->q_start ||
+        !s->kv_lens)
+        return FP8Q_ERR_NULL;
+    const int64_t P = c->page_size;
+    if (!(P == 16 || P == 32 || P == 64 || P == 128) || !paged_head_dim_ok(c->head_dim) ||
+        c->kv_heads < 1 || c->kv_heads > kMaxPagedHeads || c->pages < 1 || c->pages > kMaxDim ||
+        c->pages > ((int64_t)1 << 42) / (c->kv_heads * P * c->head_dim))
+        return FP8Q_ERR_SHAPE;
+    if (s->tokens < 1 || s->tokens > kMaxPagedTokens || s->seqs < 1 || s->seqs > kMaxPagedSeqs ||
+        s->max_q < 1 || s->max_q > s->tokens || s->table_width < 1 || s->table_width > kMaxPagedLen / P)
+        return FP8Q_ERR_SHAPE;
+    if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
+        !aligned4(s->page_table) || !aligned4(s->q_start) || !aligned4(s->kv_lens))
+        return FP8Q_ERR_ALIGN;
+    return FP8Q_OK;
+}
+
+// Row strides of 16-bit matrices [tokens, heads, D].
+bool stride_ok(int64_t stride, int64_t heads, int64_t D)
+{
+    return stride >= heads * D && stride <= ((int64_t)1 << 32) && stride % 8 == 0;
+}
+Rows rows_of(const void* p, int64_t tokens, int64_t heads, int64_t D, int64_t stride)
+{
+    return Rows{p, u64(tokens), 2 * u64(heads) * u64(D), 2 * u64(stride)};
+}
+Rows one_row(const Buf& b) { return Rows{b.p, 1, b.n, b.n}; }
+
+PagedBatch paged_batch(const fp8q_kv_batch& s)
+{
+    return PagedBatch{s.page_table, s.q_start, s.kv_lens, (int)s.tokens, (int)s.seqs,
+                      (int)s.table_width, (int)s.max_q};
+}
+}  // namespace
+
+fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int dtype,
+                          const float* rope, int64_t rope_rows, int64_t rope_dim, int interleaved,
+                          const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride,
+                          int64_t q_heads, fp8q_stream stream)
+{
+    if (!k || !v || (rope_dim != 0 && !rope) || (q == nullptr) != (q_out == nullptr))
+        return FP8Q_ERR_NULL;
+    if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
+    FP8Q_TRY(check_paged(cache, batch));
+    const int64_t D = cache->head_dim, Hk = cache->kv_heads, T = batch->tokens;
+    if (!stride_ok(k_stride, Hk, D) || !stride_ok(v_stride, Hk, D) || rope_dim < 0 || rope_dim > D ||
+        rope_dim % 16 != 0 ||
+        (rope_dim != 0 && (rope_rows < batch->table_width * cache->page_size || rope_rows > kMaxDim)))
+        return FP8Q_ERR_SHAPE;
+    if (q && (q_heads < 1 || q_heads > kMaxPagedHeads || !stride_ok(q_stride, q_heads, D) ||
+              !stride_ok(q_out_stride, q_heads, D)))
+        return FP8Q_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || (q && (!aligned16(q) || !aligned16(q_out))) ||
+        (rope_dim != 0 && !aligned16(rope)))
+        return FP8Q_ERR_ALIGN;
+    const PagedBufs p = paged_bufs(*cache, *batch);
+    const Buf brope{rope, rope_dim ? 4 * u64(rope_rows) * u64(rope_dim) : 0};
+    const Rows rk = rows_of(k, T, Hk, D, k_stride), rv = rows_of(v, T, Hk, D, v_stride);
+    FP8Q_TRY(check_apart({p.k, p.v, p.ks, p.vs}, {p.table, p.start, p.lens, brope, rk.span(), rv.span()}));
+    if (q) {
+        const Rows rq = rows_of(q, T, q_heads, D, q_stride), ro = rows_of(q_out, T, q_heads, D, q_out_stride);
+        FP8Q_TRY(check_apart({p.k, p.v, p.ks, p.vs}, {rq.span(), ro.span()}));
+        if (!(q_out == q && q_out_stride == q_stride) && overlap(ro, rq)) return FP8Q_ERR_OVERLAP;
+        for (const Rows& o : {rk, rv, one_row(p.table), one_row(p.start), one_row(p.lens)})
+            if (overlap(ro, o)) return FP8Q_ERR_OVERLAP;
+        if (brope.n != 0 && overlap(ro, one_row(brope))) return FP8Q_ERR_OVERLAP;
+    }
+    FP8Q_TRY(check_device());
+    const AppendArgs a{paged_batch(*batch), cache->k, cache->v, cache->k_scale, cache->v_scale,
+                       (const uint16_t*)k, (const uint16_t*)v, (const uint16_t*)q, (uint16_t*)q_out,
+                       rope, k_stride, v_stride, q_stride, q_out_stride, (int)cache->pages, (int)Hk,
+                       (int)cache->page_size, (int)D, q ? (int)q_heads : 0, (int)rope_dim,
+                       interleaved != 0};
+    return finish("fp8_kv_append", launch_kv_append(a, dtype, (hipStream_t)stream));
+}
+
+int64_t fp8_paged_attention_work_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                                       int64_t max_q)
+{
+    if (kv_heads < 1 || kv_heads > kMaxPagedHeads || q_heads < 1 || q_heads > kMaxPagedHeads ||
+        q_heads % kv_heads != 0 || !paged_head_dim_ok(head_dim) || max_q < 1 || max_q > kMaxPagedTokens)
+        return 0;
+    return attend_work_bytes(q_heads, kv_heads, head_dim, max_q);
+}
+
+fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch,
+                                const void* q, int64_t q_stride, int dtype, int64_t q_heads,
+                                float scale, int causal, int64_t window, uint16_t* y, float* lse,
+                                void* work, fp8q_stream stream)
+{
+    if (!q || !y || !work) return FP8Q_ERR_NULL;
+    if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
+    FP8Q_TRY(check_paged(cache, batch));
+    const int64_t D = cache->head_dim, Hk = cache->kv_heads, T = batch->tokens;
+    if (q_heads < 1 || q_heads > kMaxPagedHeads || q_heads % Hk != 0 || !stride_ok(q_stride, q_heads, D) ||
+        !(scale >= -FLT_MAX && scale <= FLT_MAX) || window < 0 || window > kMaxPagedLen ||
+        (window > 0 && !causal))
+        return FP8Q_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(y) || !aligned16(work) || !aligned4(lse)) return FP8Q_ERR_ALIGN;
+    const PagedBufs p = paged_bufs(*cache, *batch);
+    const Buf by{y, 2 * u64(T) * u64(q_heads) * u64(D)}, bl{lse, lse ? 4 * u64(T) * u64(q_heads) : 0},
+        bw{work, u64(fp8_paged_attention_work_bytes(q_heads, Hk, D, batch->max_q))};
+    FP8Q_TRY(check_apart({by, bl, bw}, {rows_of(q, T, q_heads, D, q_stride).span(), p.k, p.v, p.ks, p.vs,
+                                        p.table, p.start, p.lens}));
+    FP8Q_TRY(check_device());
+    const AttendArgs a{paged_batch(*batch), cache->k, cache->v, cache->k_scale, cache->v_scale,
+                       (const uint16_t*)q, y, lse, (float*)work, q_stride, (int)cache->pages, (int)Hk,
+                       (int)cache->page_size, (int)D, (int)q_heads, (int)(q_heads / Hk),
+                       scale * 1.4426950408889634f, causal != 0, (int)window};
+    return finish("fp8_paged_attention", launch_paged_attention(a, dtype, (hipStream_t)stream));
 }
 
 fp8q_status fp8q_e4m3_encode_f32(const float* v, uint8_t* q, int64_t n, fp8q_stream stream)

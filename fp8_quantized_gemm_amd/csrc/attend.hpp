@@ -1,0 +1,126 @@
+// What the attention kernels over the paged FP8 cache share.
+#pragma once
+
+#include "half.hpp"
+#include "paged.hpp"
+
+namespace fp8q {
+
+// The terms are kept as fp16(2^15 * term / largest term): fp16 then holds
+// terms down to 2^-29 of the largest with all its 11 bits.
+constexpr float kShift = 15.0f, kShiftScale = 0x1p15f;
+
+struct KeyRange {
+    int lo, hi;
+};
+// The keys that the new token i of a sequence sees.
+__device__ __forceinline__ KeyRange key_range(const AttendArgs& a, const PagedSeq& q, int i)
+{
+    const int pos = q.start + i;
+    KeyRange k{0, q.len};
+    if (a.causal) {
+        k.hi = clamp_int(pos + 1, 0, q.len);
+        if (a.window > 0) k.lo = clamp_int(pos - a.window + 1, 0, k.hi);
+    }
+    return k;
+}
+
+struct PageRef {
+    int64_t page;            // 0 where there is none, so that an address can be made of it
+    int inside;              // the token's place in its page
+    bool valid;
+};
+__device__ __forceinline__ PageRef page_ref(const AttendArgs& a, int b, int len, int key)
+{
+    const int slot = key / a.P;
+    const int id = key < len ? a.batch.page_table[(int64_t)b * a.batch.W + slot] : -1;
+    const bool valid = id >= 0 && id < a.pages;
+    return PageRef{valid ? id : 0, key - slot * a.P, valid};
+}
+
+// The E4M3 codes of NaN in four codes, as 0x80 in their bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
+{
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Terms of keys that a row does not see become 2^-inf.  Their values must not
+// count either, but 0 * NaN would: codes of NaN become 0 and, where a row does
+// see one, NaN is added to its sum.
+template <int ND>
+__device__ __forceinline__ void mask_tile(v4f (&s)[4], v4f (&acc)[ND], v4i (&vf)[ND],
+                                          const KeyRange& see, int key0, int g, bool valid)
+{
+    const float none = -__builtin_inff();
+    v8h seen[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 16 * g + 4 * i + e;
+            const bool in = valid && key >= see.lo && key < see.hi;
+            s[i][e] = in ? s[i][e] : none;
+            seen[i >> 1][(i & 1) * 4 + e] = in ? (_Float16)1.0f : (_Float16)0.0f;
+        }
+    uint32_t any = 0;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) any |= nan_bytes((uint32_t)vf[d][k]);
+    if (__ballot(any != 0) == 0) return;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        v4i one;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t n = nan_bytes((uint32_t)vf[d][k]), full = (n >> 7) * 255u;
+            vf[d][k] = (int)((uint32_t)vf[d][k] & ~full);
+            one[k] = (int)(full & 0x38383838u);            // E4M3 1.0 where NaN was
+        }
+        v4f hits = {0.f, 0.f, 0.f, 0.f};
+        hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(Half<DT_FP16>::widen(one[0], one[1]), seen[0],
+                                                      hits, 0, 0, 0);
+        hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(Half<DT_FP16>::widen(one[2], one[3]), seen[1],
+                                                      hits, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[d][e] += hits[e] > 0.f ? __builtin_nanf("") : 0.f;
+    }
+}
+
+// Several partial results of a row: the common maximum, the denominator over it.
+struct Joined {
+    float m, ref, l;
+};
+template <int ROWS>
+__device__ __forceinline__ Joined join(const float (*stat)[ROWS][2], int row, int count)
+{
+    Joined j;
+    j.m = -__builtin_inff();
+    for (int k = 0; k < count; ++k) j.m = fmaxf(j.m, stat[k][row][0]);
+    j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
+    j.l = 0.0f;
+    for (int k = 0; k < count; ++k)
+        j.l += stat[k][row][1] * __builtin_amdgcn_exp2f(stat[k][row][0] - j.ref);
+    return j;
+}
+
+// Four channels of a row from its sums, and the row's lse from its first channels.
+template <int DT>
+__device__ __forceinline__ void store_row(const AttendArgs& a, int64_t token, int head, int d, v4f o,
+                                          const Joined& j)
+{
+    const bool empty = j.l == 0.0f;         // not by the maximum, which skips NaN
+    const float f = empty ? 0.0f : 1.0f / (j.l * kShiftScale);
+    const int64_t row = token * a.Hq + head;
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float x = empty ? 0.0f : o[2 * i] * f, y = empty ? 0.0f : o[2 * i + 1] * f;
+        w[i] = f32_to_out_bits<DT>(x) | (f32_to_out_bits<DT>(y) << 16);
+    }
+    *reinterpret_cast<v2i*>(a.y + row * a.D + d) = v2i{(int)w[0], (int)w[1]};
+    if (d == 0 && a.lse != nullptr)
+        a.lse[row] = empty ? -__builtin_inff() : (j.ref + __builtin_amdgcn_logf(j.l)) * 0.6931471805599453f;
+}
+
+}  // namespace fp8q

@@ -1,0 +1,76 @@
+// The paged FP8 key/value cache: what the appending and the attention kernels
+// share, and their launchers.
+#pragma once
+
+#include "common.hpp"
+
+namespace fp8q {
+
+// A scale of the cache counts as the nearest value of this range (NaN as the
+// lowest): both ends and their reciprocals are normal fp32 numbers, and a sum of
+// 2^24 softmax terms, each divided by a scale, stays below fp32's largest.
+constexpr float kMinPageScale = 0x1p-100f, kMaxPageScale = 0x1p100f;
+constexpr int kMinPageExp = -100, kMaxPageExp = 100;
+__device__ __forceinline__ float page_scale(float s)
+{
+    return s > kMinPageScale ? (s < kMaxPageScale ? s : kMaxPageScale) : kMinPageScale;
+}
+
+constexpr int64_t kMaxHeadDim = 256;
+constexpr int64_t kMaxPagedLen = (int64_t)1 << 24;      // table_width * page_size
+constexpr int64_t kMaxPagedTokens = (int64_t)1 << 26;   // new tokens of a batch
+constexpr int64_t kMaxPagedSeqs = (int64_t)1 << 16;
+constexpr int64_t kMaxPagedHeads = 1024;
+
+struct PagedBatch {
+    const int* page_table;   // [B, W]
+    const int* q_start;      // [B + 1]
+    const int* kv_lens;      // [B]
+    int T, B, W, max_q;
+};
+
+// The new tokens of sequence b as the kernels take them from the batch's
+// arrays: n rows from `row` on, the first at position `start` (which may be
+// negative: a batch slot without a sequence), `len` tokens in the cache.  Rows
+// and lengths outside the batch's bounds are cut off, so that no value in the
+// arrays leads to an access out of bounds.
+struct PagedSeq {
+    int row, n, start, len;
+};
+__device__ __forceinline__ int clamp_int(int v, int lo, int hi) { return v < lo ? lo : (v > hi ? hi : v); }
+__device__ __forceinline__ PagedSeq paged_seq(const PagedBatch& s, int b, int page_size)
+{
+    const int r0 = clamp_int(s.q_start[b], 0, s.T), r1 = clamp_int(s.q_start[b + 1], r0, s.T);
+    const int len = clamp_int(s.kv_lens[b], 0, s.W * page_size);
+    return PagedSeq{r0, min(r1 - r0, s.max_q), len - (r1 - r0), len};
+}
+
+struct AppendArgs {
+    PagedBatch batch;
+    uint8_t *k_pages, *v_pages;      // [pages, Hk, P, D], [pages, Hk, D, P]
+    float *k_scale, *v_scale;        // [pages, Hk]
+    const uint16_t *k, *v, *q;       // [T, Hk, D], [T, Hk, D], [T, Hq, D] with row strides; q may be null
+    uint16_t* q_out;
+    const float* rope;               // [rows, R]
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    int pages, Hk, P, D, Hq, R, interleaved;
+};
+hipError_t launch_kv_append(const AppendArgs& a, int dtype, hipStream_t stream);
+
+struct AttendArgs {
+    PagedBatch batch;
+    const uint8_t *k_pages, *v_pages;
+    const float *k_scale, *v_scale;
+    const uint16_t* q;               // [T, Hq, D] with a row stride
+    uint16_t* y;                     // [T, Hq, D]
+    float* lse;                      // [T, Hq] or null
+    float* work;
+    int64_t q_stride;
+    int pages, Hk, P, D, Hq, group;
+    float scale_log2;                // softmax scale * log2(e)
+    int causal, window;
+};
+int64_t attend_work_bytes(int64_t Hq, int64_t Hk, int64_t D, int64_t max_q);
+hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream);
+
+}  // namespace fp8q

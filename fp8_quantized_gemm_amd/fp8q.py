@@ -27,6 +27,16 @@ _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i = ctypes.c_int
 
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("pages", _i64),
+                ("kv_heads", _i64), ("page_size", _i64), ("head_dim", _i64)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("page_table", _p), ("q_start", _p), ("kv_lens", _p), ("tokens", _i64),
+                ("seqs", _i64), ("table_width", _i64), ("max_q", _i64)]
+
+
 _SIGS = {
     "fp8q_abi_version": (_i, []),
     "fp8q_status_str": (ctypes.c_char_p, [_i]),
@@ -60,6 +70,11 @@ _SIGS = {
     "fp8_moe_blockwise_work_bytes": (_i64, [_i64, _i64, _i64]),
     "fp8_moe_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64,
                                _i64, _i, _p]),
+    "fp8_kv_append": (_i, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _p, _i64, _p, _i64,
+                           _i, _p, _i64, _i64, _i, _p, _i64, _p, _i64, _i64, _p]),
+    "fp8_paged_attention_work_bytes": (_i64, [_i64, _i64, _i64, _i64]),
+    "fp8_paged_attention": (_i, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _p, _i64, _i,
+                                 _i64, ctypes.c_float, _i, _i64, _p, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -453,6 +468,145 @@ def fp8_moe_blockwise(x: torch.Tensor, logits: torch.Tensor, w13: torch.Tensor,
 def moe_work_bytes(tokens: int, inter: int, top_k: int) -> int:
     """Bytes of scratch fp8_moe_blockwise needs (0 for sizes it refuses)."""
     return int(lib.fp8_moe_blockwise_work_bytes(tokens, inter, top_k))
+
+
+def _kv_cache(k_pages, v_pages, k_scale, v_scale, index: int) -> _KvCache:
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages must be [pages, kv_heads, page_size, head_dim], got "
+                         f"{tuple(k_pages.shape)}")
+    pages, heads, size, dim = k_pages.shape
+    return _KvCache(_ptr(k_pages, "k_pages", torch.uint8, (pages, heads, size, dim), index),
+                    _ptr(v_pages, "v_pages", torch.uint8, (pages, heads, dim, size), index),
+                    _ptr(k_scale, "k_scale", torch.float32, (pages, heads), index),
+                    _ptr(v_scale, "v_scale", torch.float32, (pages, heads), index),
+                    pages, heads, size, dim)
+
+
+def _kv_batch(page_table, q_start, kv_lens, tokens: int, max_q: int, index: int) -> _KvBatch:
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [seqs, width], got {tuple(page_table.shape)}")
+    seqs, width = page_table.shape
+    return _KvBatch(_ptr(page_table, "page_table", torch.int32, (seqs, width), index),
+                    _ptr(q_start, "q_start", torch.int32, (seqs + 1,), index),
+                    _ptr(kv_lens, "kv_lens", torch.int32, (seqs,), index),
+                    tokens, seqs, width, max_q)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, shape, index: int):
+    """Pointer and row stride of a [tokens, heads, head_dim] tensor whose rows may lie apart."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    tokens, heads, dim = shape
+    row, head, one = t.stride()
+    if t.numel() and ((dim > 1 and one != 1) or (heads > 1 and head != dim)):
+        raise ValueError(f"{name}: a row's heads must be contiguous, got strides {t.stride()}")
+    return t.data_ptr(), row if tokens > 1 else max(row, heads * dim)
+
+
+def fp8_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, page_table: torch.Tensor,
+                  q_start: torch.Tensor, kv_lens: torch.Tensor, max_q: int,
+                  rope: torch.Tensor | None = None, interleaved: bool = False,
+                  q: torch.Tensor | None = None, q_out: torch.Tensor | None = None):
+    """Appends a batch's new keys and values k, v [tokens, kv_heads, head_dim] (bf16/fp16) to a
+    paged FP8 cache, the keys rotated by their positions, and rotates the queries
+    q [tokens, q_heads, head_dim] likewise.
+
+    The cache: k_pages uint8 [pages, kv_heads, page_size, head_dim], v_pages uint8 [pages,
+    kv_heads, head_dim, page_size], k_scale and v_scale float32 [pages, kv_heads]; changed in
+    place.  A page's scale is a power of two, and grows with the page.  The batch (int32):
+    page_table [seqs, width] (-1: no page), q_start [seqs + 1], the first row of each sequence's
+    new tokens, kv_lens [seqs], the sequences' lengths with them; max_q, the most new tokens of
+    a sequence.  rope float32 [positions, R]: R/2 cosines, then R/2 sines of a position's angles
+    (interleaved: pairs are neighbours).  k, v, q may be slices of one projection's output;
+    q_out may be q.  Returns q_out (None without q)."""
+    code = _dtype_code(k)
+    index, stream = _where(k)
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("k, v and q must be [tokens, heads, head_dim]")
+    tokens = k.shape[0]
+    batch = _kv_batch(page_table, q_start, kv_lens, tokens, max_q, index)
+    shape = (tokens, cache.kv_heads, cache.head_dim)
+    rows, dim = 0, 0
+    if rope is not None:
+        if rope.dim() != 2:
+            raise ValueError(f"rope must be [positions, R], got {tuple(rope.shape)}")
+        rows, dim = rope.shape
+    heads, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qshape = (tokens, heads, cache.head_dim)
+        qp, qs = _rows(q, "q", k.dtype, qshape, index)
+        op, os_ = _rows(q_out, "q_out", k.dtype, qshape, index)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _check("fp8_kv_append", lib.fp8_kv_append(
+        cache, batch, *_rows(k, "k", k.dtype, shape, index), *_rows(v, "v", k.dtype, shape, index),
+        code, _ptr(rope, "rope", torch.float32, (rows, dim), index) if dim else None, rows, dim,
+        1 if interleaved else 0, qp, qs, op, os_, heads, stream))
+    return q_out
+
+
+def paged_attention_work_bytes(q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
+    """Bytes of scratch fp8_paged_attention needs (0 for sizes it refuses)."""
+    return int(lib.fp8_paged_attention_work_bytes(q_heads, kv_heads, head_dim, max_q))
+
+
+def paged_attention_work(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor,
+                         max_q: int) -> torch.Tensor:
+    """Scratch for fp8_paged_attention calls of these sizes.  Calls that may run at the same
+    time need one each, and so do captured graphs that may."""
+    need = paged_attention_work_bytes(q.shape[1], k_pages.shape[1], k_pages.shape[3], max_q)
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+
+
+def fp8_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                        k_scale: torch.Tensor, v_scale: torch.Tensor, page_table: torch.Tensor,
+                        q_start: torch.Tensor, kv_lens: torch.Tensor, max_q: int,
+                        scale: float | None = None, causal: bool = True, window: int = 0,
+                        y: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        work: torch.Tensor | None = None):
+    """softmax(scale * q k^T) v of a batch's new tokens over a paged FP8 cache (see fp8_kv_append
+    for the cache and the batch; their keys and values are appended before).
+
+    q [tokens, q_heads, head_dim] bf16/fp16; query head j reads key/value head j // (q_heads //
+    kv_heads).  scale: 1/sqrt(head_dim) when not given.  causal: a token sees those at or before
+    its position; window > 0: of these only the last `window`.  work is scratch (uint8,
+    allocated when not given; paged_attention_work).  Returns (y like q, lse float32 [tokens,
+    q_heads]); a row that sees no token gets zeros and -inf."""
+    code = _dtype_code(q)
+    index, stream = _where(q)
+    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
+    tokens, heads = q.shape[:2]
+    batch = _kv_batch(page_table, q_start, kv_lens, tokens, max_q, index)
+    shape = (tokens, heads, cache.head_dim)
+    if y is None:
+        y = torch.empty(shape, dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+    need = lib.fp8_paged_attention_work_bytes(heads, cache.kv_heads, cache.head_dim, max_q)
+    if work is None:
+        # never empty: sizes that need is 0 for are refused below, as sizes
+        work = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif work.numel() < need:
+        raise ValueError(f"work must hold at least {need} bytes, got {work.numel()}")
+    _check("fp8_paged_attention", lib.fp8_paged_attention(
+        cache, batch, *_rows(q, "q", q.dtype, shape, index), code, heads,
+        cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+        _ptr(y, "y", q.dtype, shape, index), _ptr(lse, "lse", torch.float32, (tokens, heads), index),
+        _ptr(work, "work", torch.uint8, work.shape, index), stream))
+    return y, lse
 
 
 class DelayedScaling:

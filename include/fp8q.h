@@ -458,6 +458,112 @@ FP8Q_API fp8q_status fp8_moe_blockwise(const void* x, int dtype, const float* lo
                                        int64_t top_k, int renormalize, fp8q_stream stream);
 
 /*
+ * The paged FP8 key/value cache: a pool of pages of P tokens that sequences of
+ * a batch take as they grow.  A page holds for each key/value head h the E4M3
+ * codes of its keys and of its values, and one fp32 scale for each of the two:
+ *   k[pages, kv_heads, P, D]   keys, a token's D values contiguous
+ *   v[pages, kv_heads, D, P]   values, a channel's P tokens contiguous
+ *   k_scale, v_scale[pages, kv_heads]   (a scale counts as the nearest value of
+ *                              2^-100 .. 2^100, NaN as the lowest)
+ *   P = 16, 32, 64 or 128;  16 <= D <= 256, D % 16 == 0;  1 <= kv_heads <= 1024;
+ *   1 <= pages <= 2^31-1 and pages*kv_heads*P*D <= 2^42.
+ */
+typedef struct {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages, kv_heads, page_size, head_dim;
+} fp8q_kv_cache;
+
+/*
+ * A batch of sequences with new tokens: the new tokens of sequence b are rows
+ * q_start[b] .. q_start[b+1]-1 of the batch's token matrices, n of them, and
+ * the i-th has the position kv_lens[b] - n + i.
+ *   page_table[seqs, table_width]  page of the tokens jP .. jP+P-1 of each
+ *                  sequence; an id outside 0 .. pages-1 is no page: tokens on it
+ *                  are neither stored nor seen
+ *   q_start[seqs+1] ascending, within 0 .. tokens
+ *   kv_lens[seqs]  tokens of each sequence, the new ones included (0: an idle
+ *                  slot of the batch); at most table_width * P count
+ *   max_q          no sequence has more new tokens than this; rows beyond it are
+ *                  left out
+ *   1 <= tokens <= 2^26;  1 <= seqs <= 65536;  1 <= max_q <= tokens;
+ *   table_width >= 1 and table_width * P <= 2^24.
+ * The arrays are device memory; the struct itself is read during the call.
+ */
+typedef struct {
+    const int32_t *page_table, *q_start, *kv_lens;
+    int64_t tokens, seqs, table_width, max_q;
+} fp8q_kv_batch;
+
+/*
+ * fp8_kv_append - the new tokens' keys and values into their pages, and their
+ *   queries rotated for the attention:
+ *
+ *   k, v[tokens, kv_heads, D], q[tokens, q_heads, D] in: bf16/fp16 bit patterns
+ *       (dtype as for fp8_quantize_act); rows k_stride, v_stride, q_stride values
+ *       apart, multiples of 8, so that they may be parts of one projection's
+ *       output.  q may be NULL (with q_out NULL): nothing is done for queries
+ *   rope[rope_rows, rope_dim] in: fp32; row p holds rope_dim/2 cosines, then
+ *       rope_dim/2 sines of the angles at position p.  Keys and queries are
+ *       rotated in their first rope_dim values: the pair (a, b) becomes
+ *       (a c - b s, b c + a s), each product and sum rounded to fp32.  Pair i is
+ *       (x[i], x[i + rope_dim/2]), or (x[2i], x[2i+1]) with interleaved != 0.
+ *       rope_dim % 16 == 0, 0 <= rope_dim <= D (0: no rotation, rope may be NULL);
+ *       rope_rows >= table_width * P
+ *   cache->k, v, k_scale, v_scale  in/out: a page and head that gains tokens gets
+ *       the scale s = 2^e, the smallest that |x| <= 448 s allows for them (e within
+ *       -100 .. 100; infinities and NaN do not count), and codes E4M3_rne_sat(x/s).
+ *       Where the page holds older tokens of the sequence s is never smaller than
+ *       its scale, and if it is larger their codes become
+ *       E4M3_rne(code * fl32(old/s)): with scales that are powers of two nothing
+ *       but bits below E4M3's smallest step is lost.  Other slots stay as they are
+ *   q_out[tokens, q_heads, D] out: rotated queries, rounded to dtype once, rows
+ *       q_out_stride values apart; may be q itself (with q's stride)
+ *   Rows outside q_start[0] .. q_start[seqs]-1 and tokens at negative positions are
+ *   left out.  Calls that append to one page must not overlap in time, and two
+ *   sequences of a call must not append to one page.  1 <= q_heads <= 1024.
+ *   One launch.
+ */
+FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch,
+                                   const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, int dtype, const float* rope,
+                                   int64_t rope_rows, int64_t rope_dim, int interleaved,
+                                   const void* q, int64_t q_stride, void* q_out,
+                                   int64_t q_out_stride, int64_t q_heads, fp8q_stream stream);
+
+/*
+ * fp8_paged_attention - attention of the new tokens' queries over the cached
+ *   keys and values; query head j reads key/value head j / (q_heads / kv_heads):
+ *
+ *   z[i,t] = scale * sum_d q[i,d] dec(k[t,d]) * k_scale
+ *   y[i]   = sum_t softmax_t(z[i,t]) * dec(v[t]) * v_scale
+ *   lse[i] = log(sum_t exp(z[i,t]))
+ *   over the tokens t of the sequence that are on a page and, with causal != 0,
+ *   at or before i's position p, with window > 0 (causal only) also p - t < window.
+ *   Products with the keys are exact and summed in fp32; softmax terms are
+ *   rounded to 11 bits for the product with the values, which is summed in fp32.
+ *
+ *   q[tokens, q_heads, D] in: bf16/fp16, rows q_stride values apart (a multiple of 8)
+ *   cache in: not changed
+ *   y[tokens, q_heads, D] out: of q's type, dense.  A row that sees no token gets
+ *       zeros (lse -inf); rows outside q_start[0] .. q_start[seqs]-1 are left as
+ *       they are
+ *   lse[tokens, q_heads]  out: fp32, natural logarithm; may be NULL
+ *   work   scratch of fp8_paged_attention_work_bytes bytes, 16-byte aligned;
+ *          contents before and after the call are of no meaning.  Calls that may
+ *          run at the same time need one each.
+ *   q_heads % kv_heads == 0, q_heads <= 1024;  scale finite;
+ *   0 <= window <= 2^24.
+ *   fp8_paged_attention_work_bytes gives 0 for sizes that the call refuses.
+ */
+FP8Q_API int64_t fp8_paged_attention_work_bytes(int64_t q_heads, int64_t kv_heads,
+                                                int64_t head_dim, int64_t max_q);
+FP8Q_API fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch,
+                                         const void* q, int64_t q_stride, int dtype,
+                                         int64_t q_heads, float scale, int causal, int64_t window,
+                                         uint16_t* y, float* lse, void* work, fp8q_stream stream);
+
+/*
  * fp8q_e4m3_encode_f32 - the device E4M3 encoder used by fp8_quantize_act,
  *   applied to binary32 values directly: q[i] = E4M3_rne_sat(v[i]).  n >= 1.
  *   Exported so the encoder can be checked exhaustively; not on the hot path.
