@@ -337,6 +337,7 @@ int64_t attend_work_bytes(int64_t, int64_t, int64_t D, int64_t)
 
 hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream)
 {
+    if ((int64_t)a.batch.max_q * a.group > 32) return launch_attend_prompt(a, dtype, stream);
     return dtype == DT_BF16 ? launch<DT_BF16>(a, stream) : launch<DT_FP16>(a, stream);
 }
 

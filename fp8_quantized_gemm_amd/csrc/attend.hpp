@@ -44,6 +44,27 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// Clears the codes of NaN in 16 codes; not 0 if there were any.
+__device__ __forceinline__ uint32_t clear_nan(v4i& v)
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t n = nan_bytes((uint32_t)v[k]);
+        v[k] = (int)((uint32_t)v[k] & ~((n >> 7) * 255u));
+        any |= n;
+    }
+    return any;
+}
+// E4M3 1.0 where NaN is in 16 codes, 0 elsewhere.
+__device__ __forceinline__ v4i nan_ones(const v4i& v)
+{
+    v4i one;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) one[k] = (int)((nan_bytes((uint32_t)v[k]) >> 7) * 0x38u);
+    return one;
+}
+
 // Terms of keys that a row does not see become 2^-inf.  Their values must not
 // count either, but 0 * NaN would: codes of NaN become 0 and, where a row does
 // see one, NaN is added to its sum.
@@ -70,13 +91,8 @@ __device__ __forceinline__ void mask_tile(v4f (&s)[4], v4f (&acc)[ND], v4i (&vf)
     if (__ballot(any != 0) == 0) return;
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-        v4i one;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t n = nan_bytes((uint32_t)vf[d][k]), full = (n >> 7) * 255u;
-            vf[d][k] = (int)((uint32_t)vf[d][k] & ~full);
-            one[k] = (int)(full & 0x38383838u);            // E4M3 1.0 where NaN was
-        }
+        const v4i one = nan_ones(vf[d]);
+        clear_nan(vf[d]);
         v4f hits = {0.f, 0.f, 0.f, 0.f};
         hits = __builtin_amdgcn_mfma_f32_16x16x32_f16(Half<DT_FP16>::widen(one[0], one[1]), seen[0],
                                                       hits, 0, 0, 0);

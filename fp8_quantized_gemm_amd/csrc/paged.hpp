@@ -70,6 +70,7 @@ struct AttendArgs {
     float scale_log2;                // softmax scale * log2(e)
     int causal, window;
 };
+hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream);
 int64_t attend_work_bytes(int64_t Hq, int64_t Hk, int64_t D, int64_t max_q);
 hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream);
 

@@ -1,0 +1,285 @@
+// Attention over the paged FP8 cache for many query rows: a workgroup takes
+// 128 rows (token, head of the group) of one key/value head, a wave 32 of them,
+// and goes through the keys in tiles of 64.
+//
+//   S^T = K Q^T   MFMA 32x32x16, keys along M, query rows along N
+//   P   = 2^(S^T * ks + lv - m)   in the lane of its row
+//   Y^T = V^T P   MFMA 32x32x16, channels along M
+//
+// The products run on 16-bit operands: E4M3 codes widen exactly to bf16 and
+// fp16.  A lane of S^T holds 16 consecutive keys of one row for each 32 keys
+// (the rows of K are put in LDS in the order that makes it so), which are the
+// lane's part of the second product's operand, so P needs no exchange between
+// lanes, and a row's maximum one.
+#include "attend.hpp"
+#include "tile.hpp"
+
+namespace fp8q {
+namespace {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+constexpr int kWaves = 4, kThreads = kWaves * 64, kWaveRows = 32, kTileRows = kWaves * kWaveRows;
+constexpr int kKeys = 64;                 // keys of a tile
+
+template <int DT>
+__device__ __forceinline__ v16f mfma32(typename Half<DT>::vec a, v4i b, v16f c)
+{
+    if constexpr (DT == DT_BF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(v8b, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(v8h, b), c, 0, 0, 0);
+}
+
+// 16 bytes of global memory for each active lane to lds_block + 16 * lane.
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* lds_block)
+{
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                     (__attribute__((address_space(3))) void*)lds_block, 16, 0, 0);
+}
+
+// Tiles in LDS.  Keys: row r of PITCH bytes is key 32 (r / 32) + key_of_row(r % 32), its 16-byte
+// units exchanged by row.  Values: a channel's 64 bytes, units exchanged as by swz64.
+__device__ __forceinline__ int key_of_row(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
+template <int DP>
+struct Tile {
+    static constexpr int kPitch = DP <= 64 ? 64 : (DP <= 128 ? 128 : 256);
+    static constexpr int kUnits = kPitch / 16;
+    static constexpr int kKeyBytes = kKeys * kPitch, kValueBytes = DP * kKeys;
+    static constexpr int kKeyBlocks = kKeyBytes / 1024, kValueBlocks = kValueBytes / 1024;
+    static __device__ __forceinline__ int swizzle(int row)
+    {
+        return kUnits == 4 ? (row >> 1) & 3 : row & (kUnits - 1);
+    }
+    static __device__ __forceinline__ int key_at(int row, int u) { return row * kPitch + ((u ^ swizzle(row)) << 4); }
+};
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_kernel(const AttendArgs a, int64_t units)
+{
+    using T = Tile<DP>;
+    constexpr int NC = DP / 32, ND = DP / 32;
+    constexpr int KB = T::kKeyBlocks / kWaves, VB = T::kValueBlocks / kWaves;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[2][T::kKeyBytes + T::kValueBytes];
+    __shared__ int found[kWaves];
+
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, hf = lane >> 5;
+    // units of kTileRows rows; those of sequence b begin at unit q_start[b] * group / kTileRows + b.
+    // The last ones first: under a causal mask they are the longest.
+    const int64_t index = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+    const int h = (int)(index % a.Hk);
+    const int64_t u = units - 1 - index / a.Hk;
+    if (u < 0) return;
+    int below = 0;
+    for (int b = tid; b < a.batch.B; b += kThreads)
+        below += (int64_t)clamp_int(a.batch.q_start[b], 0, a.batch.T) * a.group / kTileRows + b <= u ? 1 : 0;
+    const int b = max(block_sum_int<kThreads>(below, found) - 1, 0);
+    const PagedSeq q = paged_seq(a.batch, b, a.P);
+    const int64_t rows64 = (int64_t)q.n * a.group;
+    const int64_t row64 = (u - ((int64_t)q.row * a.group / kTileRows + b)) * kTileRows;
+    if (row64 < 0 || row64 >= rows64) return;
+    const int row0 = (int)row64, rows = (int)(rows64 - row64 < kTileRows ? rows64 - row64 : kTileRows);
+
+    const int wave_row0 = row0 + wave * kWaveRows;
+    const int my_row = wave_row0 + r, token = my_row / a.group, head = h * a.group + my_row % a.group;
+    const bool have_row = my_row < row0 + rows;
+    KeyRange see = key_range(a, q, token);
+    if (!have_row) see.lo = see.hi = 0;
+    const KeyRange first = key_range(a, q, row0 / a.group), last = key_range(a, q, (row0 + rows - 1) / a.group);
+    const bool idle = wave_row0 >= row0 + rows;
+    const int wave_last = min(wave_row0 + kWaveRows, row0 + rows) - 1;
+    const KeyRange wfirst = key_range(a, q, wave_row0 / a.group), wlast = key_range(a, q, wave_last / a.group);
+    const int t0 = first.lo / kKeys, t1 = (last.hi + kKeys - 1) / kKeys;
+
+    v4i qf[NC][2];
+    {
+        const uint16_t* src = a.q + (int64_t)(q.row + token) * a.q_stride + (int64_t)head * a.D;
+        const v4i zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int d = 32 * c + 16 * hf;
+            const bool have = have_row && d < a.D;
+            qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) : zero;
+            qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) : zero;
+        }
+    }
+    if (a.D < T::kPitch) {                // channels that no load fills
+        for (int i = tid; i < 2 * T::kKeyBytes / 16; i += kThreads)
+            *reinterpret_cast<v4i*>(&lds[i / (T::kKeyBytes / 16)][i % (T::kKeyBytes / 16) * 16]) = v4i{0, 0, 0, 0};
+        __syncthreads();
+    }
+
+    const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
+    const uint8_t* const kbase = a.k_pages + h * page_bytes;
+    const uint8_t* const vbase = a.v_pages + h * page_bytes;
+    const auto load_tile = [&](int t, uint8_t* dst) {
+        const int key0 = t * kKeys;
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+            const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
+            const int c = (unit % T::kUnits) ^ T::swizzle(row);
+            const PageRef p = page_ref(a, b, q.len, key0 + (row & 32) + key_of_row(row & 31));
+            if (16 * c < a.D)
+                load_lds16(kbase + p.page * pool_stride + (int64_t)p.inside * a.D + 16 * c,
+                           dst + (wave * KB + j) * 1024);
+        }
+#pragma unroll
+        for (int j = 0; j < VB; ++j) {
+            const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
+            const PageRef p = page_ref(a, b, q.len, key0 + 16 * g);
+            if (d < a.D)
+                load_lds16(vbase + p.page * pool_stride + (int64_t)d * a.P + p.inside,
+                           dst + T::kKeyBytes + (wave * VB + j) * 1024);
+        }
+    };
+
+    v16f acc[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
+
+    if (t0 < t1) load_tile(t0, lds[0]);
+    for (int t = t0; t < t1; ++t) {
+        const uint8_t* const kt = lds[(t - t0) & 1];
+        const uint8_t* const vt = kt + T::kKeyBytes;
+        wait_vm<0>();
+        __syncthreads();                  // tile t is there, and tile t - 1 has been read
+        if (t + 1 < t1) load_tile(t + 1, lds[(t + 1 - t0) & 1]);
+        const int key0 = t * kKeys;
+        if (idle || key0 >= wlast.hi || key0 + kKeys <= wfirst.lo) continue;   // no row of this wave sees the tile
+
+        v16f s[2];
+        float ks[2], lv[2], vs[2];
+        bool valid = true;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            const PageRef p = page_ref(a, b, q.len, key0 + 32 * tb + 16 * hf);
+            ks[tb] = page_scale(a.k_scale[p.page * a.Hk + h]) * a.scale_log2;
+            vs[tb] = page_scale(a.v_scale[p.page * a.Hk + h]);
+            lv[tb] = __builtin_amdgcn_logf(vs[tb]);
+            valid = valid && p.valid;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const v4i k = *reinterpret_cast<const v4i*>(kt + T::key_at(32 * tb + r, 2 * c + hf));
+                s[tb] = mfma32<DT>(Half<DT>::widen(k[0], k[1]), qf[c][0], s[tb]);
+                s[tb] = mfma32<DT>(Half<DT>::widen(k[2], k[3]), qf[c][1], s[tb]);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[tb][i] = __builtin_fmaf(s[tb][i], ks[tb], lv[tb]);
+        }
+        const bool whole = wfirst.lo <= key0 && wlast.lo <= key0 && wfirst.hi >= key0 + kKeys &&
+                           wlast.hi >= key0 + kKeys && __all(valid);
+        v8h seen[2][2];
+        if (!whole) {
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                const int k0 = key0 + 32 * tb + 16 * hf;
+                const bool on_page = page_ref(a, b, q.len, k0).valid;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const bool in = on_page && k0 + i >= see.lo && k0 + i < see.hi;
+                    s[tb][i] = in ? s[tb][i] : -__builtin_inff();
+                    seen[tb][i >> 3][i & 7] = in ? (_Float16)1.0f : (_Float16)0.0f;
+                }
+            }
+        }
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[tb][i]);
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m1 = fmaxf(m, top), ref = m1 == -__builtin_inff() ? 0.0f : m1;
+        if (__any(m1 > m)) {
+            const float alpha = __builtin_amdgcn_exp2f(m - ref);
+            l *= alpha;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[d] *= alpha;
+        }
+        m = m1;
+        v8h p[2][2];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float v = __builtin_amdgcn_exp2f(s[tb][i] - (ref - kShift));
+                sum += v;
+                p[tb][i >> 3][i & 7] = (_Float16)v;
+            }
+            l = __builtin_fmaf(sum, 1.0f / (vs[tb] * kShiftScale), l);
+        }
+        uint32_t any = 0;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb) {
+                v4i v = *reinterpret_cast<const v4i*>(vt + swz64(32 * d + r, 2 * tb + hf));
+                if (!whole) any |= clear_nan(v);
+                acc[d] = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[0], v[1]), __builtin_bit_cast(v4i, p[tb][0]), acc[d]);
+                acc[d] = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[2], v[3]), __builtin_bit_cast(v4i, p[tb][1]), acc[d]);
+            }
+        if (!whole && __ballot(any != 0) != 0) {
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                v16f hits;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) hits[i] = 0.0f;
+#pragma unroll
+                for (int tb = 0; tb < 2; ++tb) {
+                    const v4i v = *reinterpret_cast<const v4i*>(vt + swz64(32 * d + r, 2 * tb + hf));
+                    const v4i one = nan_ones(v);
+                    hits = mfma32<DT_FP16>(Half<DT_FP16>::widen(one[0], one[1]), __builtin_bit_cast(v4i, seen[tb][0]), hits);
+                    hits = mfma32<DT_FP16>(Half<DT_FP16>::widen(one[2], one[3]), __builtin_bit_cast(v4i, seen[tb][1]), hits);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[d][i] += hits[i] > 0.f ? __builtin_nanf("") : 0.f;
+            }
+        }
+    }
+
+    l += __shfl_xor(l, 32);
+    if (!have_row) return;
+    const Joined j{m, m == -__builtin_inff() ? 0.0f : m, l};
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int c = 32 * d + 8 * e + 4 * hf;
+            if (c < a.D)
+                store_row<DT>(a, q.row + token, head, c,
+                              v4f{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]}, j);
+        }
+}
+
+template <int DT, int DP>
+hipError_t launch(const AttendArgs& a, hipStream_t stream)
+{
+    const int64_t units = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
+    const int64_t groups = units * a.Hk, most = max_groups(kThreads), gx = groups < most ? groups : most;
+    hipLaunchKernelGGL((attend_prompt_kernel<DT, DP>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
+                       dim3(kThreads), 0, stream, a, units);
+    return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch(const AttendArgs& a, hipStream_t stream)
+{
+    if (a.D <= 64) return launch<DT, 64>(a, stream);
+    if (a.D <= 128) return launch<DT, 128>(a, stream);
+    if (a.D <= 192) return launch<DT, 192>(a, stream);
+    return launch<DT, 256>(a, stream);
+}
+
+}  // namespace
+
+hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream)
+{
+    return dtype == DT_BF16 ? launch<DT_BF16>(a, stream) : launch<DT_FP16>(a, stream);
+}
+
+}  // namespace fp8q
