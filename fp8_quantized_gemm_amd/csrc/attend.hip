@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
                 const int d = 64 * c + 16 * g;
                 const bool have = r < rows && d < a.D;
                 const v4i zero = {0, 0, 0, 0};
-                qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) : zero;
-                qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) : zero;
+                qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
+                qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
             }
         }
         v4f acc[ND];
@@ -181,8 +181,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
                 vf[d] = v4i{0, 0, 0, 0};
                 if (16 * d < a.D) vf[d] = *reinterpret_cast<const v4i*>(vt + (int64_t)(16 * d + r) * a.P);
             }
-            const float ks = page_scale(a.k_scale[vp.page * a.Hk + h]) * a.scale_log2;
-            const float vs = page_scale(a.v_scale[vp.page * a.Hk + h]);
+            const PageScales sc = page_scales(a, vp.page, h);
 
             v4f s[4];
 #pragma unroll
@@ -194,38 +193,40 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
                     s[i] = Half<DT>::mfma(Half<DT>::widen(kf[i][c][2], kf[i][c][3]), qf[c][1], s[i]);
                 }
             }
-            // x = log2 of the softmax term times the values' scale
-            const float lv = __builtin_amdgcn_logf(vs);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[i][e] = __builtin_fmaf(s[i][e], ks, lv);
             const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + 64 &&
                                last.hi >= key0 + 64 && __all(vp.valid);
             if (!whole) mask_tile<ND>(s, acc, vf, see, key0, g, vp.valid);
 
             float top = s[0][0];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
+            for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
+            top = __builtin_fmaf(top, sc.key, sc.log_value);
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float m1 = fmaxf(m, top), ref = m1 == -__builtin_inff() ? 0.0f : m1;
-            const float alpha = __builtin_amdgcn_exp2f(m - ref);
+            if (__any(top > m + kSlack)) {
+                const float m1 = fmaxf(m, top);
+                const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - m1);
+                l *= alpha;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) acc[d] *= alpha;
+                m = m1;
+            }
+            const float offset = sc.log_value - ((m == -__builtin_inff() ? 0.0f : m) - kShift);
             float sum = 0.0f;
             v8h p[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float v = __builtin_amdgcn_exp2f(s[i][e] - (ref - kShift));
-                    sum += v;
-                    p[i >> 1][(i & 1) * 4 + e] = (_Float16)v;
-                }
-            l = __builtin_fmaf(sum, 1.0f / (vs * kShiftScale), l * alpha);
-            m = m1;
+            for (int i = 0; i < 16; i += 2) {
+                const v2f v = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], sc.key, offset)),
+                               __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][(i & 3) + 1], sc.key, offset))};
+                sum += v[0];
+                sum += v[1];
+                const v2h w = __builtin_convertvector(v, v2h);
+                p[i >> 3][i & 7] = w[0];
+                p[i >> 3][(i & 7) + 1] = w[1];
+            }
+            l = __builtin_fmaf(sum, sc.inverse_value, l);
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
-                acc[d] *= alpha;
                 acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
                     Half<DT_FP16>::widen(vf[d][0], vf[d][1]), p[0], acc[d], 0, 0, 0);
                 acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(

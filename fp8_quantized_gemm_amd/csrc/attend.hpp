@@ -1,14 +1,18 @@
 // What the attention kernels over the paged FP8 cache share.
 #pragma once
 
+#include <float.h>
+
 #include "half.hpp"
 #include "paged.hpp"
 
 namespace fp8q {
 
-// The terms are kept as fp16(2^15 * term / largest term): fp16 then holds
-// terms down to 2^-29 of the largest with all its 11 bits.
-constexpr float kShift = 15.0f, kShiftScale = 0x1p15f;
+// A term is kept as fp16(2^kShift * term / reference).  The reference follows
+// the largest term only where that outgrows it by more than 2^kSlack, so that
+// the sums are seldom rescaled; fp16 then holds terms up to 2^15, and those
+// down to 2^-23 of the reference with all its 11 bits.
+constexpr float kSlack = 6.0f, kShift = 9.0f, kShiftScale = 0x1p9f;
 
 struct KeyRange {
     int lo, hi;
@@ -23,6 +27,20 @@ __device__ __forceinline__ KeyRange key_range(const AttendArgs& a, const PagedSe
         if (a.window > 0) k.lo = clamp_int(pos - a.window + 1, 0, k.hi);
     }
     return k;
+}
+
+// Scales of a page and head: a term is 2^(s * key + log_value) with s = q k^T,
+// times the values' scale, and counts inverse_value times that in the sum.
+struct PageScales {
+    float key, log_value, inverse_value;
+};
+__device__ __forceinline__ PageScales page_scales(const AttendArgs& a, int64_t page, int h)
+{
+    const int64_t cell = page * a.Hk + h;
+    const float v = page_scale(a.v_scale[cell]);
+    // never 0, which would make NaN of a masked key's -inf
+    const float k = fmaxf(page_scale(a.k_scale[cell]) * a.scale_log2, FLT_MIN);
+    return PageScales{k, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v) * (1.0f / kShiftScale)};
 }
 
 struct PageRef {

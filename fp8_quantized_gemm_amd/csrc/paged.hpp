@@ -67,7 +67,8 @@ struct AttendArgs {
     float* work;
     int64_t q_stride;
     int pages, Hk, P, D, Hq, group;
-    float scale_log2;                // softmax scale * log2(e)
+    float scale_log2;                // |softmax scale| * log2(e)
+    int q_flip;                      // sign bits of two queries where the scale is negative, else 0
     int causal, window;
 };
 hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream);

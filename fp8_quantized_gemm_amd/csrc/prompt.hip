@@ -54,6 +54,13 @@ struct Tile {
     static __device__ __forceinline__ int key_at(int row, int u) { return row * kPitch + ((u ^ swizzle(row)) << 4); }
 };
 
+__device__ __forceinline__ const uint8_t* shuffle(const uint8_t* p, int lane)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = (uint32_t)__shfl((int)(uint32_t)v, lane), hi = (uint32_t)__shfl((int)(v >> 32), lane);
+    return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
+}
+
 template <int DT, int DP>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_kernel(const AttendArgs a, int64_t units)
 {
@@ -99,8 +106,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         for (int c = 0; c < NC; ++c) {
             const int d = 32 * c + 16 * hf;
             const bool have = have_row && d < a.D;
-            qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) : zero;
-            qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) : zero;
+            qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
+            qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
         }
     }
     if (a.D < T::kPitch) {                // channels that no load fills
@@ -109,27 +116,26 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         __syncthreads();
     }
 
+    // A tile's keys in four groups of 16, each on one page; lane i of a wave keeps what is known of
+    // group i % 4.  The page ids are requested two tiles ahead, the scales and codes one.
     const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
-    const uint8_t* const kbase = a.k_pages + h * page_bytes;
-    const uint8_t* const vbase = a.v_pages + h * page_bytes;
-    const auto load_tile = [&](int t, uint8_t* dst) {
-        const int key0 = t * kKeys;
+    const int group_key = 16 * (lane & 3);
+    const auto load_tile = [&](int t, const PageRef& p, uint8_t* dst) {
+        const int64_t page_at = p.page * pool_stride + h * page_bytes;
+        const uint8_t* const kp = a.k_pages + page_at + (int64_t)p.inside * a.D;
+        const uint8_t* const vp = a.v_pages + page_at + p.inside;
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
             const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
-            const int c = (unit % T::kUnits) ^ T::swizzle(row);
-            const PageRef p = page_ref(a, b, q.len, key0 + (row & 32) + key_of_row(row & 31));
-            if (16 * c < a.D)
-                load_lds16(kbase + p.page * pool_stride + (int64_t)p.inside * a.D + 16 * c,
-                           dst + (wave * KB + j) * 1024);
+            const int c = (unit % T::kUnits) ^ T::swizzle(row), key = (row & 32) + key_of_row(row & 31);
+            const uint8_t* src = shuffle(kp, key >> 4) + (key & 15) * a.D + 16 * c;
+            if (16 * c < a.D) load_lds16(src, dst + (wave * KB + j) * 1024);
         }
 #pragma unroll
         for (int j = 0; j < VB; ++j) {
             const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
-            const PageRef p = page_ref(a, b, q.len, key0 + 16 * g);
-            if (d < a.D)
-                load_lds16(vbase + p.page * pool_stride + (int64_t)d * a.P + p.inside,
-                           dst + T::kKeyBytes + (wave * VB + j) * 1024);
+            const uint8_t* src = shuffle(vp, g) + d * a.P;
+            if (d < a.D) load_lds16(src, dst + T::kKeyBytes + (wave * VB + j) * 1024);
         }
     };
 
@@ -140,26 +146,30 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
     float m = -__builtin_inff(), l = 0.0f;
 
-    if (t0 < t1) load_tile(t0, lds[0]);
+    PageRef next = page_ref(a, b, q.len, t0 * kKeys + group_key);
+    if (t0 < t1) load_tile(t0, next, lds[0]);
+    PageScales next_scales = page_scales(a, next.page, h);
+    bool next_valid = next.valid;
+    next = page_ref(a, b, q.len, (t0 + 1) * kKeys + group_key);
     for (int t = t0; t < t1; ++t) {
         const uint8_t* const kt = lds[(t - t0) & 1];
         const uint8_t* const vt = kt + T::kKeyBytes;
         wait_vm<0>();
         __syncthreads();                  // tile t is there, and tile t - 1 has been read
-        if (t + 1 < t1) load_tile(t + 1, lds[(t + 1 - t0) & 1]);
+        const PageScales now = next_scales;
+        const bool valid = next_valid;
+        if (t + 1 < t1) {
+            load_tile(t + 1, next, lds[(t + 1 - t0) & 1]);
+            next_scales = page_scales(a, next.page, h);
+            next_valid = next.valid;
+            next = page_ref(a, b, q.len, (t + 2) * kKeys + group_key);
+        }
         const int key0 = t * kKeys;
         if (idle || key0 >= wlast.hi || key0 + kKeys <= wfirst.lo) continue;   // no row of this wave sees the tile
 
         v16f s[2];
-        float ks[2], lv[2], vs[2];
-        bool valid = true;
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
-            const PageRef p = page_ref(a, b, q.len, key0 + 32 * tb + 16 * hf);
-            ks[tb] = page_scale(a.k_scale[p.page * a.Hk + h]) * a.scale_log2;
-            vs[tb] = page_scale(a.v_scale[p.page * a.Hk + h]);
-            lv[tb] = __builtin_amdgcn_logf(vs[tb]);
-            valid = valid && p.valid;
 #pragma unroll
             for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
 #pragma unroll
@@ -168,8 +178,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
                 s[tb] = mfma32<DT>(Half<DT>::widen(k[0], k[1]), qf[c][0], s[tb]);
                 s[tb] = mfma32<DT>(Half<DT>::widen(k[2], k[3]), qf[c][1], s[tb]);
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[tb][i] = __builtin_fmaf(s[tb][i], ks[tb], lv[tb]);
         }
         const bool whole = wfirst.lo <= key0 && wlast.lo <= key0 && wfirst.hi >= key0 + kKeys &&
                            wlast.hi >= key0 + kKeys && __all(valid);
@@ -178,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
 #pragma unroll
             for (int tb = 0; tb < 2; ++tb) {
                 const int k0 = key0 + 32 * tb + 16 * hf;
-                const bool on_page = page_ref(a, b, q.len, k0).valid;
+                const bool on_page = __shfl(valid ? 1 : 0, 2 * tb + hf) != 0;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const bool in = on_page && k0 + i >= see.lo && k0 + i < see.hi;
@@ -187,31 +195,43 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
                 }
             }
         }
-        float top = -__builtin_inff();
+        // logarithms: a term is 2^(s * ks + lv), times the values' scale; one page a lane and block
+        float ks[2], lv[2], top[2];
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb)
+        for (int tb = 0; tb < 2; ++tb) {
+            ks[tb] = __shfl(now.key, 2 * tb + hf);
+            lv[tb] = __shfl(now.log_value, 2 * tb + hf);
+            top[tb] = s[tb][0];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) top = fmaxf(top, s[tb][i]);
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m1 = fmaxf(m, top), ref = m1 == -__builtin_inff() ? 0.0f : m1;
-        if (__any(m1 > m)) {
-            const float alpha = __builtin_amdgcn_exp2f(m - ref);
+            for (int i = 1; i < 16; ++i) top[tb] = fmaxf(top[tb], s[tb][i]);
+            top[tb] = __builtin_fmaf(top[tb], ks[tb], lv[tb]);
+        }
+        const float both = fmaxf(top[0], top[1]), highest = fmaxf(both, __shfl_xor(both, 32));
+        if (__any(highest > m + kSlack)) {
+            const float m1 = fmaxf(m, highest);
+            const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - m1);
             l *= alpha;
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[d] *= alpha;
+            m = m1;
         }
-        m = m1;
+        const float ref = m == -__builtin_inff() ? 0.0f : m;
         v8h p[2][2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
+            const float offset = lv[tb] - (ref - kShift);
             float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float v = __builtin_amdgcn_exp2f(s[tb][i] - (ref - kShift));
-                sum += v;
-                p[tb][i >> 3][i & 7] = (_Float16)v;
+            for (int i = 0; i < 16; i += 2) {
+                const v2f v = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i], ks[tb], offset)),
+                               __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i + 1], ks[tb], offset))};
+                sum += v[0];
+                sum += v[1];
+                const v2h w = __builtin_convertvector(v, v2h);
+                p[tb][i >> 3][i & 7] = w[0];
+                p[tb][i >> 3][(i & 7) + 1] = w[1];
             }
-            l = __builtin_fmaf(sum, 1.0f / (vs[tb] * kShiftScale), l);
+            l = __builtin_fmaf(sum, __shfl(now.inverse_value, 2 * tb + hf), l);
         }
         uint32_t any = 0;
 #pragma unroll

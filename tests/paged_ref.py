@@ -181,12 +181,12 @@ def attend(bt, q, scale, causal=True, window=0):
                     w = torch.exp(z - lse[r, j])
                     y[r, j] = w @ v[see]
                     mass = w @ v[see].abs()
-                    # a term is off by its logit's error, its rounding to 11 bits (or to 2^-40 of the
-                    # largest term times scale) and the exponential's; the denominator by the same
+                    # a term is off by its logit's error, its rounding to 11 bits (or, fp16's smallest
+                    # half step 2^-25 over 2^9, to 2^-34 of the largest term times scale) and the exponential's; the denominator by the same
                     # without the rounding; sums of fp32
                     rel = 2 * dz + 2.0 ** -11 + 2.0 ** -20 + len(w) * 2.0 ** -24
                     least = (torch.exp(z - z.max()) * clamp_scale(bt.vs[pg[see], h])).max() * \
-                        torch.exp(z.max() - lse[r, j]) * 448 * len(w) * 2.0 ** -40
+                        torch.exp(z.max() - lse[r, j]) * 448 * len(w) * 2.0 ** -34
                     ytol[r, j] = mass * rel + least + y[r, j].abs() * EPS[q.dtype] + TINY[q.dtype]
                     ltol[r, j] = dz + 2.0 ** -20 * (1 + lse[r, j].abs()) + len(w) * 2.0 ** -24
     return y, lse, ytol, ltol

@@ -152,6 +152,19 @@ def test_large_logits():
     run(bt, 8, torch.bfloat16, spread=30.0)
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30])
+def test_any_softmax_scale(scale):
+    """Negative (the sign goes to the queries), zero and tiny: masked keys stay masked."""
+    say("softmax scale", scale)
+    for new, lens in (([1, 1], [70, 130]), ([70, 3], [100, 90])):
+        bt = ref.Batch(new, lens, 2, 64, 32, seed=20)
+        q = bt.values(4, torch.float16)
+        want = ref.attend(bt, q, scale)
+        got = call(on_gpu(bt), q.to(DEV), bt.max_q, scale=scale)
+        torch.cuda.synchronize()
+        compare(bt, q, got, want)
+
+
 def test_pages_that_are_none():
     """Tokens on ids outside the pool are not seen; a sequence of nothing else gets zeros."""
     bt = ref.Batch([1, 3, 1, 20], [150, 70, 40, 60], 2, 64, 16, seed=10)
