@@ -6,20 +6,24 @@ namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 constexpr int kRows = 16;                 // query rows of a unit: (token, head of the group) pairs
-constexpr int kMinTiles = 4;              // key tiles that a workgroup takes at least
+constexpr int kKeys = 64;                 // keys of a tile
+// Two workgroups on each of 256 CUs, one from 192 channels on (registers).
+constexpr int groups_for(int dp) { return dp <= 128 ? 512 : 256; }
+constexpr int kMinShare = 3;              // what a wave takes at least
 
-// The work is a list of units (sequence, key/value head, row tile), each a run
-// of 64-token key tiles; workgroup w takes tiles [w * share, (w + 1) * share)
-// of the whole list.
-struct Share {
-    int64_t begin, end;
-};
-
+// The work is a list of units (sequence, key/value head, row tile), each a run of
+// key tiles with one place before them for what a unit costs by itself; wave i
+// of the grid takes the places [i * share, (i + 1) * share) of the whole list.
+// That evens out any mixture of lengths, and is computed from the batch's arrays
+// by every workgroup, so the host needs no lengths and a graph can be replayed
+// with others.  A wave stores the units that it has whole; the pieces of the
+// others are joined in LDS, and those of units that several workgroups have by
+// attend_join_kernel.
 struct SeqWork {
     PagedSeq q;
     int tile0, tiles;                     // key tiles that some row of the sequence sees
     int row_tiles;
-    int units;                            // key/value heads x row tiles
+    __device__ __forceinline__ int64_t places(int Hk) const { return (int64_t)row_tiles * Hk * (tiles + 1); }
 };
 
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b)
@@ -27,111 +31,116 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b)
     SeqWork w;
     w.q = paged_seq(a.batch, b, a.P);
     const KeyRange first = key_range(a, w.q, 0), last = key_range(a, w.q, w.q.n - 1);
-    w.tile0 = first.lo >> 6;
-    w.tiles = max(((last.hi + 63) >> 6) - w.tile0, 1);
+    w.tile0 = first.lo / kKeys;
+    w.tiles = max((last.hi + kKeys - 1) / kKeys - w.tile0, 1);
     w.row_tiles = (w.q.n * a.group + kRows - 1) / kRows;
-    w.units = w.row_tiles * a.Hk;
     return w;
 }
 
 struct ScanLds {
-    int64_t wave[kWaves];
-    int64_t before;
-    int b;
+    int64_t sums[kWaves];
+    int64_t before[kWaves];
+    int seq[kWaves];
 };
 
-// Tiles of all sequences (the return value) and, for the tile `at`, the sequence that
-// holds it and the tiles before that sequence.  Every thread sums a run of sequences.
-template <class F>
-__device__ __forceinline__ int64_t scan_sequences(const AttendArgs& a, ScanLds& lds, F pick)
+__device__ __forceinline__ int64_t share_of(int64_t total, int waves)
+{
+    const int64_t s = (total + waves - 1) / waves;
+    return s > kMinShare ? s : kMinShare;
+}
+
+// Places of all sequences, and for the first place of each of the workgroup's waves the
+// sequence that holds it and the places before that sequence.  Every thread sums a run of
+// sequences.
+__device__ __forceinline__ int64_t scan_sequences(const AttendArgs& a, ScanLds& lds)
 {
     const int B = a.batch.B, per = (B + kThreads - 1) / kThreads, lane = threadIdx.x & 63;
     const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        const SeqWork w = seq_work(a, b);
-        mine += (int64_t)w.units * w.tiles;
-    }
+    for (int b = b0; b < b1; ++b) mine += seq_work(a, b).places(a.Hk);
     int64_t sum = mine;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
         const int64_t up = __shfl_up(sum, off);
         if (lane >= off) sum += up;
     }
-    if (lane == 63) lds.wave[threadIdx.x >> 6] = sum;
-    if (threadIdx.x == 0) lds.b = B;
+    if (lane == 63) lds.sums[threadIdx.x >> 6] = sum;
     __syncthreads();
     int64_t total = 0, before = sum - mine;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-        if (w < (int)(threadIdx.x >> 6)) before += lds.wave[w];
-        total += lds.wave[w];
+        if (w < (int)(threadIdx.x >> 6)) before += lds.sums[w];
+        total += lds.sums[w];
     }
-    const int64_t at = pick(total);
-    if (at >= before && at < before + mine) {
+    const int64_t share = share_of(total, gridDim.x * kWaves);
+    for (int w = 0; w < kWaves; ++w) {
+        const int64_t at = ((int64_t)blockIdx.x * kWaves + w) * share;
+        if (at < before || at >= before + mine) continue;
+        int64_t from = before;
         for (int b = b0; b < b1; ++b) {
-            const SeqWork w = seq_work(a, b);
-            const int64_t n = (int64_t)w.units * w.tiles;
-            if (at < before + n) {
-                lds.b = b;
-                lds.before = before;
+            const int64_t n = seq_work(a, b).places(a.Hk);
+            if (at < from + n) {
+                lds.seq[w] = b;
+                lds.before[w] = from;
                 break;
             }
-            before += n;
+            from += n;
         }
     }
     __syncthreads();
     return total;
 }
 
-__device__ __forceinline__ int64_t share_of(int64_t total, int groups)
-{
-    const int64_t s = (total + groups - 1) / groups;
-    return s > kMinTiles ? s : kMinTiles;
-}
-
-// The scratch of G workgroups: for each the unit that it begins and another one
-// ends (parts = 0: none), then two partial results for each, of a unit that it
-// goes on with and of one that it begins: kRows rows of maximum, denominator and,
-// from the fifth float on, DP sums.
+// A piece of a unit that its wave has not whole; parts: how many workgroups have some of it.
 struct Unit {
-    int parts, token0, head, row0, rows, unused[3];
+    int64_t at;                           // the unit's first place
+    int parts, begins, ends, token0, head, row0, rows, unused;
 };
+
+// The scratch: for each workgroup the unit that it begins and another one ends (parts = 0:
+// none), then its two partial results, of a unit that it goes on with and of one that it
+// begins: kRows rows of maximum, denominator and, from the fifth float on, DP sums.
 template <int DP>
 __device__ __forceinline__ float* part_of(float* work, int groups, int64_t group, bool begins)
 {
     return work + groups * (int)(sizeof(Unit) / 4) + (group * 2 + (begins ? 1 : 0)) * (kRows * (DP + 4));
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
 template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kernel(const AttendArgs a)
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_rows_kernel(const AttendArgs a)
 {
     constexpr int NC = DP / 64, ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
     __shared__ ScanLds scan;
-    __shared__ float stat[kWaves][kRows][2];
-    __shared__ __attribute__((aligned(16))) float part[kWaves * kRows * RS];
+    __shared__ Unit piece[2 * kWaves];
+    __shared__ float stat[2 * kWaves][kRows][2];
+    __shared__ __attribute__((aligned(16))) float sums[2 * kWaves][kRows * RS];
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-    const int W = gridDim.x;
-    const int64_t total = scan_sequences(
-        a, scan, [&](int64_t t) { return (int64_t)blockIdx.x * share_of(t, W); });
-    const int64_t share = share_of(total, W);
-    int64_t at = blockIdx.x * share;
+    const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const int64_t total = uniform(scan_sequences(a, scan)), share = share_of(total, gridDim.x * kWaves);
+    int64_t at = ((int64_t)blockIdx.x * kWaves + wave) * share;
     const int64_t end = at + share < total ? at + share : total;
-    bool told = false;                    // in thread 0: a unit is left for the joining kernel
-    int b = scan.b;
-    int64_t seq_at = scan.before;
+    if (lane < 2) piece[2 * wave + lane].rows = 0;
+    int b = at < end ? uniform(scan.seq[wave]) : 0;
+    int64_t seq_at = at < end ? uniform(scan.before[wave]) : 0;
     const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
 
     while (at < end) {
         const SeqWork w = seq_work(a, b);
-        const int64_t seq_tiles = (int64_t)w.units * w.tiles;
-        if (at >= seq_at + seq_tiles) { seq_at += seq_tiles; ++b; continue; }
-        const int unit = (int)((at - seq_at) / w.tiles);
-        const int64_t unit_at = seq_at + (int64_t)unit * w.tiles;
-        const int t0 = (int)(at - unit_at);
-        const int t1 = (int)(end - unit_at < w.tiles ? end - unit_at : w.tiles);
+        const int64_t seq_places = w.places(a.Hk);
+        if (at >= seq_at + seq_places) { seq_at += seq_places; ++b; continue; }
+        const int unit = (int)((at - seq_at) / (w.tiles + 1));
+        const int64_t unit_at = seq_at + (int64_t)unit * (w.tiles + 1);
+        const int t0 = max((int)(at - unit_at) - 1, 0);
+        const int t1 = (int)(end - unit_at - 1 < w.tiles ? end - unit_at - 1 : w.tiles);
+        at = unit_at + w.tiles + 1;
+        if (t0 >= t1) continue;                             // only the place before the tiles
         const int h = unit / w.row_tiles, row0 = unit % w.row_tiles * kRows;
         const int rows = min(kRows, w.q.n * a.group - row0);
 
@@ -158,8 +167,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
         for (int d = 0; d < ND; ++d) acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
         float m = -__builtin_inff(), l = 0.0f;
 
-        for (int t = t0 + wave; t < t1; t += kWaves) {
-            const int key0 = (w.tile0 + t) << 6;
+        for (int t = t0; t < t1; ++t) {
+            const int key0 = (w.tile0 + t) * kKeys;
             // key rows of the first product are read by row group, values by lane group
             const PageRef kp = page_ref(a, b, w.q.len, key0 + 16 * (r >> 2));
             const PageRef vp = page_ref(a, b, w.q.len, key0 + 16 * g);
@@ -173,8 +182,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
                 for (int c = 0; c < NC; ++c) {
                     const int d = 64 * c + 16 * g;
                     kf[i][c] = v4i{0, 0, 0, 0};
-                    if (d < a.D)
-                        kf[i][c] = *reinterpret_cast<const v4i*>(kt + 4 * i * a.D + d);
+                    if (d < a.D) kf[i][c] = *reinterpret_cast<const v4i*>(kt + 4 * i * a.D + d);
                 }
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
@@ -193,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
                     s[i] = Half<DT>::mfma(Half<DT>::widen(kf[i][c][2], kf[i][c][3]), qf[c][1], s[i]);
                 }
             }
-            const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + 64 &&
-                               last.hi >= key0 + 64 && __all(vp.valid);
+            const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + kKeys &&
+                               last.hi >= key0 + kKeys && __all(vp.valid);
             if (!whole) mask_tile<ND>(s, acc, vf, see, key0, g, vp.valid);
 
             float top = s[0][0];
@@ -220,9 +228,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
                                __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][(i & 3) + 1], sc.key, offset))};
                 sum += v[0];
                 sum += v[1];
-                const v2h w = __builtin_convertvector(v, v2h);
-                p[i >> 3][i & 7] = w[0];
-                p[i >> 3][(i & 7) + 1] = w[1];
+                const v2h w2 = __builtin_convertvector(v, v2h);
+                p[i >> 3][i & 7] = w2[0];
+                p[i >> 3][(i & 7) + 1] = w2[1];
             }
             l = __builtin_fmaf(sum, sc.inverse_value, l);
 #pragma unroll
@@ -234,89 +242,138 @@ __global__ void __launch_bounds__(kThreads, DP <= 192 ? 2 : 1) attend_rows_kerne
             }
         }
 
-        // the waves' results together; l is spread over the lane groups
-        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 16);                             // the lane groups had keys of their own
         l += __shfl_xor(l, 32);
-        if (g == 0) { stat[wave][r][0] = m; stat[wave][r][1] = l; }
-        float* mine = part + (wave * kRows + r) * RS + 4 * g;
+        if (t0 == 0 && t1 == w.tiles) {
+            const Joined j{m, m == -__builtin_inff() ? 0.0f : m, l};
+            if (r < rows)
 #pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(mine + 16 * d) = acc[d];
-        __syncthreads();
-        const bool all = t0 == 0 && t1 == w.tiles;
-        if (t0 == 0 && t1 < w.tiles && threadIdx.x == 0) {
-            const int64_t last_group = (unit_at + w.tiles - 1) / share;
-            told = true;
-            reinterpret_cast<Unit*>(a.work)[blockIdx.x] =
-                Unit{(int)(last_group - blockIdx.x) + 1, w.q.row, h, row0, rows, {0, 0, 0}};
-        }
-        float* out = part_of<DP>(a.work, W, blockIdx.x, t0 == 0);
-        const int quads = a.D / 4;
-        for (int i = threadIdx.x; i < rows * quads; i += kThreads) {
-            const int row = i / quads, d = i % quads * 4;
-            const Joined j = join(stat, row, kWaves);
-            v4f o = {0.f, 0.f, 0.f, 0.f};
+                for (int d = 0; d < ND; ++d)
+                    if (16 * d < a.D) store_row<DT>(a, w.q.row + token, head, 16 * d + 4 * g, acc[d], j);
+        } else {
+            const int slot = 2 * wave + (t0 == 0 ? 1 : 0);
+            if (g == 0) { stat[slot][r][0] = m; stat[slot][r][1] = l; }
 #pragma unroll
-            for (int k = 0; k < kWaves; ++k)
-                o += *reinterpret_cast<const v4f*>(part + (k * kRows + row) * RS + d) *
-                     __builtin_amdgcn_exp2f(stat[k][row][0] - j.ref);
-            if (all) {
-                const int gr = row0 + row, at_head = h * a.group + gr % a.group;
-                store_row<DT>(a, w.q.row + gr / a.group, at_head, d, o, j);
-            } else {
-                *reinterpret_cast<v4f*>(out + row * (DP + 4) + 4 + d) = o;
-                if (d == 0) { out[row * (DP + 4)] = j.m; out[row * (DP + 4) + 1] = j.l; }
+            for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[slot][r * RS + 16 * d + 4 * g]) = acc[d];
+            if (lane == 0) {
+                const int64_t w0 = (unit_at + 1) / share / kWaves, w1 = (unit_at + w.tiles) / share / kWaves;
+                piece[slot] = Unit{unit_at, (int)(w1 - w0) + 1, t0 == 0, t1 == w.tiles, w.q.row, h, row0, rows, 0};
             }
         }
-        __syncthreads();
-        at = unit_at + t1;
+    }
+
+    // pieces of one unit lie next to each other, in order
+    __syncthreads();
+    bool told = false;
+    for (int p0 = 0; p0 < 2 * kWaves;) {
+        const Unit u = piece[p0];
+        int p1 = p0 + 1;
+        if (u.rows == 0) { p0 = p1; continue; }
+        int ends = u.ends;
+        for (int p = p1; p < 2 * kWaves; ++p) {
+            if (piece[p].rows == 0) continue;
+            if (piece[p].at != u.at) break;
+            ends = piece[p].ends;
+            p1 = p + 1;
+        }
+        const bool all = u.begins && ends;
+        float* out = part_of<DP>(a.work, gridDim.x, blockIdx.x, u.begins);
+        if (u.begins && !ends) {
+            told = true;
+            if (threadIdx.x == 0) reinterpret_cast<Unit*>(a.work)[blockIdx.x] = u;
+        }
+        const int quads = a.D / 4;
+        for (int i = threadIdx.x; i < u.rows * quads; i += kThreads) {
+            const int row = i / quads, d = i % quads * 4;
+            Joined j{-__builtin_inff(), 0.0f, 0.0f};
+            for (int p = p0; p < p1; ++p)
+                if (piece[p].rows != 0) j.m = fmaxf(j.m, stat[p][row][0]);
+            j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
+            v4f o = {0.f, 0.f, 0.f, 0.f};
+            for (int p = p0; p < p1; ++p)
+                if (piece[p].rows != 0) {
+                    const float f = __builtin_amdgcn_exp2f(stat[p][row][0] - j.ref);
+                    j.l += stat[p][row][1] * f;
+                    o += *reinterpret_cast<const v4f*>(&sums[p][row * RS + d]) * f;
+                }
+            if (all) {
+                const int gr = u.row0 + row;
+                store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, j);
+            } else {
+                *reinterpret_cast<v4f*>(out + row * RS + 4 + d) = o;
+                if (d == 0) { out[row * RS] = j.m; out[row * RS + 1] = j.l; }
+            }
+        }
+        p0 = p1;
     }
     if (threadIdx.x == 0 && !told) reinterpret_cast<Unit*>(a.work)[blockIdx.x].parts = 0;
 }
 
 // Joins the partial results of a unit that several workgroups had, told by the
-// first of them: a workgroup for each row, its waves taking turns at the parts.
+// first of them: a workgroup for each row.  D / 4 threads have a share of the
+// parts; the factors of all parts come first, so that no load waits for another.
 template <int DT, int DP>
 __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a)
 {
-    __shared__ float stat[kWaves][1][2];
-    __shared__ __attribute__((aligned(16))) float part[kWaves][DP];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = blockIdx.y;
+    constexpr int kGroups = groups_for(DP);
+    __shared__ float factor[kGroups], red[2][kWaves];
+    __shared__ __attribute__((aligned(16))) float sums[kThreads * 4];
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const Unit u = reinterpret_cast<const Unit*>(a.work)[blockIdx.x];
     if (u.parts == 0 || row >= u.rows) return;
-    float m = -__builtin_inff(), l = 0.0f;
-    v4f o = {0.f, 0.f, 0.f, 0.f};
-    const int d = 4 * lane;
-    for (int k = wave; k < u.parts; k += kWaves) {
-        const float* p = part_of<DP>(a.work, gridDim.x, blockIdx.x + k, k == 0) + row * (DP + 4);
-        const float pm = p[0], pl = p[1], m1 = fmaxf(m, pm), ref = m1 == -__builtin_inff() ? 0.0f : m1;
-        const float f0 = __builtin_amdgcn_exp2f(m - ref), f1 = __builtin_amdgcn_exp2f(pm - ref);
-        l = l * f0 + pl * f1;
-        if (d < a.D) o = o * f0 + *reinterpret_cast<const v4f*>(p + 4 + d) * f1;
-        m = m1;
-    }
-    if (lane == 0) { stat[wave][0][0] = m; stat[wave][0][1] = l; }
-    if (d < a.D) *reinterpret_cast<v4f*>(&part[wave][d]) = o;
-    __syncthreads();
-    if (wave != 0 || d >= a.D) return;
-    const Joined j = join(stat, 0, kWaves);
-    o = v4f{0.f, 0.f, 0.f, 0.f};
+    // parts lie two partial results apart, but the first, which begins the unit
+    const float* const first = part_of<DP>(a.work, gridDim.x, blockIdx.x, true) + row * (DP + 4);
+    const float* const other = part_of<DP>(a.work, gridDim.x, blockIdx.x, false) + row * (DP + 4);
+    constexpr int64_t step = 2 * kRows * (DP + 4);
+    constexpr int kEach = (kGroups + kThreads - 1) / kThreads;
+    float pm[kEach], pl[kEach], m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k)
-        o += *reinterpret_cast<const v4f*>(&part[k][d]) * __builtin_amdgcn_exp2f(stat[k][0][0] - j.ref);
+    for (int e = 0; e < kEach; ++e) {
+        const int k = tid + e * kThreads;
+        const float* p = k == 0 ? first : other + k * step;
+        pm[e] = k < u.parts ? p[0] : -__builtin_inff();
+        pl[e] = k < u.parts ? p[1] : 0.0f;
+        m = fmaxf(m, pm[e]);
+    }
+    m = wave_max(m);
+    if (lane == 0) red[0][wave] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red[0][w]);
+    const float ref = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int k = tid + e * kThreads;
+        const float f = __builtin_amdgcn_exp2f(pm[e] - ref);
+        if (k < u.parts) { factor[k] = f; l += pl[e] * f; }
+    }
+    l = wave_sum(l);
+    if (lane == 0) red[1][wave] = l;
+    __syncthreads();
+    const int quads = a.D / 4, sets = kThreads / quads, set = tid / quads, d = tid % quads * 4;
+    v4f o = {0.f, 0.f, 0.f, 0.f};
+    if (set < sets) {
+#pragma unroll 4
+        for (int k = set; k < u.parts; k += sets)
+            o += *reinterpret_cast<const v4f*>((k == 0 ? first : other + k * step) + 4 + d) * factor[k];
+        *reinterpret_cast<v4f*>(&sums[4 * tid]) = o;
+    }
+    __syncthreads();
+    if (set != 0) return;
+    for (int k = 1; k < sets; ++k) o += *reinterpret_cast<const v4f*>(&sums[4 * (k * quads + tid)]);
+    const Joined j{m, ref, red[1][0] + red[1][1] + red[1][2] + red[1][3]};
     const int gr = u.row0 + row;
     store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, j);
 }
 
-constexpr int kGroups = 512;              // two workgroups on each of 256 CUs
-
 template <int DT, int DP>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((attend_rows_kernel<DT, DP>), dim3(kGroups), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attend_rows_kernel<DT, DP>), dim3(groups_for(DP)), dim3(kThreads), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int rows = a.batch.max_q < kRows / a.group ? a.batch.max_q * a.group : kRows;
-    hipLaunchKernelGGL((attend_join_kernel<DT, DP>), dim3(kGroups, rows), dim3(kThreads), 0, stream, a);
+    hipLaunchKernelGGL((attend_join_kernel<DT, DP>), dim3(groups_for(DP), rows), dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -333,7 +390,8 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
 
 int64_t attend_work_bytes(int64_t, int64_t, int64_t D, int64_t)
 {
-    return (int64_t)kGroups * ((int64_t)sizeof(Unit) + 2 * kRows * ((D + 63) / 64 * 64 + 4) * 4);
+    const int64_t dp = (D + 63) / 64 * 64;
+    return groups_for((int)dp) * ((int64_t)sizeof(Unit) + 2 * kRows * (dp + 4) * 4);
 }
 
 hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream)

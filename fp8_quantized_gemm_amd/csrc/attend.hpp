@@ -121,23 +121,10 @@ __device__ __forceinline__ void mask_tile(v4f (&s)[4], v4f (&acc)[ND], v4i (&vf)
     }
 }
 
-// Several partial results of a row: the common maximum, the denominator over it.
+// A row's reference (0 for ref where there was no key), and its denominator over it.
 struct Joined {
     float m, ref, l;
 };
-template <int ROWS>
-__device__ __forceinline__ Joined join(const float (*stat)[ROWS][2], int row, int count)
-{
-    Joined j;
-    j.m = -__builtin_inff();
-    for (int k = 0; k < count; ++k) j.m = fmaxf(j.m, stat[k][row][0]);
-    j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
-    j.l = 0.0f;
-    for (int k = 0; k < count; ++k)
-        j.l += stat[k][row][1] * __builtin_amdgcn_exp2f(stat[k][row][0] - j.ref);
-    return j;
-}
-
 // Four channels of a row from its sums, and the row's lse from its first channels.
 template <int DT>
 __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t token, int head, int d, v4f o,
