@@ -5,10 +5,15 @@ namespace fp8q {
 namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
+constexpr int kPolicy = CP_DEFAULT;
 constexpr int kRows = 16;                 // query rows of a unit: (token, head of the group) pairs
 constexpr int kKeys = 64;                 // keys of a tile
 // Two workgroups on each of 256 CUs, one from 192 channels on (registers).
 constexpr int groups_for(int dp) { return dp <= 128 ? 512 : 256; }
+// Waves of a workgroup: eight where it takes a whole unit and the registers allow.
+constexpr int waves_for(int dp, bool shared) { return shared || dp > 128 ? 4 : 8; }
+// Units of at most this many keys are taken whole by a workgroup, without a join.
+constexpr int kShortKeys = 1024;
 constexpr int kMinShare = 3;              // what a wave takes at least
 
 // The work is a list of units (sequence, key/value head, row tile), each a run of
@@ -112,24 +117,191 @@ __device__ __forceinline__ int64_t uniform(int64_t v)
     return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
 }
 
-template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_rows_kernel(const AttendArgs a)
+// A key tile as a wave holds it: lane (r, g) has 16 channels for each 64 of the keys
+// 16 (r / 4) + 4 i + r % 4, i < 4, and the 16 keys from 16 g on of the channels 16 d + r.
+template <int DP>
+struct KvTile {
+    v4i k[4][DP / 64], v[DP / 16];
+};
+
+// The pages of a tile, asked for a tile ahead of its loads: where a page holds whole tiles
+// (WIDE) they are wave-uniform.
+template <bool WIDE>
+struct TilePages;
+template <>
+struct TilePages<true> {
+    PageRef p;
+    __device__ __forceinline__ const PageRef& mine() const { return p; }   // of the lane's terms
+};
+template <>
+struct TilePages<false> {
+    PageRef k, v;
+    __device__ __forceinline__ const PageRef& mine() const { return v; }
+};
+template <bool WIDE>
+__device__ __forceinline__ TilePages<WIDE> tile_pages(const AttendArgs& a, int b, int len, int key0, int r, int g)
+{
+    if constexpr (WIDE) return {page_ref(a, b, len, key0)};
+    else return {page_ref(a, b, len, key0 + 16 * (r >> 2)), page_ref(a, b, len, key0 + 16 * g)};
+}
+
+template <int DP, bool WIDE>
+__device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, const TilePages<WIDE>& p, int h,
+                                          int r, int g)
+{
+    constexpr int NC = DP / 64;
+    const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
+    if constexpr (WIDE) {
+        // buffer loads: one 32-bit offset a lane, the rest scalar; channels past D are sent out of
+        // the buffer's range and read as 0
+        const rsrc_t rk = make_rsrc(a.k_pages + p.p.page * pool_stride + h * page_bytes + p.p.inside * a.D,
+                                    (uint32_t)((a.P - p.p.inside) * a.D));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = 64 * c + 16 * g;
+                const uint32_t at = (uint32_t)((16 * (r >> 2) + (r & 3)) * a.D + d);
+                t.k[i][c] = __builtin_amdgcn_raw_buffer_load_b128(rk, d < a.D ? at : kOOB, uniform(4 * i * a.D),
+                                                                  kPolicy);
+            }
+    } else {
+        const uint8_t* kt = a.k_pages + p.k.page * pool_stride + h * page_bytes +
+                            (int64_t)(p.k.inside + (r & 3)) * a.D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                const int d = 64 * c + 16 * g;
+                t.k[i][c] = v4i{0, 0, 0, 0};
+                if (d < a.D) t.k[i][c] = *reinterpret_cast<const v4i*>(kt + 4 * i * a.D + d);
+            }
+    }
+}
+
+template <int DP, bool WIDE>
+__device__ __forceinline__ void load_values(const AttendArgs& a, KvTile<DP>& t, const TilePages<WIDE>& p, int h,
+                                            int r, int g)
+{
+    constexpr int ND = DP / 16;
+    const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
+    if constexpr (WIDE) {
+        const rsrc_t rv = make_rsrc(a.v_pages + p.p.page * pool_stride + h * page_bytes + p.p.inside,
+                                    (uint32_t)(page_bytes - p.p.inside));
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            t.v[d] = __builtin_amdgcn_raw_buffer_load_b128(rv, (uint32_t)(r * a.P + 16 * g),
+                                                           uniform(16 * d * a.P), kPolicy);
+    } else {
+        const uint8_t* vt = a.v_pages + p.v.page * pool_stride + h * page_bytes + p.v.inside;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            t.v[d] = v4i{0, 0, 0, 0};
+            if (16 * d < a.D) t.v[d] = *reinterpret_cast<const v4i*>(vt + (int64_t)(16 * d + r) * a.P);
+        }
+    }
+}
+
+// What a wave has of 16 query rows: lane (r, g) the sums of row r's channels 16 d + 4 g ..,
+// the reference, and its own keys' share of the denominator.
+template <int DP>
+struct Rows {
+    v4i q[DP / 64][2];
+    v4f acc[DP / 16];
+    float m, l;
+};
+
+// A tile's terms; keys_read is called when its keys are no longer needed.
+template <int DT, int DP, class F>
+__device__ __forceinline__ void add_tile(Rows<DP>& x, KvTile<DP>& t, const PageScales& sc, const KeyRange& see,
+                                         bool whole, bool valid, int key0, int g, F keys_read)
 {
     constexpr int NC = DP / 64, ND = DP / 16;
+    v4f s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s[i] = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            s[i] = Half<DT>::mfma(Half<DT>::widen(t.k[i][c][0], t.k[i][c][1]), x.q[c][0], s[i]);
+            s[i] = Half<DT>::mfma(Half<DT>::widen(t.k[i][c][2], t.k[i][c][3]), x.q[c][1], s[i]);
+        }
+    }
+    keys_read();
+    if (!whole) mask_tile<ND>(s, x.acc, t.v, see, key0, g, valid);
+
+    float top = s[0][0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
+    top = __builtin_fmaf(top, sc.key, sc.log_value);
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    if (__any(top > x.m + kSlack)) {
+        const float m1 = fmaxf(x.m, top);
+        const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.m - m1);
+        x.l *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) x.acc[d] *= alpha;
+        x.m = m1;
+    }
+    const float offset = sc.log_value - ((x.m == -__builtin_inff() ? 0.0f : x.m) - kShift);
+    float sum = 0.0f;
+    v8h p[2];
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const v2f v = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], sc.key, offset)),
+                       __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][(i & 3) + 1], sc.key, offset))};
+        sum += v[0];
+        sum += v[1];
+        const v2h w = __builtin_convertvector(v, v2h);
+        p[i >> 3][i & 7] = w[0];
+        p[i >> 3][(i & 7) + 1] = w[1];
+    }
+    x.l = __builtin_fmaf(sum, sc.inverse_value, x.l);
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        x.acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Half<DT_FP16>::widen(t.v[d][0], t.v[d][1]), p[0],
+                                                          x.acc[d], 0, 0, 0);
+        x.acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Half<DT_FP16>::widen(t.v[d][2], t.v[d][3]), p[1],
+                                                          x.acc[d], 0, 0, 0);
+    }
+}
+
+// SHARED: the grid's waves share the list of all units' tiles.  Else a workgroup takes one unit.
+template <int DT, int DP, bool WIDE, bool SHARED>
+__global__ void __launch_bounds__(waves_for(DP, SHARED) * 64, DP <= 128 ? 2 : 1)
+    attend_rows_kernel(const AttendArgs a)
+{
+    constexpr int kWaves = waves_for(DP, SHARED), kThreads = kWaves * 64, kPieces = SHARED ? 2 * kWaves : kWaves;
+    constexpr int NC = DP / 64, ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
-    __shared__ ScanLds scan;
-    __shared__ Unit piece[2 * kWaves];
-    __shared__ float stat[2 * kWaves][kRows][2];
-    __shared__ __attribute__((aligned(16))) float sums[2 * kWaves][kRows * RS];
+    __shared__ Unit piece[kPieces];
+    __shared__ float stat[kPieces][kRows][2];
+    __shared__ __attribute__((aligned(16))) float sums[kPieces][kRows * RS];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const int64_t total = uniform(scan_sequences(a, scan)), share = share_of(total, gridDim.x * kWaves);
-    int64_t at = ((int64_t)blockIdx.x * kWaves + wave) * share;
-    const int64_t end = at + share < total ? at + share : total;
-    if (lane < 2) piece[2 * wave + lane].rows = 0;
-    int b = at < end ? uniform(scan.seq[wave]) : 0;
-    int64_t seq_at = at < end ? uniform(scan.before[wave]) : 0;
-    const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
+    int64_t share = 0, at = 0, end = 0, seq_at = 0;
+    int b = 0;
+    if constexpr (SHARED) {
+        __shared__ ScanLds scan;
+        const int64_t total = uniform(scan_sequences(a, scan));
+        share = share_of(total, gridDim.x * kWaves);
+        at = ((int64_t)blockIdx.x * kWaves + wave) * share;
+        end = at + share < total ? at + share : total;
+        if (at < end) {
+            b = uniform(scan.seq[wave]);
+            seq_at = uniform(scan.before[wave]);
+        }
+        if (lane < 2) piece[2 * wave + lane].rows = 0;
+    } else {
+        b = blockIdx.x;
+        const SeqWork w = seq_work(a, b);
+        const int s = (w.tiles + kWaves - 1) / kWaves, unit = blockIdx.y;
+        if (unit >= w.row_tiles * a.Hk) return;
+        at = (int64_t)unit * (w.tiles + 1) + 1 + wave * s;
+        end = at + min(s, w.tiles - wave * s);
+        if (lane == 0) piece[wave].rows = 0;
+    }
 
     while (at < end) {
         const SeqWork w = seq_work(a, b);
@@ -150,7 +322,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_rows_kerne
         if (r >= rows) see.lo = see.hi = 0;
         const KeyRange first = key_range(a, w.q, row0 / a.group),
                        last = key_range(a, w.q, (row0 + rows - 1) / a.group);
-        v4i qf[NC][2];
+        const auto key_of = [&](int t) { return (w.tile0 + t) * kKeys; };
+        TilePages<WIDE> pages = tile_pages<WIDE>(a, b, w.q.len, key_of(t0), r, g);
+        Rows<DP> x;
         {
             const uint16_t* src = a.q + (int64_t)(w.q.row + token) * a.q_stride + (int64_t)head * a.D;
 #pragma unroll
@@ -158,106 +332,57 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_rows_kerne
                 const int d = 64 * c + 16 * g;
                 const bool have = r < rows && d < a.D;
                 const v4i zero = {0, 0, 0, 0};
-                qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
-                qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
+                x.q[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
+                x.q[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
             }
         }
-        v4f acc[ND];
 #pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
-        float m = -__builtin_inff(), l = 0.0f;
+        for (int d = 0; d < ND; ++d) x.acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
+        x.m = -__builtin_inff();
+        x.l = 0.0f;
 
+        // the next tile's keys are asked for when this tile's have been read, its values likewise, and
+        // its pages' ids a tile before
+        KvTile<DP> tile;
+        load_keys<DP, WIDE>(a, tile, pages, h, r, g);
+        load_values<DP, WIDE>(a, tile, pages, h, r, g);
+        PageScales sc = page_scales(a, pages.mine().page, h);
+        bool valid = pages.mine().valid;
         for (int t = t0; t < t1; ++t) {
-            const int key0 = (w.tile0 + t) * kKeys;
-            // key rows of the first product are read by row group, values by lane group
-            const PageRef kp = page_ref(a, b, w.q.len, key0 + 16 * (r >> 2));
-            const PageRef vp = page_ref(a, b, w.q.len, key0 + 16 * g);
-            const uint8_t* kt = a.k_pages + kp.page * pool_stride + h * page_bytes +
-                                (int64_t)(kp.inside + (r & 3)) * a.D;
-            const uint8_t* vt = a.v_pages + vp.page * pool_stride + h * page_bytes + vp.inside;
-            v4i kf[4][NC], vf[ND];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int d = 64 * c + 16 * g;
-                    kf[i][c] = v4i{0, 0, 0, 0};
-                    if (d < a.D) kf[i][c] = *reinterpret_cast<const v4i*>(kt + 4 * i * a.D + d);
-                }
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                vf[d] = v4i{0, 0, 0, 0};
-                if (16 * d < a.D) vf[d] = *reinterpret_cast<const v4i*>(vt + (int64_t)(16 * d + r) * a.P);
-            }
-            const PageScales sc = page_scales(a, vp.page, h);
-
-            v4f s[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[i] = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    s[i] = Half<DT>::mfma(Half<DT>::widen(kf[i][c][0], kf[i][c][1]), qf[c][0], s[i]);
-                    s[i] = Half<DT>::mfma(Half<DT>::widen(kf[i][c][2], kf[i][c][3]), qf[c][1], s[i]);
-                }
-            }
+            const int key0 = key_of(t);
+            const bool more = t + 1 < t1;
+            pages = tile_pages<WIDE>(a, b, w.q.len, key0 + kKeys, r, g);
             const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + kKeys &&
-                               last.hi >= key0 + kKeys && __all(vp.valid);
-            if (!whole) mask_tile<ND>(s, acc, vf, see, key0, g, vp.valid);
-
-            float top = s[0][0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
-            top = __builtin_fmaf(top, sc.key, sc.log_value);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (__any(top > m + kSlack)) {
-                const float m1 = fmaxf(m, top);
-                const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - m1);
-                l *= alpha;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) acc[d] *= alpha;
-                m = m1;
-            }
-            const float offset = sc.log_value - ((m == -__builtin_inff() ? 0.0f : m) - kShift);
-            float sum = 0.0f;
-            v8h p[2];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const v2f v = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][i & 3], sc.key, offset)),
-                               __builtin_amdgcn_exp2f(__builtin_fmaf(s[i >> 2][(i & 3) + 1], sc.key, offset))};
-                sum += v[0];
-                sum += v[1];
-                const v2h w2 = __builtin_convertvector(v, v2h);
-                p[i >> 3][i & 7] = w2[0];
-                p[i >> 3][(i & 7) + 1] = w2[1];
-            }
-            l = __builtin_fmaf(sum, sc.inverse_value, l);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    Half<DT_FP16>::widen(vf[d][0], vf[d][1]), p[0], acc[d], 0, 0, 0);
-                acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    Half<DT_FP16>::widen(vf[d][2], vf[d][3]), p[1], acc[d], 0, 0, 0);
-            }
+                               last.hi >= key0 + kKeys && __all(valid);
+            PageScales next = sc;
+            add_tile<DT, DP>(x, tile, sc, see, whole, valid, key0, g, [&] {
+                if (!more) return;
+                load_keys<DP, WIDE>(a, tile, pages, h, r, g);
+                next = page_scales(a, pages.mine().page, h);
+            });
+            if (more) load_values<DP, WIDE>(a, tile, pages, h, r, g);
+            sc = next;
+            valid = pages.mine().valid;
         }
 
-        l += __shfl_xor(l, 16);                             // the lane groups had keys of their own
-        l += __shfl_xor(l, 32);
+        x.l += __shfl_xor(x.l, 16);                         // the lane groups had keys of their own
+        x.l += __shfl_xor(x.l, 32);
         if (t0 == 0 && t1 == w.tiles) {
-            const Joined j{m, m == -__builtin_inff() ? 0.0f : m, l};
+            const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
             if (r < rows)
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
-                    if (16 * d < a.D) store_row<DT>(a, w.q.row + token, head, 16 * d + 4 * g, acc[d], j);
+                    if (16 * d < a.D) store_row<DT>(a, w.q.row + token, head, 16 * d + 4 * g, x.acc[d], j);
         } else {
-            const int slot = 2 * wave + (t0 == 0 ? 1 : 0);
-            if (g == 0) { stat[slot][r][0] = m; stat[slot][r][1] = l; }
+            const int slot = SHARED ? 2 * wave + (t0 == 0 ? 1 : 0) : wave;
+            if (g == 0) { stat[slot][r][0] = x.m; stat[slot][r][1] = x.l; }
 #pragma unroll
-            for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[slot][r * RS + 16 * d + 4 * g]) = acc[d];
+            for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[slot][r * RS + 16 * d + 4 * g]) = x.acc[d];
             if (lane == 0) {
-                const int64_t w0 = (unit_at + 1) / share / kWaves, w1 = (unit_at + w.tiles) / share / kWaves;
-                piece[slot] = Unit{unit_at, (int)(w1 - w0) + 1, t0 == 0, t1 == w.tiles, w.q.row, h, row0, rows, 0};
+                int parts = 1;
+                if constexpr (SHARED)
+                    parts += (int)((unit_at + w.tiles) / share / kWaves - (unit_at + 1) / share / kWaves);
+                piece[slot] = Unit{unit_at, parts, t0 == 0, t1 == w.tiles, w.q.row, h, row0, rows, 0};
             }
         }
     }
@@ -265,20 +390,20 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_rows_kerne
     // pieces of one unit lie next to each other, in order
     __syncthreads();
     bool told = false;
-    for (int p0 = 0; p0 < 2 * kWaves;) {
+    for (int p0 = 0; p0 < kPieces;) {
         const Unit u = piece[p0];
         int p1 = p0 + 1;
         if (u.rows == 0) { p0 = p1; continue; }
         int ends = u.ends;
-        for (int p = p1; p < 2 * kWaves; ++p) {
+        for (int p = p1; p < kPieces; ++p) {
             if (piece[p].rows == 0) continue;
             if (piece[p].at != u.at) break;
             ends = piece[p].ends;
             p1 = p + 1;
         }
-        const bool all = u.begins && ends;
-        float* out = part_of<DP>(a.work, gridDim.x, blockIdx.x, u.begins);
-        if (u.begins && !ends) {
+        const bool all = !SHARED || (u.begins && ends);
+        float* out = SHARED ? part_of<DP>(a.work, gridDim.x, blockIdx.x, u.begins) : nullptr;
+        if (SHARED && u.begins && !ends) {
             told = true;
             if (threadIdx.x == 0) reinterpret_cast<Unit*>(a.work)[blockIdx.x] = u;
         }
@@ -306,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_rows_kerne
         }
         p0 = p1;
     }
-    if (threadIdx.x == 0 && !told) reinterpret_cast<Unit*>(a.work)[blockIdx.x].parts = 0;
+    if (SHARED && threadIdx.x == 0 && !told) reinterpret_cast<Unit*>(a.work)[blockIdx.x].parts = 0;
 }
 
 // Joins the partial results of a unit that several workgroups had, told by the
@@ -366,15 +491,28 @@ __global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs 
     store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, j);
 }
 
+template <int DT, int DP, bool WIDE>
+hipError_t launch(const AttendArgs& a, hipStream_t stream)
+{
+    const int64_t rows = (int64_t)a.batch.max_q * a.group;
+    if ((int64_t)a.batch.W * a.P <= kShortKeys) {
+        const dim3 grid((unsigned)a.batch.B, (unsigned)((rows + kRows - 1) / kRows * a.Hk));
+        hipLaunchKernelGGL((attend_rows_kernel<DT, DP, WIDE, false>), grid, dim3(waves_for(DP, false) * 64), 0,
+                           stream, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((attend_rows_kernel<DT, DP, WIDE, true>), dim3(groups_for(DP)), dim3(kThreads), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attend_join_kernel<DT, DP>), dim3(groups_for(DP), rows < kRows ? rows : kRows),
+                       dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <int DT, int DP>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((attend_rows_kernel<DT, DP>), dim3(groups_for(DP)), dim3(kThreads), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    const int rows = a.batch.max_q < kRows / a.group ? a.batch.max_q * a.group : kRows;
-    hipLaunchKernelGGL((attend_join_kernel<DT, DP>), dim3(groups_for(DP), rows), dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+    return a.P % kKeys == 0 ? launch<DT, DP, true>(a, stream) : launch<DT, DP, false>(a, stream);
 }
 
 template <int DT>

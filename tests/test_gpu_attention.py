@@ -55,14 +55,17 @@ def run(bt, heads, dtype, causal=True, window=0, spread=1.0, spoil=True):
     q = bt.values(heads, dtype, spread)
     scale = bt.dim ** -0.5
     want = ref.attend(bt, q, scale, causal, window)
-    y = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
-    lse = torch.full(q.shape[:2], 7.0, device=DEV)
-    got = call(on_gpu(bt), q.to(DEV), bt.max_q, scale=scale, causal=causal, window=window, y=y, lse=lse)
-    torch.cuda.synchronize()
-    compare(bt, q, got, want)
-    outside = torch.isnan(want[1])
-    assert torch.all(y.cpu()[outside] == 7.0) and torch.all(lse.cpu()[outside] == 7.0)
-    return got
+    d = on_gpu(bt)
+    # a narrow page table, and one that has room for more keys than a workgroup takes by itself
+    for room in (0, 1100):
+        d["table"] = torch.nn.functional.pad(bt.table, (0, -(-room // bt.page)), value=-1).to(DEV)
+        y = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
+        lse = torch.full(q.shape[:2], 7.0, device=DEV)
+        got = call(d, q.to(DEV), bt.max_q, scale=scale, causal=causal, window=window, y=y, lse=lse)
+        torch.cuda.synchronize()
+        compare(bt, q, got, want)
+        outside = torch.isnan(want[1])
+        assert torch.all(y.cpu()[outside] == 7.0) and torch.all(lse.cpu()[outside] == 7.0)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
