@@ -794,7 +794,8 @@ fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch*
     FP8Q_TRY(check_device());
     const AttendArgs a{paged_batch(*batch), cache->k, cache->v, cache->k_scale, cache->v_scale,
                        (const uint16_t*)q, y, lse, (float*)work, q_stride, (int)cache->pages, (int)Hk,
-                       (int)cache->page_size, (int)D, (int)q_heads, (int)(q_heads / Hk),
+                       (int)cache->page_size, __builtin_ctz((unsigned)cache->page_size), (int)D, (int)q_heads,
+                       (int)(q_heads / Hk),
                        std::fabs(scale) * 1.4426950408889634f, scale < 0 ? (int)0x80008000u : 0,
                        causal != 0, (int)window};
     return finish("fp8_paged_attention", launch_paged_attention(a, dtype, (hipStream_t)stream));

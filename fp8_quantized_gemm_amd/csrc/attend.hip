@@ -267,124 +267,149 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, KvTile<DP>& t, const PageS
     }
 }
 
-// SHARED: the grid's waves share the list of all units' tiles.  Else a workgroup takes one unit.
+// A run of tiles [t0, t1) of a unit (key/value head h, rows from row0 on) by one wave.
+struct Run {
+    int h, row0, rows, t0, t1;
+};
+template <int DT, int DP, bool WIDE>
+__device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const SeqWork& w, const Run& u, Rows<DP>& x,
+                                           int& token, int& head)
+{
+    constexpr int NC = DP / 64, ND = DP / 16;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, h = u.h;
+    // this lane's query row and the keys it sees
+    const int my_row = u.row0 + r;
+    token = my_row / a.group;
+    head = h * a.group + (my_row - token * a.group);
+    KeyRange see = key_range(a, w.q, token);
+    if (r >= u.rows) see.lo = see.hi = 0;
+    const KeyRange first = key_range(a, w.q, uniform(token)),
+                   last = key_range(a, w.q, __builtin_amdgcn_readlane(token, u.rows - 1));
+    const auto key_of = [&](int t) { return (w.tile0 + t) * kKeys; };
+    TilePages<WIDE> pages = tile_pages<WIDE>(a, b, w.q.len, key_of(u.t0), r, g);
+    {
+        const uint16_t* src = a.q + (int64_t)(w.q.row + token) * a.q_stride + (int64_t)head * a.D;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const int d = 64 * c + 16 * g;
+            const bool have = r < u.rows && d < a.D;
+            const v4i zero = {0, 0, 0, 0};
+            x.q[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
+            x.q[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) x.acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
+    x.m = -__builtin_inff();
+    x.l = 0.0f;
+
+    // the next tile's keys are asked for when this tile's have been read, its values likewise, and
+    // its pages' ids a tile before
+    KvTile<DP> tile;
+    load_keys<DP, WIDE>(a, tile, pages, h, r, g);
+    load_values<DP, WIDE>(a, tile, pages, h, r, g);
+    PageScales sc = page_scales(a, pages.mine().page, h);
+    bool valid = pages.mine().valid;
+    for (int t = u.t0; t < u.t1; ++t) {
+        const int key0 = key_of(t);
+        const bool more = t + 1 < u.t1;
+        pages = tile_pages<WIDE>(a, b, w.q.len, key0 + kKeys, r, g);
+        const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + kKeys &&
+                           last.hi >= key0 + kKeys && __all(valid);
+        PageScales next = sc;
+        add_tile<DT, DP>(x, tile, sc, see, whole, valid, key0, g, [&] {
+            if (!more) return;
+            load_keys<DP, WIDE>(a, tile, pages, h, r, g);
+            next = page_scales(a, pages.mine().page, h);
+        });
+        if (more) load_values<DP, WIDE>(a, tile, pages, h, r, g);
+        sc = next;
+        valid = pages.mine().valid;
+    }
+    x.l += __shfl_xor(x.l, 16);                             // the lane groups had keys of their own
+    x.l += __shfl_xor(x.l, 32);
+}
+
+// SHARED: the grid's waves share the list of all units' tiles.  Else a workgroup takes one unit,
+// its waves equal runs of the tiles.
 template <int DT, int DP, bool WIDE, bool SHARED>
 __global__ void __launch_bounds__(waves_for(DP, SHARED) * 64, DP <= 128 ? 2 : 1)
     attend_rows_kernel(const AttendArgs a)
 {
     constexpr int kWaves = waves_for(DP, SHARED), kThreads = kWaves * 64, kPieces = SHARED ? 2 * kWaves : kWaves;
-    constexpr int NC = DP / 64, ND = DP / 16;
+    constexpr int ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
     __shared__ Unit piece[kPieces];
     __shared__ float stat[kPieces][kRows][2];
     __shared__ __attribute__((aligned(16))) float sums[kPieces][kRows * RS];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    int64_t share = 0, at = 0, end = 0, seq_at = 0;
-    int b = 0;
+    const auto keep = [&](const SeqWork& w, const Run& u, const Rows<DP>& x, int slot, int64_t unit_at, int parts) {
+        if (g == 0) { stat[slot][r][0] = x.m; stat[slot][r][1] = x.l; }
+#pragma unroll
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[slot][r * RS + 16 * d + 4 * g]) = x.acc[d];
+        if (lane == 0)
+            piece[slot] = Unit{unit_at, parts, u.t0 == 0, u.t1 == w.tiles, w.q.row, u.h, u.row0, u.rows, 0};
+    };
+    const auto store = [&](const SeqWork& w, const Run& u, const Rows<DP>& x, int token, int head) {
+        const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
+        if (r < u.rows)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                if (16 * d < a.D) store_row<DT>(a, w.q.row + token, head, 16 * d + 4 * g, x.acc[d], j);
+    };
+    Rows<DP> x;
+    int token, head;
     if constexpr (SHARED) {
         __shared__ ScanLds scan;
-        const int64_t total = uniform(scan_sequences(a, scan));
-        share = share_of(total, gridDim.x * kWaves);
-        at = ((int64_t)blockIdx.x * kWaves + wave) * share;
-        end = at + share < total ? at + share : total;
+        const int64_t total = uniform(scan_sequences(a, scan)), share = share_of(total, gridDim.x * kWaves);
+        int64_t at = ((int64_t)blockIdx.x * kWaves + wave) * share, seq_at = 0;
+        const int64_t end = at + share < total ? at + share : total;
+        int b = 0;
         if (at < end) {
             b = uniform(scan.seq[wave]);
             seq_at = uniform(scan.before[wave]);
         }
         if (lane < 2) piece[2 * wave + lane].rows = 0;
+        while (at < end) {
+            const SeqWork w = seq_work(a, b);
+            const int64_t seq_places = w.places(a.Hk);
+            if (at >= seq_at + seq_places) { seq_at += seq_places; ++b; continue; }
+            const int unit = (int)((at - seq_at) / (w.tiles + 1));
+            const int64_t unit_at = seq_at + (int64_t)unit * (w.tiles + 1);
+            Run u;
+            u.t0 = max((int)(at - unit_at) - 1, 0);
+            u.t1 = (int)(end - unit_at - 1 < w.tiles ? end - unit_at - 1 : w.tiles);
+            at = unit_at + w.tiles + 1;
+            if (u.t0 >= u.t1) continue;                     // only the place before the tiles
+            u.h = unit / w.row_tiles;
+            u.row0 = (unit - u.h * w.row_tiles) * kRows;
+            u.rows = min(kRows, w.q.n * a.group - u.row0);
+            attend_run<DT, DP, WIDE>(a, b, w, u, x, token, head);
+            if (u.t0 == 0 && u.t1 == w.tiles) store(w, u, x, token, head);
+            else
+                keep(w, u, x, 2 * wave + (u.t0 == 0 ? 1 : 0), unit_at,
+                     1 + (int)((unit_at + w.tiles) / share / kWaves - (unit_at + 1) / share / kWaves));
+        }
     } else {
-        b = blockIdx.x;
+        const int b = blockIdx.x, unit = blockIdx.y;
         const SeqWork w = seq_work(a, b);
-        const int s = (w.tiles + kWaves - 1) / kWaves, unit = blockIdx.y;
         if (unit >= w.row_tiles * a.Hk) return;
-        at = (int64_t)unit * (w.tiles + 1) + 1 + wave * s;
-        end = at + min(s, w.tiles - wave * s);
-        if (lane == 0) piece[wave].rows = 0;
-    }
-
-    while (at < end) {
-        const SeqWork w = seq_work(a, b);
-        const int64_t seq_places = w.places(a.Hk);
-        if (at >= seq_at + seq_places) { seq_at += seq_places; ++b; continue; }
-        const int unit = (int)((at - seq_at) / (w.tiles + 1));
-        const int64_t unit_at = seq_at + (int64_t)unit * (w.tiles + 1);
-        const int t0 = max((int)(at - unit_at) - 1, 0);
-        const int t1 = (int)(end - unit_at - 1 < w.tiles ? end - unit_at - 1 : w.tiles);
-        at = unit_at + w.tiles + 1;
-        if (t0 >= t1) continue;                             // only the place before the tiles
-        const int h = unit / w.row_tiles, row0 = unit % w.row_tiles * kRows;
-        const int rows = min(kRows, w.q.n * a.group - row0);
-
-        // this lane's query row and the keys it sees
-        const int my_row = row0 + r, token = my_row / a.group, head = h * a.group + my_row % a.group;
-        KeyRange see = key_range(a, w.q, token);
-        if (r >= rows) see.lo = see.hi = 0;
-        const KeyRange first = key_range(a, w.q, row0 / a.group),
-                       last = key_range(a, w.q, (row0 + rows - 1) / a.group);
-        const auto key_of = [&](int t) { return (w.tile0 + t) * kKeys; };
-        TilePages<WIDE> pages = tile_pages<WIDE>(a, b, w.q.len, key_of(t0), r, g);
-        Rows<DP> x;
-        {
-            const uint16_t* src = a.q + (int64_t)(w.q.row + token) * a.q_stride + (int64_t)head * a.D;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int d = 64 * c + 16 * g;
-                const bool have = r < rows && d < a.D;
-                const v4i zero = {0, 0, 0, 0};
-                x.q[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
-                x.q[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
-            }
-        }
-#pragma unroll
-        for (int d = 0; d < ND; ++d) x.acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
-        x.m = -__builtin_inff();
-        x.l = 0.0f;
-
-        // the next tile's keys are asked for when this tile's have been read, its values likewise, and
-        // its pages' ids a tile before
-        KvTile<DP> tile;
-        load_keys<DP, WIDE>(a, tile, pages, h, r, g);
-        load_values<DP, WIDE>(a, tile, pages, h, r, g);
-        PageScales sc = page_scales(a, pages.mine().page, h);
-        bool valid = pages.mine().valid;
-        for (int t = t0; t < t1; ++t) {
-            const int key0 = key_of(t);
-            const bool more = t + 1 < t1;
-            pages = tile_pages<WIDE>(a, b, w.q.len, key0 + kKeys, r, g);
-            const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + kKeys &&
-                               last.hi >= key0 + kKeys && __all(valid);
-            PageScales next = sc;
-            add_tile<DT, DP>(x, tile, sc, see, whole, valid, key0, g, [&] {
-                if (!more) return;
-                load_keys<DP, WIDE>(a, tile, pages, h, r, g);
-                next = page_scales(a, pages.mine().page, h);
-            });
-            if (more) load_values<DP, WIDE>(a, tile, pages, h, r, g);
-            sc = next;
-            valid = pages.mine().valid;
-        }
-
-        x.l += __shfl_xor(x.l, 16);                         // the lane groups had keys of their own
-        x.l += __shfl_xor(x.l, 32);
-        if (t0 == 0 && t1 == w.tiles) {
-            const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
-            if (r < rows)
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    if (16 * d < a.D) store_row<DT>(a, w.q.row + token, head, 16 * d + 4 * g, x.acc[d], j);
+        const int each = (w.tiles + kWaves - 1) / kWaves;
+        Run u;
+        u.t0 = wave * each;
+        u.t1 = min(u.t0 + each, w.tiles);
+        u.h = unit % a.Hk;
+        u.row0 = unit / a.Hk * kRows;
+        u.rows = min(kRows, w.q.n * a.group - u.row0);
+        if (u.t0 >= u.t1) {
+            if (lane == 0) piece[wave].rows = 0;
         } else {
-            const int slot = SHARED ? 2 * wave + (t0 == 0 ? 1 : 0) : wave;
-            if (g == 0) { stat[slot][r][0] = x.m; stat[slot][r][1] = x.l; }
-#pragma unroll
-            for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[slot][r * RS + 16 * d + 4 * g]) = x.acc[d];
-            if (lane == 0) {
-                int parts = 1;
-                if constexpr (SHARED)
-                    parts += (int)((unit_at + w.tiles) / share / kWaves - (unit_at + 1) / share / kWaves);
-                piece[slot] = Unit{unit_at, parts, t0 == 0, t1 == w.tiles, w.q.row, h, row0, rows, 0};
-            }
+            attend_run<DT, DP, WIDE>(a, b, w, u, x, token, head);
+            if (w.tiles == 1) { store(w, u, x, token, head); return; }
+            keep(w, u, x, wave, 0, 1);
         }
+        if (w.tiles == 1) return;
     }
 
     // pieces of one unit lie next to each other, in order

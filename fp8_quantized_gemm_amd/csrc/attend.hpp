@@ -50,10 +50,10 @@ struct PageRef {
 };
 __device__ __forceinline__ PageRef page_ref(const AttendArgs& a, int b, int len, int key)
 {
-    const int slot = key / a.P;
+    const int slot = key >> a.page_shift;
     const int id = key < len ? a.batch.page_table[(int64_t)b * a.batch.W + slot] : -1;
     const bool valid = id >= 0 && id < a.pages;
-    return PageRef{valid ? id : 0, key - slot * a.P, valid};
+    return PageRef{valid ? id : 0, key & (a.P - 1), valid};
 }
 
 // The E4M3 codes of NaN in four codes, as 0x80 in their bytes.

@@ -66,7 +66,7 @@ struct AttendArgs {
     float* lse;                      // [T, Hq] or null
     float* work;
     int64_t q_stride;
-    int pages, Hk, P, D, Hq, group;
+    int pages, Hk, P, page_shift, D, Hq, group;
     float scale_log2;                // |softmax scale| * log2(e)
     int q_flip;                      // sign bits of two queries where the scale is negative, else 0
     int causal, window;
