@@ -111,12 +111,6 @@ __device__ __forceinline__ float* part_of(float* work, int groups, int64_t group
     return work + groups * (int)(sizeof(Unit) / 4) + (group * 2 + (begins ? 1 : 0)) * (kRows * (DP + 4));
 }
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v)
-{
-    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
-}
-
 // A key tile as a wave holds it: lane (r, g) has 16 channels for each 64 of the keys
 // 16 (r / 4) + 4 i + r % 4, i < 4, and the 16 keys from 16 g on of the channels 16 d + r.
 template <int DP>

@@ -14,6 +14,13 @@ namespace fp8q {
 // down to 2^-23 of the reference with all its 11 bits.
 constexpr float kSlack = 6.0f, kShift = 9.0f, kShiftScale = 0x1p9f;
 
+// A value that all lanes of the wave have, told to the compiler.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform(int64_t v)
+{
+    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
+}
+
 struct KeyRange {
     int lo, hi;
 };

@@ -61,6 +61,154 @@ __device__ __forceinline__ const uint8_t* shuffle(const uint8_t* p, int lane)
     return reinterpret_cast<const uint8_t*>((uint64_t)hi << 32 | lo);
 }
 
+__device__ __forceinline__ v4i value_at(const uint8_t* vt, int d, int tb, int r, int hf)
+{
+    return *reinterpret_cast<const v4i*>(vt + swz64(32 * d + r, 2 * tb + hf));
+}
+__device__ __forceinline__ void times16(v16f& sum, const v4i& v, const v8h (&w)[2])
+{
+    sum = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[0], v[1]), __builtin_bit_cast(v4i, w[0]), sum);
+    sum = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[2], v[3]), __builtin_bit_cast(v4i, w[1]), sum);
+}
+
+// Values of keys that a row does not see must not count, but 0 * NaN would.  A tile that is not
+// whole is looked through for codes of NaN; if there are any the wave goes on with a copy that has
+// 0 for them, and notes the channels where a row does see one.
+template <int DP>
+__device__ __forceinline__ bool any_nan(const uint8_t* vt, int r, int hf)
+{
+    uint32_t any = 0;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            const v4i v = value_at(vt, d, tb, r, hf);
+            any |= nan_bytes((uint32_t)v[0]) | nan_bytes((uint32_t)v[1]) | nan_bytes((uint32_t)v[2]) |
+                   nan_bytes((uint32_t)v[3]);
+        }
+    return __ballot(any != 0) != 0;
+}
+template <int DP>
+__device__ __forceinline__ void take_nan(uint32_t (&nan)[DP / 64], const uint8_t* vt, uint8_t* clean,
+                                         const v8h (&seen)[2][2], int r, int hf)
+{
+    uint32_t got[DP / 64] = {};
+#pragma unroll 1
+    for (int d = DP / 32 - 1; d >= 0; --d) {               // 16 bits a time, the first channels last
+        v16f hits;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) hits[i] = 0.0f;
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            v4i v = value_at(vt, d, tb, r, hf);
+            times16(hits, nan_ones(v), seen[tb]);
+            clear_nan(v);
+            *reinterpret_cast<v4i*>(clean + swz64(32 * d + r, 2 * tb + hf)) = v;
+        }
+#pragma unroll
+        for (int j = DP / 64 - 1; j > 0; --j) got[j] = got[j] << 16 | got[j - 1] >> 16;
+        got[0] <<= 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) got[0] |= hits[i] > 0.f ? 1u << i : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < DP / 64; ++j) nan[j] |= got[j];
+}
+
+// What a wave has of its 32 query rows: lane (r, hf) half of row r's channels (32 d + 8 i + 4 hf ..),
+// the row's reference, and its own keys' share of the denominator; a bit of `nan` for each channel
+// that has seen NaN.
+template <int DP>
+struct Rows {
+    v4i q[DP / 32][2];
+    v16f acc[DP / 32];
+    uint32_t nan[DP / 64];
+    float m, l;
+};
+
+// A tile's terms.  whole: every row sees every key; clean: room for a tile of values.
+template <int DT, int DP>
+__device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const PageScales& sc, const KeyRange& see,
+                                         int key0, bool valid, bool whole, uint8_t* clean)
+{
+    using T = Tile<DP>;
+    constexpr int NC = DP / 32, ND = DP / 32;
+    const int lane = threadIdx.x & 63, r = lane & 31, hf = lane >> 5;
+    const uint8_t* vt = kt + T::kKeyBytes;
+    v16f s[2];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const v4i k = *reinterpret_cast<const v4i*>(kt + T::key_at(32 * tb + r, 2 * c + hf));
+            s[tb] = mfma32<DT>(Half<DT>::widen(k[0], k[1]), x.q[c][0], s[tb]);
+            s[tb] = mfma32<DT>(Half<DT>::widen(k[2], k[3]), x.q[c][1], s[tb]);
+        }
+    }
+    if (!whole) {
+        const bool on_page[2] = {__shfl(valid ? 1 : 0, hf) != 0, __shfl(valid ? 1 : 0, 2 + hf) != 0};
+        v8h seen[2][2];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) {
+            const int key = key0 + 32 * tb + 16 * hf, lo = see.lo - key, hi = on_page[tb] ? see.hi - key : 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const bool in = i >= lo && i < hi;
+                s[tb][i] = in ? s[tb][i] : -__builtin_inff();
+                seen[tb][i >> 3][i & 7] = in ? (_Float16)1.0f : (_Float16)0.0f;
+            }
+        }
+        if (any_nan<DP>(vt, r, hf)) {
+            take_nan<DP>(x.nan, vt, clean, seen, r, hf);
+            vt = clean;
+        }
+    }
+    // logarithms: a term is 2^(s * ks + lv), times the values' scale; one page a lane and block
+    float ks[2], lv[2], top[2];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+        ks[tb] = __shfl(sc.key, 2 * tb + hf);
+        lv[tb] = __shfl(sc.log_value, 2 * tb + hf);
+        top[tb] = s[tb][0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i) top[tb] = fmaxf(top[tb], s[tb][i]);
+        top[tb] = __builtin_fmaf(top[tb], ks[tb], lv[tb]);
+    }
+    const float both = fmaxf(top[0], top[1]), highest = fmaxf(both, __shfl_xor(both, 32));
+    if (__any(highest > x.m + kSlack)) {
+        const float m1 = fmaxf(x.m, highest);
+        const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.m - m1);
+        x.l *= alpha;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) x.acc[d] *= alpha;
+        x.m = m1;
+    }
+    const float ref = x.m == -__builtin_inff() ? 0.0f : x.m;
+    v8h p[2][2];
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) {
+        const float offset = lv[tb] - (ref - kShift);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const v2f v = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i], ks[tb], offset)),
+                           __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i + 1], ks[tb], offset))};
+            sum += v[0];
+            sum += v[1];
+            const v2h w = __builtin_convertvector(v, v2h);
+            p[tb][i >> 3][i & 7] = w[0];
+            p[tb][i >> 3][(i & 7) + 1] = w[1];
+        }
+        x.l = __builtin_fmaf(sum, __shfl(sc.inverse_value, 2 * tb + hf), x.l);
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) times16(x.acc[d], value_at(vt, d, tb, r, hf), p[tb]);
+}
+
 template <int DT, int DP>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_kernel(const AttendArgs a, int64_t units)
 {
@@ -68,9 +216,10 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     constexpr int NC = DP / 32, ND = DP / 32;
     constexpr int KB = T::kKeyBlocks / kWaves, VB = T::kValueBlocks / kWaves;
     __shared__ __attribute__((aligned(16))) uint8_t lds[2][T::kKeyBytes + T::kValueBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t clean[kWaves][T::kValueBytes];
     __shared__ int found[kWaves];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r = lane & 31, hf = lane >> 5;
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, hf = lane >> 5;
     // units of kTileRows rows; those of sequence b begin at unit q_start[b] * group / kTileRows + b.
     // The last ones first: under a causal mask they are the longest.
     const int64_t index = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
@@ -80,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     int below = 0;
     for (int b = tid; b < a.batch.B; b += kThreads)
         below += (int64_t)clamp_int(a.batch.q_start[b], 0, a.batch.T) * a.group / kTileRows + b <= u ? 1 : 0;
-    const int b = max(block_sum_int<kThreads>(below, found) - 1, 0);
+    const int b = uniform(max(block_sum_int<kThreads>(below, found) - 1, 0));
     const PagedSeq q = paged_seq(a.batch, b, a.P);
     const int64_t rows64 = (int64_t)q.n * a.group;
     const int64_t row64 = (u - ((int64_t)q.row * a.group / kTileRows + b)) * kTileRows;
@@ -98,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     const KeyRange wfirst = key_range(a, q, wave_row0 / a.group), wlast = key_range(a, q, wave_last / a.group);
     const int t0 = first.lo / kKeys, t1 = (last.hi + kKeys - 1) / kKeys;
 
-    v4i qf[NC][2];
+    Rows<DP> x;
     {
         const uint16_t* src = a.q + (int64_t)(q.row + token) * a.q_stride + (int64_t)head * a.D;
         const v4i zero = {0, 0, 0, 0};
@@ -106,8 +255,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         for (int c = 0; c < NC; ++c) {
             const int d = 32 * c + 16 * hf;
             const bool have = have_row && d < a.D;
-            qf[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
-            qf[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
+            x.q[c][0] = have ? *reinterpret_cast<const v4i*>(src + d) ^ a.q_flip : zero;
+            x.q[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
         }
     }
     if (a.D < T::kPitch) {                // channels that no load fills
@@ -139,12 +288,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         }
     };
 
-    v16f acc[ND];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[d][i] = 0.0f;
-    float m = -__builtin_inff(), l = 0.0f;
+        for (int i = 0; i < 16; ++i) x.acc[d][i] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < DP / 64; ++d) x.nan[d] = 0u;
+    x.m = -__builtin_inff();
+    x.l = 0.0f;
 
     PageRef next = page_ref(a, b, q.len, t0 * kKeys + group_key);
     if (t0 < t1) load_tile(t0, next, lds[0]);
@@ -153,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     next = page_ref(a, b, q.len, (t0 + 1) * kKeys + group_key);
     for (int t = t0; t < t1; ++t) {
         const uint8_t* const kt = lds[(t - t0) & 1];
-        const uint8_t* const vt = kt + T::kKeyBytes;
         wait_vm<0>();
         __syncthreads();                  // tile t is there, and tile t - 1 has been read
         const PageScales now = next_scales;
@@ -167,112 +317,24 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         const int key0 = t * kKeys;
         if (idle || key0 >= wlast.hi || key0 + kKeys <= wfirst.lo) continue;   // no row of this wave sees the tile
 
-        v16f s[2];
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const v4i k = *reinterpret_cast<const v4i*>(kt + T::key_at(32 * tb + r, 2 * c + hf));
-                s[tb] = mfma32<DT>(Half<DT>::widen(k[0], k[1]), qf[c][0], s[tb]);
-                s[tb] = mfma32<DT>(Half<DT>::widen(k[2], k[3]), qf[c][1], s[tb]);
-            }
-        }
         const bool whole = wfirst.lo <= key0 && wlast.lo <= key0 && wfirst.hi >= key0 + kKeys &&
                            wlast.hi >= key0 + kKeys && __all(valid);
-        v8h seen[2][2];
-        if (!whole) {
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                const int k0 = key0 + 32 * tb + 16 * hf;
-                const bool on_page = __shfl(valid ? 1 : 0, 2 * tb + hf) != 0;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const bool in = on_page && k0 + i >= see.lo && k0 + i < see.hi;
-                    s[tb][i] = in ? s[tb][i] : -__builtin_inff();
-                    seen[tb][i >> 3][i & 7] = in ? (_Float16)1.0f : (_Float16)0.0f;
-                }
-            }
-        }
-        // logarithms: a term is 2^(s * ks + lv), times the values' scale; one page a lane and block
-        float ks[2], lv[2], top[2];
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            ks[tb] = __shfl(now.key, 2 * tb + hf);
-            lv[tb] = __shfl(now.log_value, 2 * tb + hf);
-            top[tb] = s[tb][0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i) top[tb] = fmaxf(top[tb], s[tb][i]);
-            top[tb] = __builtin_fmaf(top[tb], ks[tb], lv[tb]);
-        }
-        const float both = fmaxf(top[0], top[1]), highest = fmaxf(both, __shfl_xor(both, 32));
-        if (__any(highest > m + kSlack)) {
-            const float m1 = fmaxf(m, highest);
-            const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - m1);
-            l *= alpha;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) acc[d] *= alpha;
-            m = m1;
-        }
-        const float ref = m == -__builtin_inff() ? 0.0f : m;
-        v8h p[2][2];
-#pragma unroll
-        for (int tb = 0; tb < 2; ++tb) {
-            const float offset = lv[tb] - (ref - kShift);
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const v2f v = {__builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i], ks[tb], offset)),
-                               __builtin_amdgcn_exp2f(__builtin_fmaf(s[tb][i + 1], ks[tb], offset))};
-                sum += v[0];
-                sum += v[1];
-                const v2h w = __builtin_convertvector(v, v2h);
-                p[tb][i >> 3][i & 7] = w[0];
-                p[tb][i >> 3][(i & 7) + 1] = w[1];
-            }
-            l = __builtin_fmaf(sum, __shfl(now.inverse_value, 2 * tb + hf), l);
-        }
-        uint32_t any = 0;
-#pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int tb = 0; tb < 2; ++tb) {
-                v4i v = *reinterpret_cast<const v4i*>(vt + swz64(32 * d + r, 2 * tb + hf));
-                if (!whole) any |= clear_nan(v);
-                acc[d] = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[0], v[1]), __builtin_bit_cast(v4i, p[tb][0]), acc[d]);
-                acc[d] = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[2], v[3]), __builtin_bit_cast(v4i, p[tb][1]), acc[d]);
-            }
-        if (!whole && __ballot(any != 0) != 0) {
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                v16f hits;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) hits[i] = 0.0f;
-#pragma unroll
-                for (int tb = 0; tb < 2; ++tb) {
-                    const v4i v = *reinterpret_cast<const v4i*>(vt + swz64(32 * d + r, 2 * tb + hf));
-                    const v4i one = nan_ones(v);
-                    hits = mfma32<DT_FP16>(Half<DT_FP16>::widen(one[0], one[1]), __builtin_bit_cast(v4i, seen[tb][0]), hits);
-                    hits = mfma32<DT_FP16>(Half<DT_FP16>::widen(one[2], one[3]), __builtin_bit_cast(v4i, seen[tb][1]), hits);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) acc[d][i] += hits[i] > 0.f ? __builtin_nanf("") : 0.f;
-            }
-        }
+        add_tile<DT, DP>(x, kt, now, see, key0, valid, whole, clean[wave]);
     }
 
-    l += __shfl_xor(l, 32);
+    x.l += __shfl_xor(x.l, 32);
     if (!have_row) return;
-    const Joined j{m, m == -__builtin_inff() ? 0.0f : m, l};
+    const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int c = 32 * d + 8 * e + 4 * hf;
-            if (c < a.D)
-                store_row<DT>(a, q.row + token, head, c,
-                              v4f{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]}, j);
+            v4f o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                o[i] = (x.nan[d >> 1] >> (16 * (d & 1) + 4 * e + i) & 1u) != 0 ? __builtin_nanf("") : x.acc[d][4 * e + i];
+            if (c < a.D) store_row<DT>(a, q.row + token, head, c, o, j);
         }
 }
 
