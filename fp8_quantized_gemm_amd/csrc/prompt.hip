@@ -209,7 +209,7 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
         for (int tb = 0; tb < 2; ++tb) times16(x.acc[d], value_at(vt, d, tb, r, hf), p[tb]);
 }
 
-template <int DT, int DP>
+template <int DT, int DP, bool WIDE>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_kernel(const AttendArgs a, int64_t units)
 {
     using T = Tile<DP>;
@@ -259,32 +259,54 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
             x.q[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
         }
     }
-    if (a.D < T::kPitch) {                // channels that no load fills
+    if (!WIDE && a.D < T::kPitch) {       // channels that no load fills
         for (int i = tid; i < 2 * T::kKeyBytes / 16; i += kThreads)
             *reinterpret_cast<v4i*>(&lds[i / (T::kKeyBytes / 16)][i % (T::kKeyBytes / 16) * 16]) = v4i{0, 0, 0, 0};
         __syncthreads();
     }
 
     // A tile's keys in four groups of 16, each on one page; lane i of a wave keeps what is known of
-    // group i % 4.  The page ids are requested two tiles ahead, the scales and codes one.
+    // group i % 4.
     const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
     const int group_key = 16 * (lane & 3);
-    const auto load_tile = [&](int t, const PageRef& p, uint8_t* dst) {
-        const int64_t page_at = p.page * pool_stride + h * page_bytes;
-        const uint8_t* const kp = a.k_pages + page_at + (int64_t)p.inside * a.D;
-        const uint8_t* const vp = a.v_pages + page_at + p.inside;
+    const auto load_tile = [&](const PageRef& p, uint8_t* dst) {
+        if constexpr (WIDE) {
+            // the tile is on one page: a lane's offsets are the same in every tile; channels past D
+            // are out of the buffer's range (values) or sent there (keys) and become 0
+            const int64_t page = uniform((int)p.page);
+            const int inside = uniform(p.inside);
+            const rsrc_t rk = make_rsrc(a.k_pages + page * pool_stride + h * page_bytes + inside * a.D,
+                                        (uint32_t)(kKeys * a.D));
+            const rsrc_t rv = make_rsrc(a.v_pages + page * pool_stride + h * page_bytes + inside,
+                                        (uint32_t)(page_bytes - inside));
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
-            const int c = (unit % T::kUnits) ^ T::swizzle(row), key = (row & 32) + key_of_row(row & 31);
-            const uint8_t* src = shuffle(kp, key >> 4) + (key & 15) * a.D + 16 * c;
-            if (16 * c < a.D) load_lds16(src, dst + (wave * KB + j) * 1024);
-        }
+            for (int j = 0; j < KB; ++j) {
+                const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
+                const int c = (unit % T::kUnits) ^ T::swizzle(row), key = (row & 32) + key_of_row(row & 31);
+                dma_load16(rk, dst + (wave * KB + j) * 1024, 16 * c < a.D ? (uint32_t)(key * a.D + 16 * c) : kOOB);
+            }
 #pragma unroll
-        for (int j = 0; j < VB; ++j) {
-            const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
-            const uint8_t* src = shuffle(vp, g) + d * a.P;
-            if (d < a.D) load_lds16(src, dst + T::kKeyBytes + (wave * VB + j) * 1024);
+            for (int j = 0; j < VB; ++j) {
+                const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
+                dma_load16(rv, dst + T::kKeyBytes + (wave * VB + j) * 1024, (uint32_t)(d * a.P + 16 * g));
+            }
+        } else {
+            const int64_t page_at = p.page * pool_stride + h * page_bytes;
+            const uint8_t* const kp = a.k_pages + page_at + (int64_t)p.inside * a.D;
+            const uint8_t* const vp = a.v_pages + page_at + p.inside;
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
+                const int c = (unit % T::kUnits) ^ T::swizzle(row), key = (row & 32) + key_of_row(row & 31);
+                const uint8_t* src = shuffle(kp, key >> 4) + (key & 15) * a.D + 16 * c;
+                if (16 * c < a.D) load_lds16(src, dst + (wave * KB + j) * 1024);
+            }
+#pragma unroll
+            for (int j = 0; j < VB; ++j) {
+                const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
+                const uint8_t* src = shuffle(vp, g) + d * a.P;
+                if (d < a.D) load_lds16(src, dst + T::kKeyBytes + (wave * VB + j) * 1024);
+            }
         }
     };
 
@@ -297,23 +319,34 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     x.m = -__builtin_inff();
     x.l = 0.0f;
 
-    PageRef next = page_ref(a, b, q.len, t0 * kKeys + group_key);
-    if (t0 < t1) load_tile(t0, next, lds[0]);
-    PageScales next_scales = page_scales(a, next.page, h);
+    // A tile's codes and scales are requested a tile ahead and its pages' ids two.  What is loaded to
+    // registers is requested before the codes and not touched before the next tile: loads return in
+    // order, and a use would wait for the codes as well.
+    const auto id_of = [&](int t) { return page_id(a, b, q.len, t * kKeys + group_key); };
+    int next_id = id_of(t0);
+    PageRef next = page_ref(a, next_id, t0 * kKeys + group_key);
     bool next_valid = next.valid;
-    next = page_ref(a, b, q.len, (t0 + 1) * kKeys + group_key);
+    int64_t cell = next.page * a.Hk + h;
+    float next_k = a.k_scale[cell], next_v = a.v_scale[cell];
+    next_id = id_of(t0 + 1);
+    if (t0 < t1) load_tile(next, lds[0]);
     for (int t = t0; t < t1; ++t) {
         const uint8_t* const kt = lds[(t - t0) & 1];
         wait_vm<0>();
+        asm volatile("" : "+v"(next_k), "+v"(next_v), "+v"(next_id));
         __syncthreads();                  // tile t is there, and tile t - 1 has been read
-        const PageScales now = next_scales;
+        const float now_k = next_k, now_v = next_v;
         const bool valid = next_valid;
         if (t + 1 < t1) {
-            load_tile(t + 1, next, lds[(t + 1 - t0) & 1]);
-            next_scales = page_scales(a, next.page, h);
+            next = page_ref(a, next_id, (t + 1) * kKeys + group_key);
             next_valid = next.valid;
-            next = page_ref(a, b, q.len, (t + 2) * kKeys + group_key);
+            cell = next.page * a.Hk + h;
+            next_k = a.k_scale[cell];
+            next_v = a.v_scale[cell];
+            next_id = id_of(t + 2);
+            load_tile(next, lds[(t + 1 - t0) & 1]);
         }
+        const PageScales now = page_scales(a, now_k, now_v);
         const int key0 = t * kKeys;
         if (idle || key0 >= wlast.hi || key0 + kKeys <= wfirst.lo) continue;   // no row of this wave sees the tile
 
@@ -338,14 +371,20 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
         }
 }
 
-template <int DT, int DP>
+template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
     const int64_t units = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
     const int64_t groups = units * a.Hk, most = max_groups(kThreads), gx = groups < most ? groups : most;
-    hipLaunchKernelGGL((attend_prompt_kernel<DT, DP>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
+    hipLaunchKernelGGL((attend_prompt_kernel<DT, DP, WIDE>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
                        dim3(kThreads), 0, stream, a, units);
     return hipGetLastError();
+}
+
+template <int DT, int DP>
+hipError_t launch(const AttendArgs& a, hipStream_t stream)
+{
+    return a.P % kKeys == 0 ? launch<DT, DP, true>(a, stream) : launch<DT, DP, false>(a, stream);
 }
 
 template <int DT>
