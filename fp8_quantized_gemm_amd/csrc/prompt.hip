@@ -31,11 +31,33 @@ __device__ __forceinline__ v16f mfma32(typename Half<DT>::vec a, v4i b, v16f c)
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(v8h, b), c, 0, 0, 0);
 }
 
-// 16 bytes of global memory for each active lane to lds_block + 16 * lane.
-__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* lds_block)
+// 16 bytes for each active lane to lds_block + 16 * lane, asynchronously: from a buffer, or from any
+// address.  Written as assembly because the compiler, which cannot tell the buffer being filled from
+// the one being read, would wait for builtin loads of this kind before the next read of LDS, and no
+// tile would be under way during the arithmetic.  They write no register; the kernel waits itself.
+__device__ __forceinline__ uint32_t lds_address(const void* p)
 {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                     (__attribute__((address_space(3))) void*)lds_block, 16, 0, 0);
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+__device__ __forceinline__ void buffer_to_lds(const v4i& rsrc, void* lds_block, uint32_t offset)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
+                     uniform((int)lds_address(lds_block))),
+                 "v"(offset), "s"(rsrc)
+                 : "memory", "m0");
+}
+__device__ __forceinline__ void global_to_lds(const uint8_t* src, void* lds_block)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
+                     uniform((int)lds_address(lds_block))),
+                 "v"(src)
+                 : "memory", "m0");
+}
+// The words of make_rsrc's resource.
+__device__ __forceinline__ v4i rsrc_words(const uint8_t* base, int bytes)
+{
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return v4i{uniform((int)(uint32_t)p), uniform((int)(uint32_t)(p >> 32)) & 0xffff, uniform(bytes), 0x00020000};
 }
 
 // Tiles in LDS.  Keys: row r of PITCH bytes is key 32 (r / 32) + key_of_row(r % 32), its 16-byte
@@ -137,15 +159,20 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
     const uint8_t* vt = kt + T::kKeyBytes;
     v16f s[2];
 #pragma unroll
-    for (int tb = 0; tb < 2; ++tb) {
+    for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[tb][i] = 0.0f;
+    // neighbouring matrix instructions add to different sums, so that none waits for the last
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const v4i k = *reinterpret_cast<const v4i*>(kt + T::key_at(32 * tb + r, 2 * c + hf));
-            s[tb] = mfma32<DT>(Half<DT>::widen(k[0], k[1]), x.q[c][0], s[tb]);
-            s[tb] = mfma32<DT>(Half<DT>::widen(k[2], k[3]), x.q[c][1], s[tb]);
-        }
+    for (int c = 0; c < NC; ++c) {
+        v4i k[2];
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) k[tb] = *reinterpret_cast<const v4i*>(kt + T::key_at(32 * tb + r, 2 * c + hf));
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int tb = 0; tb < 2; ++tb)
+                s[tb] = mfma32<DT>(Half<DT>::widen(k[tb][2 * e], k[tb][2 * e + 1]), x.q[c][e], s[tb]);
     }
     if (!whole) {
         const bool on_page[2] = {__shfl(valid ? 1 : 0, hf) != 0, __shfl(valid ? 1 : 0, 2 + hf) != 0};
@@ -204,9 +231,17 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
         x.l = __builtin_fmaf(sum, __shfl(sc.inverse_value, 2 * tb + hf), x.l);
     }
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
+    for (int tb = 0; tb < 2; ++tb)
 #pragma unroll
-        for (int tb = 0; tb < 2; ++tb) times16(x.acc[d], value_at(vt, d, tb, r, hf), p[tb]);
+        for (int d0 = 0; d0 < ND; d0 += 2) {
+            const v4i v[2] = {value_at(vt, d0, tb, r, hf), value_at(vt, d0 + 1, tb, r, hf)};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    x.acc[d0 + i] = mfma32<DT_FP16>(Half<DT_FP16>::widen(v[i][2 * e], v[i][2 * e + 1]),
+                                                    __builtin_bit_cast(v4i, p[tb][e]), x.acc[d0 + i]);
+        }
 }
 
 template <int DT, int DP, bool WIDE>
@@ -275,20 +310,19 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
             // are out of the buffer's range (values) or sent there (keys) and become 0
             const int64_t page = uniform((int)p.page);
             const int inside = uniform(p.inside);
-            const rsrc_t rk = make_rsrc(a.k_pages + page * pool_stride + h * page_bytes + inside * a.D,
-                                        (uint32_t)(kKeys * a.D));
-            const rsrc_t rv = make_rsrc(a.v_pages + page * pool_stride + h * page_bytes + inside,
-                                        (uint32_t)(page_bytes - inside));
+            const v4i rk = rsrc_words(a.k_pages + page * pool_stride + h * page_bytes + inside * a.D, kKeys * a.D);
+            const v4i rv = rsrc_words(a.v_pages + page * pool_stride + h * page_bytes + inside,
+                                      (int)page_bytes - inside);
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
                 const int c = (unit % T::kUnits) ^ T::swizzle(row), key = (row & 32) + key_of_row(row & 31);
-                dma_load16(rk, dst + (wave * KB + j) * 1024, 16 * c < a.D ? (uint32_t)(key * a.D + 16 * c) : kOOB);
+                buffer_to_lds(rk, dst + (wave * KB + j) * 1024, 16 * c < a.D ? (uint32_t)(key * a.D + 16 * c) : kOOB);
             }
 #pragma unroll
             for (int j = 0; j < VB; ++j) {
                 const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
-                dma_load16(rv, dst + T::kKeyBytes + (wave * VB + j) * 1024, (uint32_t)(d * a.P + 16 * g));
+                buffer_to_lds(rv, dst + T::kKeyBytes + (wave * VB + j) * 1024, (uint32_t)(d * a.P + 16 * g));
             }
         } else {
             const int64_t page_at = p.page * pool_stride + h * page_bytes;
@@ -299,13 +333,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
                 const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
                 const int c = (unit % T::kUnits) ^ T::swizzle(row), key = (row & 32) + key_of_row(row & 31);
                 const uint8_t* src = shuffle(kp, key >> 4) + (key & 15) * a.D + 16 * c;
-                if (16 * c < a.D) load_lds16(src, dst + (wave * KB + j) * 1024);
+                if (16 * c < a.D) global_to_lds(src, dst + (wave * KB + j) * 1024);
             }
 #pragma unroll
             for (int j = 0; j < VB; ++j) {
                 const int d = (wave * VB + j) * 16 + (lane >> 2), g = (lane & 3) ^ ((d >> 1) & 3);
                 const uint8_t* src = shuffle(vp, g) + d * a.P;
-                if (d < a.D) load_lds16(src, dst + T::kKeyBytes + (wave * VB + j) * 1024);
+                if (d < a.D) global_to_lds(src, dst + T::kKeyBytes + (wave * VB + j) * 1024);
             }
         }
     };
