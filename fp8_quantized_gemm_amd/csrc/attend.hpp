@@ -154,8 +154,9 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t token, in
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const float x = empty ? 0.0f : o[2 * i] * f, y = empty ? 0.0f : o[2 * i + 1] * f;
-        w[i] = f32_to_out_bits<DT>(x) | (f32_to_out_bits<DT>(y) << 16);
+        const v2f x = {empty ? 0.0f : o[2 * i] * f, empty ? 0.0f : o[2 * i + 1] * f};
+        if constexpr (DT == DT_BF16) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2b));
+        else w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2h));
     }
     *reinterpret_cast<v2i*>(a.y + row * a.D + d) = v2i{(int)w[0], (int)w[1]};
     if (d == 0 && a.lse != nullptr)

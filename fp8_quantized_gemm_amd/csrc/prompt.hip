@@ -137,6 +137,13 @@ __device__ __forceinline__ void take_nan(uint32_t (&nan)[DP / 64], const uint8_t
     for (int j = 0; j < DP / 64; ++j) nan[j] |= got[j];
 }
 
+// The larger of a lane's value and that of the lane 32 away.
+__device__ __forceinline__ float max_halves(float v)
+{
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
 // What a wave has of its 32 query rows: lane (r, hf) half of row r's channels (32 d + 8 i + 4 hf ..),
 // the row's reference, and its own keys' share of the denominator; a bit of `nan` for each channel
 // that has seen NaN.
@@ -149,7 +156,7 @@ struct Rows {
 };
 
 // A tile's terms.  whole: every row sees every key; clean: room for a tile of values.
-template <int DT, int DP>
+template <int DT, int DP, bool WIDE>
 __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const PageScales& sc, const KeyRange& see,
                                          int key0, bool valid, bool whole, uint8_t* clean)
 {
@@ -175,7 +182,8 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
                 s[tb] = mfma32<DT>(Half<DT>::widen(k[tb][2 * e], k[tb][2 * e + 1]), x.q[c][e], s[tb]);
     }
     if (!whole) {
-        const bool on_page[2] = {__shfl(valid ? 1 : 0, hf) != 0, __shfl(valid ? 1 : 0, 2 + hf) != 0};
+        const bool on_page[2] = {WIDE ? valid : __shfl(valid ? 1 : 0, hf) != 0,
+                                 WIDE ? valid : __shfl(valid ? 1 : 0, 2 + hf) != 0};
         v8h seen[2][2];
 #pragma unroll
         for (int tb = 0; tb < 2; ++tb) {
@@ -196,14 +204,14 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
     float ks[2], lv[2], top[2];
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb) {
-        ks[tb] = __shfl(sc.key, 2 * tb + hf);
-        lv[tb] = __shfl(sc.log_value, 2 * tb + hf);
+        ks[tb] = WIDE ? sc.key : __shfl(sc.key, 2 * tb + hf);
+        lv[tb] = WIDE ? sc.log_value : __shfl(sc.log_value, 2 * tb + hf);
         top[tb] = s[tb][0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top[tb] = fmaxf(top[tb], s[tb][i]);
         top[tb] = __builtin_fmaf(top[tb], ks[tb], lv[tb]);
     }
-    const float both = fmaxf(top[0], top[1]), highest = fmaxf(both, __shfl_xor(both, 32));
+    const float both = fmaxf(top[0], top[1]), highest = max_halves(both);
     if (__any(highest > x.m + kSlack)) {
         const float m1 = fmaxf(x.m, highest);
         const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.m - m1);
@@ -228,7 +236,7 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
             p[tb][i >> 3][i & 7] = w[0];
             p[tb][i >> 3][(i & 7) + 1] = w[1];
         }
-        x.l = __builtin_fmaf(sum, __shfl(sc.inverse_value, 2 * tb + hf), x.l);
+        x.l = __builtin_fmaf(sum, WIDE ? sc.inverse_value : __shfl(sc.inverse_value, 2 * tb + hf), x.l);
     }
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb)
@@ -301,18 +309,19 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     }
 
     // A tile's keys in four groups of 16, each on one page; lane i of a wave keeps what is known of
-    // group i % 4.
-    const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
-    const int group_key = 16 * (lane & 3);
+    // group i % 4 (where a page holds whole tiles all lanes the same).
+    const uint32_t page_bytes = (uint32_t)(a.P * a.D), pool_stride = (uint32_t)a.Hk * page_bytes;
+    const int group_key = WIDE ? 0 : 16 * (lane & 3);
+    const uint8_t* const kbase = a.k_pages + (uint32_t)h * page_bytes;
+    const uint8_t* const vbase = a.v_pages + (uint32_t)h * page_bytes;
     const auto load_tile = [&](const PageRef& p, uint8_t* dst) {
         if constexpr (WIDE) {
             // the tile is on one page: a lane's offsets are the same in every tile; channels past D
             // are out of the buffer's range (values) or sent there (keys) and become 0
-            const int64_t page = uniform((int)p.page);
-            const int inside = uniform(p.inside);
-            const v4i rk = rsrc_words(a.k_pages + page * pool_stride + h * page_bytes + inside * a.D, kKeys * a.D);
-            const v4i rv = rsrc_words(a.v_pages + page * pool_stride + h * page_bytes + inside,
-                                      (int)page_bytes - inside);
+            const uint64_t at = (uint64_t)(uint32_t)uniform((int)p.page) * pool_stride;
+            const uint32_t inside = (uint32_t)uniform(p.inside);
+            const v4i rk = rsrc_words(kbase + at + inside * (uint32_t)a.D, kKeys * a.D);
+            const v4i rv = rsrc_words(vbase + at + inside, (int)(page_bytes - inside));
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
@@ -325,9 +334,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
                 buffer_to_lds(rv, dst + T::kKeyBytes + (wave * VB + j) * 1024, (uint32_t)(d * a.P + 16 * g));
             }
         } else {
-            const int64_t page_at = p.page * pool_stride + h * page_bytes;
-            const uint8_t* const kp = a.k_pages + page_at + (int64_t)p.inside * a.D;
-            const uint8_t* const vp = a.v_pages + page_at + p.inside;
+            const uint64_t at = (uint64_t)(uint32_t)p.page * pool_stride;
+            const uint8_t* const kp = kbase + at + (uint32_t)(p.inside * a.D);
+            const uint8_t* const vp = vbase + at + (uint32_t)p.inside;
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 const int unit = (wave * KB + j) * 64 + lane, row = unit / T::kUnits;
@@ -386,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
 
         const bool whole = wfirst.lo <= key0 && wlast.lo <= key0 && wfirst.hi >= key0 + kKeys &&
                            wlast.hi >= key0 + kKeys && __all(valid);
-        add_tile<DT, DP>(x, kt, now, see, key0, valid, whole, clean[wave]);
+        add_tile<DT, DP, WIDE>(x, kt, now, see, key0, valid, whole, clean[wave]);
     }
 
     x.l += __shfl_xor(x.l, 32);
