@@ -39,17 +39,17 @@ __device__ __forceinline__ uint32_t lds_address(const void* p)
 {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
-__device__ __forceinline__ void buffer_to_lds(const v4i& rsrc, void* lds_block, uint32_t offset)
+__device__ __forceinline__ void buffer_to_lds(const v4i& rsrc, uint32_t lds_block, uint32_t offset)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
-                     uniform((int)lds_address(lds_block))),
+                     uniform((int)lds_block)),
                  "v"(offset), "s"(rsrc)
                  : "memory", "m0");
 }
-__device__ __forceinline__ void global_to_lds(const uint8_t* src, void* lds_block)
+__device__ __forceinline__ void global_to_lds(const uint8_t* src, uint32_t lds_block)
 {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
-                     uniform((int)lds_address(lds_block))),
+                     uniform((int)lds_block)),
                  "v"(src)
                  : "memory", "m0");
 }
@@ -314,7 +314,8 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     const int group_key = WIDE ? 0 : 16 * (lane & 3);
     const uint8_t* const kbase = a.k_pages + (uint32_t)h * page_bytes;
     const uint8_t* const vbase = a.v_pages + (uint32_t)h * page_bytes;
-    const auto load_tile = [&](const PageRef& p, uint8_t* dst) {
+    const uint32_t lds_at = lds_address(&lds[0][0]);
+    const auto load_tile = [&](const PageRef& p, uint32_t dst) {
         if constexpr (WIDE) {
             // the tile is on one page: a lane's offsets are the same in every tile; channels past D
             // are out of the buffer's range (values) or sent there (keys) and become 0
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     int64_t cell = next.page * a.Hk + h;
     float next_k = a.k_scale[cell], next_v = a.v_scale[cell];
     next_id = id_of(t0 + 1);
-    if (t0 < t1) load_tile(next, lds[0]);
+    if (t0 < t1) load_tile(next, lds_at);
     for (int t = t0; t < t1; ++t) {
         const uint8_t* const kt = lds[(t - t0) & 1];
         wait_vm<0>();
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
             next_k = a.k_scale[cell];
             next_v = a.v_scale[cell];
             next_id = id_of(t + 2);
-            load_tile(next, lds[(t + 1 - t0) & 1]);
+            load_tile(next, lds_at + ((t + 1 - t0) & 1) * (uint32_t)sizeof(lds[0]));
         }
         const PageScales now = page_scales(a, now_k, now_v);
         const int key0 = t * kKeys;
