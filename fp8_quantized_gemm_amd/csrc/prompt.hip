@@ -252,6 +252,52 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
         }
 }
 
+// The workgroups of a key/value head take units of kTileRows rows of one sequence; this gives the
+// `place`-th one its sequence and first row.  Places follow each other as the workgroups start: the
+// first kFirst go to a compute unit each, the next kFirst join them, the others follow where one
+// ends.  Under a causal mask a unit's time is its last position, so the longest units come first,
+// then the shortest, so that every compute unit has one of both, then the rest.
+__device__ __forceinline__ int64_t rank_of(int64_t place, int64_t count, int first)
+{
+    if (place < first) return place;
+    if (place < 2 * (int64_t)first) return count - 1 - (place - first);
+    return place - first;
+}
+__device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t place, int64_t units, int* lds, int& b, int& row0)
+{
+    const PagedBatch& s = a.batch;
+    const int first = (kCUs + a.Hk - 1) / a.Hk, lane = threadIdx.x & 63;
+    if (s.B <= 64) {
+        // ranked by the sequences' lengths, the last rows of each first
+        PagedSeq q{0, 0, 0, 0};
+        if (lane < s.B) q = paged_seq(s, lane, a.P);
+        const int tiles = (int)(((int64_t)q.n * a.group + kTileRows - 1) / kTileRows);
+        int before = 0, count = 0;
+        for (int k = 0; k < s.B; ++k) {
+            const int t = __builtin_amdgcn_readlane(tiles, k), len = __builtin_amdgcn_readlane(q.len, k);
+            before += len > q.len || (len == q.len && k < lane) ? t : 0;
+            count += t;
+        }
+        if (place >= count) return false;
+        const int rank = (int)rank_of(place, count, first);
+        const uint64_t here = __ballot(rank >= before && rank < before + tiles);
+        b = (int)__builtin_ctzll(here);
+        row0 = (__builtin_amdgcn_readlane(tiles, b) - 1 - (rank - __builtin_amdgcn_readlane(before, b))) * kTileRows;
+        return true;
+    }
+    // in the sequences' order; those of sequence b begin at unit q_start[b] * group / kTileRows + b
+    if (place >= units) return false;
+    const int64_t u = units - 1 - rank_of(place, units, first);
+    int below = 0;
+    for (int k = threadIdx.x; k < s.B; k += kThreads)
+        below += (int64_t)clamp_int(s.q_start[k], 0, s.T) * a.group / kTileRows + k <= u ? 1 : 0;
+    b = uniform(max(block_sum_int<kThreads>(below, lds) - 1, 0));
+    const PagedSeq q = paged_seq(s, b, a.P);
+    const int64_t row = (u - ((int64_t)q.row * a.group / kTileRows + b)) * kTileRows;
+    row0 = (int)row;
+    return row >= 0 && row < (int64_t)q.n * a.group;
+}
+
 template <int DT, int DP, bool WIDE>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_kernel(const AttendArgs a, int64_t units)
 {
@@ -263,21 +309,12 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     __shared__ int found[kWaves];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, hf = lane >> 5;
-    // units of kTileRows rows; those of sequence b begin at unit q_start[b] * group / kTileRows + b.
-    // The last ones first: under a causal mask they are the longest.
     const int64_t index = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int h = (int)(index % a.Hk);
-    const int64_t u = units - 1 - index / a.Hk;
-    if (u < 0) return;
-    int below = 0;
-    for (int b = tid; b < a.batch.B; b += kThreads)
-        below += (int64_t)clamp_int(a.batch.q_start[b], 0, a.batch.T) * a.group / kTileRows + b <= u ? 1 : 0;
-    const int b = uniform(max(block_sum_int<kThreads>(below, found) - 1, 0));
+    int b, row0;
+    if (!find_unit(a, index / a.Hk, units, found, b, row0)) return;
     const PagedSeq q = paged_seq(a.batch, b, a.P);
-    const int64_t rows64 = (int64_t)q.n * a.group;
-    const int64_t row64 = (u - ((int64_t)q.row * a.group / kTileRows + b)) * kTileRows;
-    if (row64 < 0 || row64 >= rows64) return;
-    const int row0 = (int)row64, rows = (int)(rows64 - row64 < kTileRows ? rows64 - row64 : kTileRows);
+    const int rows = min(q.n * a.group - row0, kTileRows);
 
     const int wave_row0 = row0 + wave * kWaveRows;
     const int my_row = wave_row0 + r, token = my_row / a.group, head = h * a.group + my_row % a.group;
