@@ -400,34 +400,61 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     x.m = -__builtin_inff();
     x.l = 0.0f;
 
-    // A tile's codes and scales are requested a tile ahead and its pages' ids two.  What is loaded to
-    // registers is requested before the codes and not touched before the next tile: loads return in
-    // order, and a use would wait for the codes as well.
+    // A tile's codes are requested a tile ahead.  WIDE: lane i of a wave keeps what is known of the
+    // tile's page with the i-th of 64 tiles, loaded when the first of them is requested.
+    PageRef many{0, 0, false};
+    PageScales many_scales{};
+    uint64_t many_valid = 0;
+    const auto look_up = [&](int t) {
+        const int key = (t + lane) * kKeys;
+        many = page_ref(a, b, q.len, key);
+        many_scales = page_scales(a, many.page, h);
+        many_valid = __ballot(many.valid);
+    };
+    // Else its scales as well, and its pages' ids two tiles ahead.  What is loaded to registers is
+    // requested before the codes and not touched before the next tile: loads return in order, and a
+    // use would wait for the codes as well.
     const auto id_of = [&](int t) { return page_id(a, b, q.len, t * kKeys + group_key); };
-    int next_id = id_of(t0);
-    PageRef next = page_ref(a, next_id, t0 * kKeys + group_key);
-    bool next_valid = next.valid;
-    int64_t cell = next.page * a.Hk + h;
-    float next_k = a.k_scale[cell], next_v = a.v_scale[cell];
-    next_id = id_of(t0 + 1);
-    if (t0 < t1) load_tile(next, lds_at);
-    for (int t = t0; t < t1; ++t) {
-        const uint8_t* const kt = lds[(t - t0) & 1];
-        wait_vm<0>();
-        asm volatile("" : "+v"(next_k), "+v"(next_v), "+v"(next_id));
-        __syncthreads();                  // tile t is there, and tile t - 1 has been read
-        const float now_k = next_k, now_v = next_v;
-        const bool valid = next_valid;
-        if (t + 1 < t1) {
-            next = page_ref(a, next_id, (t + 1) * kKeys + group_key);
+    int next_id = 0;
+    bool next_valid = false;
+    float next_k = 0.0f, next_v = 0.0f;
+    const auto request = [&](int t, uint32_t dst) {
+        if constexpr (WIDE) {
+            const int i = (t - t0) & 63;
+            if (i == 0) look_up(t);
+            load_tile(PageRef{__builtin_amdgcn_readlane((int)many.page, i), (t * kKeys) & (a.P - 1), true}, dst);
+        } else {
+            const PageRef next = page_ref(a, next_id, t * kKeys + group_key);
+            const int64_t cell = next.page * a.Hk + h;
             next_valid = next.valid;
-            cell = next.page * a.Hk + h;
             next_k = a.k_scale[cell];
             next_v = a.v_scale[cell];
-            next_id = id_of(t + 2);
-            load_tile(next, lds_at + ((t + 1 - t0) & 1) * (uint32_t)sizeof(lds[0]));
+            next_id = id_of(t + 1);
+            load_tile(next, dst);
         }
-        const PageScales now = page_scales(a, now_k, now_v);
+    };
+    if (!WIDE) next_id = id_of(t0);
+    if (t0 < t1) request(t0, lds_at);
+    for (int t = t0; t < t1; ++t) {
+        const int at = (t - t0) & 1;
+        const uint8_t* const kt = lds[at];
+        wait_vm<0>();
+        if (!WIDE) asm volatile("" : "+v"(next_k), "+v"(next_v), "+v"(next_id));
+        __syncthreads();                  // tile t is there, and tile t - 1 has been read
+        PageScales now;
+        bool valid;
+        if constexpr (WIDE) {
+            const int i = (t - t0) & 63;
+            const auto lane_i = [&](float v) {
+                return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i));
+            };
+            now = PageScales{lane_i(many_scales.key), lane_i(many_scales.log_value), lane_i(many_scales.inverse_value)};
+            valid = (many_valid >> i & 1) != 0;
+        } else {
+            now = page_scales(a, next_k, next_v);
+            valid = next_valid;
+        }
+        if (t + 1 < t1) request(t + 1, lds_at + (at ^ 1) * (uint32_t)sizeof(lds[0]));
         const int key0 = t * kKeys;
         if (idle || key0 >= wlast.hi || key0 + kKeys <= wfirst.lo) continue;   // no row of this wave sees the tile
 
