@@ -684,18 +684,26 @@ PagedBufs paged_bufs(const fp8q_kv_cache& c, const fp8q_kv_batch& s)
 
 bool paged_head_dim_ok(int64_t D) { return D >= 16 && D <= kMaxHeadDim && D % 16 == 0; }
 
+fp8q_status check_paged_sizes(const fp8q_kv_cache& c, const fp8q_kv_batch& s)
+{
+    const int64_t P = c.page_size;
+    if (!(P == 16 || P == 32 || P == 64 || P == 128) || !paged_head_dim_ok(c.head_dim) || c.kv_heads < 1 ||
+        c.kv_heads > kMaxPagedHeads)
+        return FP8Q_ERR_SHAPE;
+    if (s.tokens < 1 || s.tokens > kMaxPagedTokens || s.seqs < 1 || s.seqs > kMaxPagedSeqs || s.max_q < 1 ||
+        s.max_q > s.tokens || s.table_width < 1 || s.table_width > kMaxPagedLen / P)
+        return FP8Q_ERR_SHAPE;
+    return FP8Q_OK;
+}
+
 fp8q_status check_paged(const fp8q_kv_cache* c, const fp8q_kv_batch* s)
 {
     if (!c || !s || !c->k || !c->v || !c->k_scale || !c->v_scale || !s->page_table || !s->q_start ||
         !s->kv_lens)
         return FP8Q_ERR_NULL;
-    const int64_t P = c->page_size;
-    if (!(P == 16 || P == 32 || P == 64 || P == 128) || !paged_head_dim_ok(c->head_dim) ||
-        c->kv_heads < 1 || c->kv_heads > kMaxPagedHeads || c->pages < 1 || c->pages > kMaxDim ||
-        c->pages > ((int64_t)1 << 42) / (c->kv_heads * P * c->head_dim))
-        return FP8Q_ERR_SHAPE;
-    if (s->tokens < 1 || s->tokens > kMaxPagedTokens || s->seqs < 1 || s->seqs > kMaxPagedSeqs ||
-        s->max_q < 1 || s->max_q > s->tokens || s->table_width < 1 || s->table_width > kMaxPagedLen / P)
+    FP8Q_TRY(check_paged_sizes(*c, *s));
+    if (c->pages < 1 || c->pages > kMaxDim ||
+        c->pages > ((int64_t)1 << 42) / (c->kv_heads * c->page_size * c->head_dim))
         return FP8Q_ERR_SHAPE;
     if (!aligned16(c->k) || !aligned16(c->v) || !aligned4(c->k_scale) || !aligned4(c->v_scale) ||
         !aligned4(s->page_table) || !aligned4(s->q_start) || !aligned4(s->kv_lens))
@@ -763,13 +771,35 @@ fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch
     return finish("fp8_kv_append", launch_kv_append(a, dtype, (hipStream_t)stream));
 }
 
-int64_t fp8_paged_attention_work_bytes(int64_t q_heads, int64_t kv_heads, int64_t head_dim,
-                                       int64_t max_q)
+namespace {
+bool query_heads_ok(int64_t q_heads, int64_t kv_heads)
 {
-    if (kv_heads < 1 || kv_heads > kMaxPagedHeads || q_heads < 1 || q_heads > kMaxPagedHeads ||
-        q_heads % kv_heads != 0 || !paged_head_dim_ok(head_dim) || max_q < 1 || max_q > kMaxPagedTokens)
+    return q_heads >= 1 && q_heads <= kMaxPagedHeads && q_heads % kv_heads == 0;
+}
+AttendArgs attend_args(const fp8q_kv_cache& c, const fp8q_kv_batch& s, int64_t q_heads)
+{
+    AttendArgs a{};
+    a.batch = paged_batch(s);
+    a.k_pages = c.k;
+    a.v_pages = c.v;
+    a.k_scale = c.k_scale;
+    a.v_scale = c.v_scale;
+    a.pages = (int)c.pages;
+    a.Hk = (int)c.kv_heads;
+    a.P = (int)c.page_size;
+    a.page_shift = __builtin_ctz((unsigned)c.page_size);
+    a.D = (int)c.head_dim;
+    a.Hq = (int)q_heads;
+    a.group = (int)(q_heads / c.kv_heads);
+    return a;
+}
+}  // namespace
+
+int64_t fp8_paged_attention_work_bytes(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch, int64_t q_heads)
+{
+    if (!cache || !batch || check_paged_sizes(*cache, *batch) != FP8Q_OK || !query_heads_ok(q_heads, cache->kv_heads))
         return 0;
-    return attend_work_bytes(q_heads, kv_heads, head_dim, max_q);
+    return attend_work_bytes(attend_args(*cache, *batch, q_heads));
 }
 
 fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch,
@@ -781,23 +811,27 @@ fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch*
     if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
     FP8Q_TRY(check_paged(cache, batch));
     const int64_t D = cache->head_dim, Hk = cache->kv_heads, T = batch->tokens;
-    if (q_heads < 1 || q_heads > kMaxPagedHeads || q_heads % Hk != 0 || !stride_ok(q_stride, q_heads, D) ||
+    if (!query_heads_ok(q_heads, Hk) || !stride_ok(q_stride, q_heads, D) ||
         !(scale >= -FLT_MAX && scale <= FLT_MAX) || window < 0 || window > kMaxPagedLen ||
         (window > 0 && !causal))
         return FP8Q_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(y) || !aligned16(work) || !aligned4(lse)) return FP8Q_ERR_ALIGN;
     const PagedBufs p = paged_bufs(*cache, *batch);
     const Buf by{y, 2 * u64(T) * u64(q_heads) * u64(D)}, bl{lse, lse ? 4 * u64(T) * u64(q_heads) : 0},
-        bw{work, u64(fp8_paged_attention_work_bytes(q_heads, Hk, D, batch->max_q))};
+        bw{work, u64(fp8_paged_attention_work_bytes(cache, batch, q_heads))};
     FP8Q_TRY(check_apart({by, bl, bw}, {rows_of(q, T, q_heads, D, q_stride).span(), p.k, p.v, p.ks, p.vs,
                                         p.table, p.start, p.lens}));
     FP8Q_TRY(check_device());
-    const AttendArgs a{paged_batch(*batch), cache->k, cache->v, cache->k_scale, cache->v_scale,
-                       (const uint16_t*)q, y, lse, (float*)work, q_stride, (int)cache->pages, (int)Hk,
-                       (int)cache->page_size, __builtin_ctz((unsigned)cache->page_size), (int)D, (int)q_heads,
-                       (int)(q_heads / Hk),
-                       std::fabs(scale) * 1.4426950408889634f, scale < 0 ? (int)0x80008000u : 0,
-                       causal != 0, (int)window};
+    AttendArgs a = attend_args(*cache, *batch, q_heads);
+    a.q = (const uint16_t*)q;
+    a.y = y;
+    a.lse = lse;
+    a.work = (float*)work;
+    a.q_stride = q_stride;
+    a.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
+    a.q_flip = scale < 0 ? (int)0x80008000u : 0;
+    a.causal = causal != 0;
+    a.window = (int)window;
     return finish("fp8_paged_attention", launch_paged_attention(a, dtype, (hipStream_t)stream));
 }
 

@@ -1,5 +1,5 @@
 // Attention over the paged FP8 cache for few query rows (see paged.hpp).
-#include "attend.hpp"
+#include "join.hpp"
 
 namespace fp8q {
 namespace {
@@ -96,17 +96,11 @@ __device__ __forceinline__ int64_t scan_sequences(const AttendArgs& a, ScanLds& 
     return total;
 }
 
-// A piece of a unit that its wave has not whole; parts: how many workgroups have some of it.
-struct Unit {
-    int64_t at;                           // the unit's first place
-    int parts, begins, ends, token0, head, row0, rows, unused;
-};
-
 // The scratch: for each workgroup the unit that it begins and another one ends (parts = 0:
 // none), then its two partial results, of a unit that it goes on with and of one that it
 // begins: kRows rows of maximum, denominator and, from the fifth float on, DP sums.
 template <int DP>
-__device__ __forceinline__ float* part_of(float* work, int groups, int64_t group, bool begins)
+__host__ __device__ __forceinline__ float* part_of(float* work, int groups, int64_t group, bool begins)
 {
     return work + groups * (int)(sizeof(Unit) / 4) + (group * 2 + (begins ? 1 : 0)) * (kRows * (DP + 4));
 }
@@ -453,63 +447,6 @@ __global__ void __launch_bounds__(waves_for(DP, SHARED) * 64, DP <= 128 ? 2 : 1)
     if (SHARED && threadIdx.x == 0 && !told) reinterpret_cast<Unit*>(a.work)[blockIdx.x].parts = 0;
 }
 
-// Joins the partial results of a unit that several workgroups had, told by the
-// first of them: a workgroup for each row.  D / 4 threads have a share of the
-// parts; the factors of all parts come first, so that no load waits for another.
-template <int DT, int DP>
-__global__ void __launch_bounds__(kThreads) attend_join_kernel(const AttendArgs a)
-{
-    constexpr int kGroups = groups_for(DP);
-    __shared__ float factor[kGroups], red[2][kWaves];
-    __shared__ __attribute__((aligned(16))) float sums[kThreads * 4];
-    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Unit u = reinterpret_cast<const Unit*>(a.work)[blockIdx.x];
-    if (u.parts == 0 || row >= u.rows) return;
-    // parts lie two partial results apart, but the first, which begins the unit
-    const float* const first = part_of<DP>(a.work, gridDim.x, blockIdx.x, true) + row * (DP + 4);
-    const float* const other = part_of<DP>(a.work, gridDim.x, blockIdx.x, false) + row * (DP + 4);
-    constexpr int64_t step = 2 * kRows * (DP + 4);
-    constexpr int kEach = (kGroups + kThreads - 1) / kThreads;
-    float pm[kEach], pl[kEach], m = -__builtin_inff(), l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        const int k = tid + e * kThreads;
-        const float* p = k == 0 ? first : other + k * step;
-        pm[e] = k < u.parts ? p[0] : -__builtin_inff();
-        pl[e] = k < u.parts ? p[1] : 0.0f;
-        m = fmaxf(m, pm[e]);
-    }
-    m = wave_max(m);
-    if (lane == 0) red[0][wave] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red[0][w]);
-    const float ref = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-        const int k = tid + e * kThreads;
-        const float f = __builtin_amdgcn_exp2f(pm[e] - ref);
-        if (k < u.parts) { factor[k] = f; l += pl[e] * f; }
-    }
-    l = wave_sum(l);
-    if (lane == 0) red[1][wave] = l;
-    __syncthreads();
-    const int quads = a.D / 4, sets = kThreads / quads, set = tid / quads, d = tid % quads * 4;
-    v4f o = {0.f, 0.f, 0.f, 0.f};
-    if (set < sets) {
-#pragma unroll 4
-        for (int k = set; k < u.parts; k += sets)
-            o += *reinterpret_cast<const v4f*>((k == 0 ? first : other + k * step) + 4 + d) * factor[k];
-        *reinterpret_cast<v4f*>(&sums[4 * tid]) = o;
-    }
-    __syncthreads();
-    if (set != 0) return;
-    for (int k = 1; k < sets; ++k) o += *reinterpret_cast<const v4f*>(&sums[4 * (k * quads + tid)]);
-    const Joined j{m, ref, red[1][0] + red[1][1] + red[1][2] + red[1][3]};
-    const int gr = u.row0 + row;
-    store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, j);
-}
-
 template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
@@ -523,9 +460,12 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
     hipLaunchKernelGGL((attend_rows_kernel<DT, DP, WIDE, true>), dim3(groups_for(DP)), dim3(kThreads), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attend_join_kernel<DT, DP>), dim3(groups_for(DP), rows < kRows ? rows : kRows),
-                       dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+    constexpr int groups = groups_for(DP);
+    const Parts parts{reinterpret_cast<const Unit*>(a.work), part_of<DP>(a.work, groups, 0, true),
+                      part_of<DP>(a.work, groups, 0, false), 2 * kRows * (DP + 4), 2 * kRows * (DP + 4)};
+    // the parts that a unit has, about
+    const int64_t units = a.batch.B * a.Hk * ((rows + kRows - 1) / kRows);
+    return launch_join<DT, DP>(a, parts, groups, (int)(rows < kRows ? rows : kRows), (int)(groups / units), stream);
 }
 
 template <int DT, int DP>
@@ -545,16 +485,17 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
 
 }  // namespace
 
-int64_t attend_work_bytes(int64_t, int64_t, int64_t D, int64_t)
-{
-    const int64_t dp = (D + 63) / 64 * 64;
-    return groups_for((int)dp) * ((int64_t)sizeof(Unit) + 2 * kRows * (dp + 4) * 4);
-}
-
 hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream)
 {
-    if ((int64_t)a.batch.max_q * a.group > 32) return launch_attend_prompt(a, dtype, stream);
+    if (attend_many_rows(a)) return launch_attend_prompt(a, dtype, stream);
     return dtype == DT_BF16 ? launch<DT_BF16>(a, stream) : launch<DT_FP16>(a, stream);
+}
+
+int64_t attend_work_bytes(const AttendArgs& a)
+{
+    if (attend_many_rows(a)) return attend_prompt_work_bytes(a);
+    const int64_t dp = (a.D + 63) / 64 * 64;
+    return groups_for((int)dp) * ((int64_t)sizeof(Unit) + 2 * kRows * (dp + 4) * 4);
 }
 
 }  // namespace fp8q

@@ -71,8 +71,12 @@ struct AttendArgs {
     int q_flip;                      // sign bits of two queries where the scale is negative, else 0
     int causal, window;
 };
+// The kernels for many query rows are taken from more than 32 rows a key/value head on.
+inline bool attend_many_rows(const AttendArgs& a) { return (int64_t)a.batch.max_q * a.group > 32; }
 hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream);
-int64_t attend_work_bytes(int64_t Hq, int64_t Hk, int64_t D, int64_t max_q);
+int64_t attend_prompt_work_bytes(const AttendArgs& a);
+// Bytes of scratch; looks at the sizes in `a` only.
+int64_t attend_work_bytes(const AttendArgs& a);
 hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream);
 
 }  // namespace fp8q

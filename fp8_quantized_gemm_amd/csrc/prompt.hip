@@ -11,7 +11,7 @@
 // (the rows of K are put in LDS in the order that makes it so), which are the
 // lane's part of the second product's operand, so P needs no exchange between
 // lanes, and a row's maximum one.
-#include "attend.hpp"
+#include "join.hpp"
 #include "tile.hpp"
 
 namespace fp8q {
@@ -21,6 +21,8 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 
 constexpr int kWaves = 4, kThreads = kWaves * 64, kWaveRows = 32, kTileRows = kWaves * kWaveRows;
 constexpr int kKeys = 64;                 // keys of a tile
+constexpr int kLeastTiles = 4;            // of a part of a unit
+constexpr int kEnough = 384, kWanted = 768;
 
 template <int DT>
 __device__ __forceinline__ v16f mfma32(typename Half<DT>::vec a, v4i b, v16f c)
@@ -41,17 +43,21 @@ __device__ __forceinline__ uint32_t lds_address(const void* p)
 }
 __device__ __forceinline__ void buffer_to_lds(const v4i& rsrc, uint32_t lds_block, uint32_t offset)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(
-                     uniform((int)lds_block)),
-                 "v"(offset), "s"(rsrc)
-                 : "memory", "m0");
+    int m0;                               // kept for the compiler
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(uniform((int)lds_block)), "v"(offset), "s"(rsrc)
+                 : "memory");
 }
 __device__ __forceinline__ void global_to_lds(const uint8_t* src, uint32_t lds_block)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(
-                     uniform((int)lds_block)),
-                 "v"(src)
-                 : "memory", "m0");
+    int m0;
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %2, off\n\ts_mov_b32 m0, %0"
+                 : "=&s"(m0)
+                 : "s"(uniform((int)lds_block)), "v"(src)
+                 : "memory");
 }
 // The words of make_rsrc's resource.
 __device__ __forceinline__ v4i rsrc_words(const uint8_t* base, int bytes)
@@ -263,10 +269,11 @@ __device__ __forceinline__ int64_t rank_of(int64_t place, int64_t count, int fir
     if (place < 2 * (int64_t)first) return count - 1 - (place - first);
     return place - first;
 }
-__device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t place, int64_t units, int* lds, int& b, int& row0)
+__device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t place, int splits, int64_t units, int* lds,
+                                          int& b, int& row0)
 {
     const PagedBatch& s = a.batch;
-    const int first = (kCUs + a.Hk - 1) / a.Hk, lane = threadIdx.x & 63;
+    const int first = (kCUs + a.Hk * splits - 1) / (a.Hk * splits), lane = threadIdx.x & 63;
     if (s.B <= 64) {
         // ranked by the sequences' lengths, the last rows of each first
         PagedSeq q{0, 0, 0, 0};
@@ -298,8 +305,18 @@ __device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t place, in
     return row >= 0 && row < (int64_t)q.n * a.group;
 }
 
+// The scratch where units are cut: what each is, then its parts.
+template <int DP>
+constexpr int64_t kPart = kTileRows * (DP + 4);
+template <int DP>
+__host__ __device__ __forceinline__ float* parts_of(const AttendArgs& a, int64_t units)
+{
+    return a.work + units * a.Hk * (int64_t)(sizeof(Unit) / 4);
+}
+
 template <int DT, int DP, bool WIDE>
-__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_kernel(const AttendArgs a, int64_t units)
+__global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
+    attend_prompt_kernel(const AttendArgs a, int64_t units, int splits)
 {
     using T = Tile<DP>;
     constexpr int NC = DP / 32, ND = DP / 32;
@@ -312,7 +329,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     const int64_t index = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int h = (int)(index % a.Hk);
     int b, row0;
-    if (!find_unit(a, index / a.Hk, units, found, b, row0)) return;
+    const int64_t place = index / a.Hk / splits;
+    const int split = (int)(index / a.Hk % splits);
+    Unit* const told = reinterpret_cast<Unit*>(a.work) + place * a.Hk + h;
+    if (place >= units) return;
+    if (!find_unit(a, place, splits, units, found, b, row0)) {
+        if (splits > 1 && split == 0 && tid == 0) told->parts = 0;
+        return;
+    }
     const PagedSeq q = paged_seq(a.batch, b, a.P);
     const int rows = min(q.n * a.group - row0, kTileRows);
 
@@ -325,7 +349,16 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     const bool idle = wave_row0 >= row0 + rows;
     const int wave_last = min(wave_row0 + kWaveRows, row0 + rows) - 1;
     const KeyRange wfirst = key_range(a, q, wave_row0 / a.group), wlast = key_range(a, q, wave_last / a.group);
-    const int t0 = first.lo / kKeys, t1 = (last.hi + kKeys - 1) / kKeys;
+    int t0 = first.lo / kKeys, t1 = (last.hi + kKeys - 1) / kKeys, parts = 1;
+    if (splits > 1) {
+        const int each = max((t1 - t0 + splits - 1) / splits, kLeastTiles);
+        parts = max((t1 - t0 + each - 1) / each, 1);
+        if (split == 0 && tid == 0)
+            *told = Unit{0, parts > 1 ? parts : 0, 1, 1, q.row, h, row0, rows, 0};
+        if (split >= parts) return;
+        t0 += split * each;
+        t1 = min(t0 + each, t1);
+    }
 
     Rows<DP> x;
     {
@@ -466,6 +499,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
     x.l += __shfl_xor(x.l, 32);
     if (!have_row) return;
     const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
+    float* const part = parts_of<DP>(a, units) + ((place * a.Hk + h) * splits + split) * kPart<DP> +
+                        (wave * kWaveRows + r) * (DP + 4);
+    if (parts > 1 && hf == 0) { part[0] = x.m; part[1] = x.l; }
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -475,18 +511,39 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1) attend_prompt_ker
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 o[i] = (x.nan[d >> 1] >> (16 * (d & 1) + 4 * e + i) & 1u) != 0 ? __builtin_nanf("") : x.acc[d][4 * e + i];
-            if (c < a.D) store_row<DT>(a, q.row + token, head, c, o, j);
+            if (c >= a.D) continue;
+            if (parts > 1) *reinterpret_cast<v4f*>(part + 4 + c) = o;
+            else store_row<DT>(a, q.row + token, head, c, o, j);
         }
+}
+
+// Units of all sequences at most, and into how many parts of the keys each is cut: where they are
+// fewer than the workgroups that fit the chip.
+struct Cut {
+    int64_t units;
+    int splits;
+};
+Cut cut_of(const AttendArgs& a)
+{
+    const int64_t units = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B, groups = units * a.Hk;
+    const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys, most = (tiles + kLeastTiles - 1) / kLeastTiles;
+    int64_t splits = groups >= kEnough ? 1 : (kWanted + groups - 1) / groups;
+    splits = splits < most ? splits : most;
+    return Cut{units, (int)(splits < 1 ? 1 : splits > kMostParts ? kMostParts : splits)};
 }
 
 template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    const int64_t units = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
-    const int64_t groups = units * a.Hk, most = max_groups(kThreads), gx = groups < most ? groups : most;
+    const Cut cut = cut_of(a);
+    const int64_t groups = cut.units * a.Hk * cut.splits, most = max_groups(kThreads), gx = groups < most ? groups : most;
     hipLaunchKernelGGL((attend_prompt_kernel<DT, DP, WIDE>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
-                       dim3(kThreads), 0, stream, a, units);
-    return hipGetLastError();
+                       dim3(kThreads), 0, stream, a, cut.units, cut.splits);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || cut.splits == 1) return e;
+    const float* const parts = parts_of<DP>(a, cut.units);
+    return launch_join<DT, DP>(a, Parts{reinterpret_cast<const Unit*>(a.work), parts, parts, cut.splits * kPart<DP>, kPart<DP>},
+                               (int)(cut.units * a.Hk), kTileRows, cut.splits, stream);
 }
 
 template <int DT, int DP>
@@ -505,6 +562,14 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
 }
 
 }  // namespace
+
+int64_t attend_prompt_work_bytes(const AttendArgs& a)
+{
+    const Cut cut = cut_of(a);
+    if (cut.splits == 1) return 16;
+    const int64_t dp = (a.D + 63) / 64 * 64;
+    return cut.units * a.Hk * ((int64_t)sizeof(Unit) + cut.splits * kTileRows * (dp + 4) * 4);
+}
 
 hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream)
 {

@@ -72,7 +72,7 @@ _SIGS = {
                                _i64, _i, _p]),
     "fp8_kv_append": (_i, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _p, _i64, _p, _i64,
                            _i, _p, _i64, _i64, _i, _p, _i64, _p, _i64, _i64, _p]),
-    "fp8_paged_attention_work_bytes": (_i64, [_i64, _i64, _i64, _i64]),
+    "fp8_paged_attention_work_bytes": (_i64, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _i64]),
     "fp8_paged_attention": (_i, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _p, _i64, _i,
                                  _i64, ctypes.c_float, _i, _i64, _p, _p, _p, _p]),
 }
@@ -556,16 +556,20 @@ def fp8_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pag
     return q_out
 
 
-def paged_attention_work_bytes(q_heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
+def paged_attention_work_bytes(tokens: int, seqs: int, table_width: int, max_q: int, q_heads: int,
+                               kv_heads: int, page_size: int, head_dim: int) -> int:
     """Bytes of scratch fp8_paged_attention needs (0 for sizes it refuses)."""
-    return int(lib.fp8_paged_attention_work_bytes(q_heads, kv_heads, head_dim, max_q))
+    return int(lib.fp8_paged_attention_work_bytes(
+        _KvCache(None, None, None, None, 1, kv_heads, page_size, head_dim),
+        _KvBatch(None, None, None, tokens, seqs, table_width, max_q), q_heads))
 
 
 def paged_attention_work(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor,
                          max_q: int) -> torch.Tensor:
     """Scratch for fp8_paged_attention calls of these sizes.  Calls that may run at the same
     time need one each, and so do captured graphs that may."""
-    need = paged_attention_work_bytes(q.shape[1], k_pages.shape[1], k_pages.shape[3], max_q)
+    need = paged_attention_work_bytes(q.shape[0], page_table.shape[0], page_table.shape[1], max_q,
+                                      q.shape[1], k_pages.shape[1], k_pages.shape[2], k_pages.shape[3])
     return torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
 
 
@@ -595,7 +599,7 @@ def fp8_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
         y = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None:
         lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
-    need = lib.fp8_paged_attention_work_bytes(heads, cache.kv_heads, cache.head_dim, max_q)
+    need = lib.fp8_paged_attention_work_bytes(cache, batch, heads)
     if work is None:
         # never empty: sizes that need is 0 for are refused below, as sizes
         work = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)

@@ -554,10 +554,11 @@ FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_bat
  *          run at the same time need one each.
  *   q_heads % kv_heads == 0, q_heads <= 1024;  scale finite;
  *   0 <= window <= 2^24.
- *   fp8_paged_attention_work_bytes gives 0 for sizes that the call refuses.
+ *   fp8_paged_attention_work_bytes looks at the sizes in the structs only (pages
+ *   apart, which does not matter), and gives 0 for sizes that the call refuses.
  */
-FP8Q_API int64_t fp8_paged_attention_work_bytes(int64_t q_heads, int64_t kv_heads,
-                                                int64_t head_dim, int64_t max_q);
+FP8Q_API int64_t fp8_paged_attention_work_bytes(const fp8q_kv_cache* cache,
+                                                const fp8q_kv_batch* batch, int64_t q_heads);
 FP8Q_API fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch,
                                          const void* q, int64_t q_stride, int dtype,
                                          int64_t q_heads, float scale, int causal, int64_t window,

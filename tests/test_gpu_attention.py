@@ -99,7 +99,8 @@ def test_prompts(heads, kv_heads, dim, page, causal, window, dtype):
     run(bt, heads, dtype, causal, window)
 
 
-@pytest.mark.parametrize("heads,kv_heads,new,length", [(8, 1, 1, 9001), (2, 2, 1, 4500), (4, 1, 3, 5003)])
+@pytest.mark.parametrize("heads,kv_heads,new,length", [(8, 1, 1, 9001), (2, 2, 1, 4500), (4, 1, 3, 5003),
+                                                        (4, 1, 33, 4700), (2, 2, 40, 9000)])
 def test_long_contexts(heads, kv_heads, new, length):
     say("long", heads, kv_heads, new, length)
     bt = ref.Batch([new, 1, new], [length, 3, 70], kv_heads, 64, 64, seed=6)

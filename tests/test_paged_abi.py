@@ -112,10 +112,13 @@ def test_overlap_of_interleaved_rows():
 
 
 def test_work_bytes():
-    assert fp8q.paged_attention_work_bytes(8, 2, 128, 1) > 0
-    for sizes in ((0, 1, 64, 1), (1, 0, 64, 1), (3, 2, 64, 1), (2048, 1, 64, 1), (1, 1, 24, 1),
-                  (1, 1, 272, 1), (1, 1, 64, 0)):
-        assert fp8q.paged_attention_work_bytes(*sizes) == 0
+    good = dict(tokens=4, seqs=2, table_width=20, max_q=2, q_heads=8, kv_heads=2, page_size=64, head_dim=128)
+    assert fp8q.paged_attention_work_bytes(**good) > 0
+    assert fp8q.paged_attention_work_bytes(**{**good, "max_q": 4, "q_heads": 64}) > 0
+    for change in (dict(q_heads=0), dict(q_heads=3), dict(q_heads=2048), dict(kv_heads=0), dict(head_dim=24),
+                   dict(head_dim=272), dict(max_q=0), dict(max_q=5), dict(page_size=48), dict(seqs=0),
+                   dict(tokens=0), dict(table_width=0), dict(table_width=2 ** 18 + 1)):
+        assert fp8q.paged_attention_work_bytes(**{**good, **change}) == 0
 
 
 def test_binding_refuses_wrong_tensors():
