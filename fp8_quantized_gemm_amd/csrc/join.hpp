@@ -29,38 +29,54 @@ namespace {
 template <int DT, int DP, int R>
 __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, const Parts parts)
 {
-    constexpr int kEach = kJoinThreads / R;
-    __shared__ float stat[R][kMostParts][2];
+    constexpr int kEach = kJoinThreads / R, kLanes = kEach < 64 ? kEach : 64, kWaves = kJoinThreads / 64;
+    __shared__ float factor[R][kMostParts], red[2][kWaves];
     __shared__ __attribute__((aligned(16))) float sums[kJoinThreads * 4];
     const Unit u = parts.units[blockIdx.x];
     const int mine = threadIdx.x / kEach, tid = threadIdx.x % kEach, row = blockIdx.y * R + mine;
     if (u.parts == 0 || (int)(blockIdx.y * R) >= u.rows) return;
+    const int count = row < u.rows ? u.parts : 0;
     const int64_t at = blockIdx.x * parts.stride + (int64_t)row * (DP + 4);
     const auto part = [&](int k) { return k == 0 ? parts.first + at : parts.other + at + k * parts.step; };
-    if (row < u.rows)
-        for (int k = tid; k < u.parts; k += kEach) {
-            const float* p = part(k);
-            stat[mine][k][0] = p[0];
-            stat[mine][k][1] = p[1];
-        }
+    float m = -__builtin_inff(), l = 0.0f;
+    for (int k = tid; k < count; k += kEach) {
+        factor[mine][k] = part(k)[0];
+        m = fmaxf(m, factor[mine][k]);
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    if constexpr (kEach > 64) {
+        if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red[0][w]);
+    }
+    const float ref = m == -__builtin_inff() ? 0.0f : m;
+    for (int k = tid; k < count; k += kEach) {
+        const float f = __builtin_amdgcn_exp2f(factor[mine][k] - ref);
+        factor[mine][k] = f;
+        l += part(k)[1] * f;
+    }
+#pragma unroll
+    for (int off = kLanes / 2; off >= 1; off >>= 1) l += __shfl_xor(l, off);
+    if constexpr (kEach > 64) {
+        if ((threadIdx.x & 63) == 0) red[1][threadIdx.x >> 6] = l;
+    }
     __syncthreads();
     const int quads = a.D / 4, sets = kEach / quads, set = tid / quads, d = tid % quads * 4;
-    Joined j{-__builtin_inff(), 0.0f, 0.0f};
     v4f o = {0.f, 0.f, 0.f, 0.f};
-    if (row < u.rows && set < sets) {
-        for (int k = 0; k < u.parts; ++k) j.m = fmaxf(j.m, stat[mine][k][0]);
-        j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
-        for (int k = 0; k < u.parts; ++k) j.l += stat[mine][k][1] * __builtin_amdgcn_exp2f(stat[mine][k][0] - j.ref);
+    if (set < sets) {
 #pragma unroll 4
-        for (int k = set; k < u.parts; k += sets)
-            o += *reinterpret_cast<const v4f*>(part(k) + 4 + d) * __builtin_amdgcn_exp2f(stat[mine][k][0] - j.ref);
+        for (int k = set; k < count; k += sets)
+            o += *reinterpret_cast<const v4f*>(part(k) + 4 + d) * factor[mine][k];
         *reinterpret_cast<v4f*>(&sums[4 * threadIdx.x]) = o;
     }
     __syncthreads();
-    if (row >= u.rows || set != 0) return;
+    if (count == 0 || set != 0) return;
     for (int k = 1; k < sets; ++k) o += *reinterpret_cast<const v4f*>(&sums[4 * (threadIdx.x + k * quads)]);
+    if constexpr (kEach > 64) l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     const int gr = u.row0 + row;
-    store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, j);
+    store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, Joined{m, ref, l});
 }
 
 // `about`: the parts that a unit has, for the choice between a workgroup a row and one for several.
