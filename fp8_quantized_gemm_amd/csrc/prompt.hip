@@ -22,7 +22,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 constexpr int kWaves = 4, kThreads = kWaves * 64, kWaveRows = 32, kTileRows = kWaves * kWaveRows;
 constexpr int kKeys = 64;                 // keys of a tile
 constexpr int kLeastTiles = 4;            // of a part of a unit
-constexpr int kEnough = 384, kWanted = 768;
+constexpr int kRankedSeqs = 64;           // sequences that a wave ranks by length
 
 template <int DT>
 __device__ __forceinline__ v16f mfma32(typename Half<DT>::vec a, v4i b, v16f c)
@@ -274,7 +274,7 @@ __device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t place, in
 {
     const PagedBatch& s = a.batch;
     const int first = (kCUs + a.Hk * splits - 1) / (a.Hk * splits), lane = threadIdx.x & 63;
-    if (s.B <= 64) {
+    if (s.B <= kRankedSeqs) {
         // ranked by the sequences' lengths, the last rows of each first
         PagedSeq q{0, 0, 0, 0};
         if (lane < s.B) q = paged_seq(s, lane, a.P);
@@ -517,19 +517,21 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
         }
 }
 
-// Units of all sequences at most, and into how many parts of the keys each is cut: where they are
-// fewer than the workgroups that fit the chip.
+// Units of all sequences at most, and into how many parts of the keys each is cut: as many as make
+// one round of the workgroups that the chip holds at once.
 struct Cut {
     int64_t units;
     int splits;
 };
 Cut cut_of(const AttendArgs& a)
 {
-    const int64_t units = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B, groups = units * a.Hk;
+    const int64_t loose = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
+    const int64_t tight = a.batch.B * (((int64_t)a.batch.max_q * a.group + kTileRows - 1) / kTileRows);
+    const int64_t units = loose < tight ? loose : tight, slots = kCUs * (a.D <= 128 ? 2 : 1);
     const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys, most = (tiles + kLeastTiles - 1) / kLeastTiles;
-    int64_t splits = groups >= kEnough ? 1 : (kWanted + groups - 1) / groups;
+    int64_t splits = slots / (units * a.Hk);
     splits = splits < most ? splits : most;
-    return Cut{units, (int)(splits < 1 ? 1 : splits > kMostParts ? kMostParts : splits)};
+    return Cut{a.batch.B <= kRankedSeqs ? units : loose, (int)(splits < 1 ? 1 : splits > kMostParts ? kMostParts : splits)};
 }
 
 template <int DT, int DP, bool WIDE>
