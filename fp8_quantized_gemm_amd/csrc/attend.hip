@@ -112,29 +112,50 @@ struct KvTile {
     v4i k[4][DP / 64], v[DP / 16];
 };
 
-// The pages of a tile, asked for a tile ahead of its loads: where a page holds whole tiles
-// (WIDE) they are wave-uniform.
-template <bool WIDE>
-struct TilePages;
-template <>
-struct TilePages<true> {
-    PageRef p;
-    __device__ __forceinline__ const PageRef& mine() const { return p; }   // of the lane's terms
-};
-template <>
-struct TilePages<false> {
-    PageRef k, v;
-    __device__ __forceinline__ const PageRef& mine() const { return v; }
+// What a wave knows of the pages of the next tiles: lane i of the page with the i-th of 64 tiles where
+// a page holds whole tiles (WIDE), else of the i-th of 64 groups of 16 keys.  Looked up together, so
+// that no tile waits for its page's id or scales.
+struct Pages {
+    int page;                             // 0 where there is none
+    PageScales sc;
+    uint64_t valid;
 };
 template <bool WIDE>
-__device__ __forceinline__ TilePages<WIDE> tile_pages(const AttendArgs& a, int b, int len, int key0, int r, int g)
+constexpr int kLookUp = WIDE ? 64 : 16;   // tiles of a look-up
+template <bool WIDE>
+__device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, int key0, int h)
 {
-    if constexpr (WIDE) return {page_ref(a, b, len, key0)};
-    else return {page_ref(a, b, len, key0 + 16 * (r >> 2)), page_ref(a, b, len, key0 + 16 * g)};
+    const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
+    const PageRef p = page_ref(a, b, len, key);
+    return Pages{(int)p.page, page_scales(a, p.page, h), __ballot(p.valid)};
+}
+// What a lane needs of the i-th tile of a look-up: the pages of the keys and of the values that it
+// loads, the scales of its terms.
+struct TilePages {
+    int k, v, k_inside, v_inside;
+    PageScales sc;
+    bool valid;
+};
+template <bool WIDE>
+__device__ __forceinline__ TilePages tile_pages(const AttendArgs& a, const Pages& p, int i, int key0, int r, int g)
+{
+    if constexpr (WIDE) {
+        const auto lane_i = [&](float v) { return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), i)); };
+        const int page = __builtin_amdgcn_readlane(p.page, i), inside = key0 & (a.P - 1);
+        return TilePages{page, page, inside, inside,
+                         PageScales{lane_i(p.sc.key), lane_i(p.sc.log_value), lane_i(p.sc.inverse_value)},
+                         (p.valid >> i & 1) != 0};
+    } else {
+        const int ik = 4 * i + (r >> 2), iv = 4 * i + g;
+        return TilePages{__shfl(p.page, ik), __shfl(p.page, iv), (key0 + 16 * (r >> 2)) & (a.P - 1),
+                         (key0 + 16 * g) & (a.P - 1),
+                         PageScales{__shfl(p.sc.key, iv), __shfl(p.sc.log_value, iv), __shfl(p.sc.inverse_value, iv)},
+                         (p.valid >> iv & 1) != 0};
+    }
 }
 
 template <int DP, bool WIDE>
-__device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, const TilePages<WIDE>& p, int h,
+__device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, const TilePages& p, int h,
                                           int r, int g)
 {
     constexpr int NC = DP / 64;
@@ -142,8 +163,8 @@ __device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, co
     if constexpr (WIDE) {
         // buffer loads: one 32-bit offset a lane, the rest scalar; channels past D are sent out of
         // the buffer's range and read as 0
-        const rsrc_t rk = make_rsrc(a.k_pages + p.p.page * pool_stride + h * page_bytes + p.p.inside * a.D,
-                                    (uint32_t)((a.P - p.p.inside) * a.D));
+        const rsrc_t rk = make_rsrc(a.k_pages + p.k * pool_stride + h * page_bytes + p.k_inside * a.D,
+                                    (uint32_t)(kKeys * a.D));
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -154,8 +175,8 @@ __device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, co
                                                                   kPolicy);
             }
     } else {
-        const uint8_t* kt = a.k_pages + p.k.page * pool_stride + h * page_bytes +
-                            (int64_t)(p.k.inside + (r & 3)) * a.D;
+        const uint8_t* kt = a.k_pages + p.k * pool_stride + h * page_bytes +
+                            (int64_t)(p.k_inside + (r & 3)) * a.D;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -168,20 +189,20 @@ __device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, co
 }
 
 template <int DP, bool WIDE>
-__device__ __forceinline__ void load_values(const AttendArgs& a, KvTile<DP>& t, const TilePages<WIDE>& p, int h,
+__device__ __forceinline__ void load_values(const AttendArgs& a, KvTile<DP>& t, const TilePages& p, int h,
                                             int r, int g)
 {
     constexpr int ND = DP / 16;
     const int64_t page_bytes = (int64_t)a.P * a.D, pool_stride = a.Hk * page_bytes;
     if constexpr (WIDE) {
-        const rsrc_t rv = make_rsrc(a.v_pages + p.p.page * pool_stride + h * page_bytes + p.p.inside,
-                                    (uint32_t)(page_bytes - p.p.inside));
+        const rsrc_t rv = make_rsrc(a.v_pages + p.v * pool_stride + h * page_bytes + p.v_inside,
+                                    (uint32_t)(page_bytes - p.v_inside));
 #pragma unroll
         for (int d = 0; d < ND; ++d)
             t.v[d] = __builtin_amdgcn_raw_buffer_load_b128(rv, (uint32_t)(r * a.P + 16 * g),
                                                            uniform(16 * d * a.P), kPolicy);
     } else {
-        const uint8_t* vt = a.v_pages + p.v.page * pool_stride + h * page_bytes + p.v.inside;
+        const uint8_t* vt = a.v_pages + p.v * pool_stride + h * page_bytes + p.v_inside;
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
             t.v[d] = v4i{0, 0, 0, 0};
@@ -274,7 +295,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const Seq
     const KeyRange first = key_range(a, w.q, uniform(token)),
                    last = key_range(a, w.q, __builtin_amdgcn_readlane(token, u.rows - 1));
     const auto key_of = [&](int t) { return (w.tile0 + t) * kKeys; };
-    TilePages<WIDE> pages = tile_pages<WIDE>(a, b, w.q.len, key_of(u.t0), r, g);
+    Pages known = look_up<WIDE>(a, b, w.q.len, key_of(u.t0), h);
     {
         const uint16_t* src = a.q + (int64_t)(w.q.row + token) * a.q_stride + (int64_t)head * a.D;
 #pragma unroll
@@ -291,28 +312,25 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const Seq
     x.m = -__builtin_inff();
     x.l = 0.0f;
 
-    // the next tile's keys are asked for when this tile's have been read, its values likewise, and
-    // its pages' ids a tile before
+    // the next tile's keys are asked for when this tile's have been read, its values likewise
     KvTile<DP> tile;
+    TilePages pages = tile_pages<WIDE>(a, known, 0, key_of(u.t0), r, g);
     load_keys<DP, WIDE>(a, tile, pages, h, r, g);
     load_values<DP, WIDE>(a, tile, pages, h, r, g);
-    PageScales sc = page_scales(a, pages.mine().page, h);
-    bool valid = pages.mine().valid;
     for (int t = u.t0; t < u.t1; ++t) {
-        const int key0 = key_of(t);
+        const int key0 = key_of(t), next = (t + 1 - u.t0) % kLookUp<WIDE>;
         const bool more = t + 1 < u.t1;
-        pages = tile_pages<WIDE>(a, b, w.q.len, key0 + kKeys, r, g);
         const bool whole = first.lo <= key0 && last.lo <= key0 && first.hi >= key0 + kKeys &&
-                           last.hi >= key0 + kKeys && __all(valid);
-        PageScales next = sc;
+                           last.hi >= key0 + kKeys && __all(pages.valid);
+        const PageScales sc = pages.sc;
+        const bool valid = pages.valid;
         add_tile<DT, DP>(x, tile, sc, see, whole, valid, key0, g, [&] {
             if (!more) return;
+            if (next == 0) known = look_up<WIDE>(a, b, w.q.len, key0 + kKeys, h);
+            pages = tile_pages<WIDE>(a, known, next, key0 + kKeys, r, g);
             load_keys<DP, WIDE>(a, tile, pages, h, r, g);
-            next = page_scales(a, pages.mine().page, h);
         });
         if (more) load_values<DP, WIDE>(a, tile, pages, h, r, g);
-        sc = next;
-        valid = pages.mine().valid;
     }
     x.l += __shfl_xor(x.l, 16);                             // the lane groups had keys of their own
     x.l += __shfl_xor(x.l, 32);
