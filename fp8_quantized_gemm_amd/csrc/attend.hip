@@ -12,8 +12,6 @@ constexpr int kKeys = 64;                 // keys of a tile
 constexpr int groups_for(int dp) { return dp <= 128 ? 512 : 256; }
 // Waves of a workgroup: eight where it takes a whole unit and the registers allow.
 constexpr int waves_for(int dp, bool shared) { return shared || dp > 128 ? 4 : 8; }
-// Units of at most this many keys are taken whole by a workgroup, without a join.
-constexpr int kShortKeys = 1024;
 constexpr int kMinShare = 3;              // what a wave takes at least
 
 // The work is a list of units (sequence, key/value head, row tile), each a run of
@@ -505,13 +503,13 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
 
 hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t stream)
 {
-    if (attend_many_rows(a)) return launch_attend_prompt(a, dtype, stream);
+    if (attend_tiles(a)) return launch_attend_prompt(a, dtype, stream);
     return dtype == DT_BF16 ? launch<DT_BF16>(a, stream) : launch<DT_FP16>(a, stream);
 }
 
 int64_t attend_work_bytes(const AttendArgs& a)
 {
-    if (attend_many_rows(a)) return attend_prompt_work_bytes(a);
+    if (attend_tiles(a)) return attend_prompt_work_bytes(a);
     const int64_t dp = (a.D + 63) / 64 * 64;
     return groups_for((int)dp) * ((int64_t)sizeof(Unit) + 2 * kRows * (dp + 4) * 4);
 }

@@ -71,8 +71,12 @@ struct AttendArgs {
     int q_flip;                      // sign bits of two queries where the scale is negative, else 0
     int causal, window;
 };
-// The kernels for many query rows are taken from more than 16 rows a key/value head on.
-inline bool attend_many_rows(const AttendArgs& a) { return (int64_t)a.batch.max_q * a.group > 16; }
+// Sequences of at most this many keys with few query rows have a kernel of their own.
+constexpr int kShortKeys = 1024, kShortRows = 16;
+inline bool attend_tiles(const AttendArgs& a)
+{
+    return (int64_t)a.batch.max_q * a.group > kShortRows || (int64_t)a.batch.W * a.P > kShortKeys;
+}
 hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream);
 int64_t attend_prompt_work_bytes(const AttendArgs& a);
 // Bytes of scratch; looks at the sizes in `a` only.

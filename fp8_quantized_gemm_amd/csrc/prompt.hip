@@ -8,67 +8,113 @@ namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64, kWaveRows = 32, kTileRows = kWaves * kWaveRows;
 constexpr int kLeastTiles = 4;            // of a part of a unit
+// Workgroups that the chip holds at once.
+constexpr int slots_for(int dp) { return kCUs * (dp <= 128 ? 2 : 1); }
 constexpr int kRankedSeqs = 64;           // sequences that a wave ranks by length
 
-// The workgroups of a key/value head take units of kTileRows rows of one sequence; this gives the
-// `place`-th one its sequence and first row.  Places follow each other as the workgroups start: the
-// first kFirst go to a compute unit each, the next kFirst join them, the others follow where one
-// ends.  Under a causal mask a unit's time is its last position, so the longest units come first,
-// then the shortest, so that every compute unit has one of both, then the rest.
+// What a workgroup does: rows row0 .. of sequence b, the `part`-th of `parts` equal runs of the keys
+// that they see.
+struct Item {
+    int b, row0, part, parts;
+};
+
+// The workgroups of a key/value head take the units of all sequences (kTileRows rows each), in parts
+// where the units are fewer than the workgroups that fit the chip; this is the `place`-th one's item.
+//
+// Up to kRankedSeqs sequences every wave looks at all of them, one a lane.  They are ranked by their
+// lengths, the last rows of each first: under a causal mask a unit's time is its last position.
+// `cut`: a sequence's units get so many parts that each part has about the same number of key tiles,
+// the least for which the parts still fit.  Not cut: units follow each other as workgroups start, the
+// first `first` to a compute unit each, the next join them, the others follow where one ends; so the
+// longest come first, then the shortest, so that every compute unit has one of both, then the rest.
+//
+// More sequences are taken in their order; those of sequence b begin at unit q_start[b] * group /
+// kTileRows + b, and every unit has `splits` parts.
 __device__ __forceinline__ int64_t rank_of(int64_t place, int64_t count, int first)
 {
     if (place < first) return place;
     if (place < 2 * (int64_t)first) return count - 1 - (place - first);
     return place - first;
 }
-__device__ __forceinline__ bool find_unit(const AttendArgs& a, int64_t place, int splits, int64_t units, int* lds,
-                                          int& b, int& row0)
+__device__ __forceinline__ float wave_total(float v)
+{
+#define FP8Q_DPP_ADD(ctrl, rows) \
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false))
+    FP8Q_DPP_ADD(0xB1, 0xf);   // quad_perm [1,0,3,2]
+    FP8Q_DPP_ADD(0x4E, 0xf);   // quad_perm [2,3,0,1]
+    FP8Q_DPP_ADD(0x141, 0xf);  // row_half_mirror
+    FP8Q_DPP_ADD(0x140, 0xf);  // row_mirror
+    FP8Q_DPP_ADD(0x142, 0xa);  // row_bcast15 -> rows 1, 3
+    FP8Q_DPP_ADD(0x143, 0xc);  // row_bcast31 -> rows 2, 3: lane 63 holds the sum
+#undef FP8Q_DPP_ADD
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bool cut, int splits, int slots,
+                                          int64_t units, int* lds, Item& item)
 {
     const PagedBatch& s = a.batch;
-    const int first = (kCUs + a.Hk * splits - 1) / (a.Hk * splits), lane = threadIdx.x & 63;
+    const int first = (kCUs + a.Hk - 1) / a.Hk, lane = threadIdx.x & 63;
     if (s.B <= kRankedSeqs) {
-        // ranked by the sequences' lengths, the last rows of each first
         PagedSeq q{0, 0, 0, 0};
         if (lane < s.B) q = paged_seq(s, lane, a.P);
         const int tiles = (int)(((int64_t)q.n * a.group + kTileRows - 1) / kTileRows);
+        int parts = 1;
+        if (cut) {
+            // a unit's key tiles, as those of the sequence's middle token
+            const KeyRange mid = key_range(a, q, q.n / 2);
+            const int keys = (mid.hi - mid.lo) / kKeys + 1, most = slots / a.Hk;
+            int each = max((int)(wave_total((float)tiles * (float)keys) / (float)most), kLeastTiles);
+            for (int i = 0;; ++i) {
+                parts = i < 12 ? (keys + each - 1) / each : 1;
+                if (i == 12 || wave_total((float)tiles * (float)parts) <= (float)most) break;
+                each += (each + 7) >> 3;
+            }
+        }
         int before = 0, count = 0;
         for (int k = 0; k < s.B; ++k) {
-            const int t = __builtin_amdgcn_readlane(tiles, k), len = __builtin_amdgcn_readlane(q.len, k);
+            const int t = __builtin_amdgcn_readlane(tiles * parts, k), len = __builtin_amdgcn_readlane(q.len, k);
             before += len > q.len || (len == q.len && k < lane) ? t : 0;
             count += t;
         }
         if (place >= count) return false;
-        const int rank = (int)rank_of(place, count, first);
-        const uint64_t here = __ballot(rank >= before && rank < before + tiles);
-        b = (int)__builtin_ctzll(here);
-        row0 = (__builtin_amdgcn_readlane(tiles, b) - 1 - (rank - __builtin_amdgcn_readlane(before, b))) * kTileRows;
+        const int rank = cut ? (int)place : (int)rank_of(place, count, first);
+        const int b = (int)__builtin_ctzll(__ballot(rank >= before && rank < before + tiles * parts));
+        const int i = rank - __builtin_amdgcn_readlane(before, b);
+        item.b = b;
+        item.parts = __builtin_amdgcn_readlane(parts, b);
+        item.part = i % item.parts;
+        item.row0 = (__builtin_amdgcn_readlane(tiles, b) - 1 - i / item.parts) * kTileRows;
         return true;
     }
-    // in the sequences' order; those of sequence b begin at unit q_start[b] * group / kTileRows + b
-    if (place >= units) return false;
-    const int64_t u = units - 1 - rank_of(place, units, first);
+    if (place >= units * splits) return false;
+    const int64_t u = units - 1 - (cut ? place / splits : rank_of(place, units, first));
     int below = 0;
     for (int k = threadIdx.x; k < s.B; k += kThreads)
         below += (int64_t)clamp_int(s.q_start[k], 0, s.T) * a.group / kTileRows + k <= u ? 1 : 0;
-    b = uniform(max(block_sum_int<kThreads>(below, lds) - 1, 0));
-    const PagedSeq q = paged_seq(s, b, a.P);
-    const int64_t row = (u - ((int64_t)q.row * a.group / kTileRows + b)) * kTileRows;
-    row0 = (int)row;
+    item.b = uniform(max(block_sum_int<kThreads>(below, lds) - 1, 0));
+    const PagedSeq q = paged_seq(s, item.b, a.P);
+    const int64_t row = (u - ((int64_t)q.row * a.group / kTileRows + item.b)) * kTileRows;
+    item.row0 = (int)row;
+    item.parts = splits;
+    item.part = (int)(place % splits);
     return row >= 0 && row < (int64_t)q.n * a.group;
 }
 
-// The scratch where units are cut: what each is, then its parts.
-template <int DP>
-constexpr int64_t kPart = kTileRows * (DP + 4);
-template <int DP>
-__host__ __device__ __forceinline__ float* parts_of(const AttendArgs& a, int64_t units)
+// The scratch where units are cut: for each workgroup the unit that it has the first of several parts
+// of, then its part, of so many rows.
+__host__ __device__ __forceinline__ int64_t part_rows(const AttendArgs& a)
 {
-    return a.work + units * a.Hk * (int64_t)(sizeof(Unit) / 4);
+    const int64_t rows = (int64_t)a.batch.max_q * a.group;
+    return rows < kTileRows ? rows : kTileRows;
+}
+__host__ __device__ __forceinline__ float* parts_of(const AttendArgs& a, int64_t groups)
+{
+    return a.work + (groups + 1) / 2 * 2 * (int64_t)(sizeof(Unit) / 4);
 }
 
 template <int DT, int DP, bool WIDE>
 __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
-    attend_prompt_kernel(const AttendArgs a, int64_t units, int splits)
+    attend_prompt_kernel(const AttendArgs a, int64_t units, int64_t groups, int splits, int cut)
 {
     using T = Tile<DP>;
     constexpr int KB = T::kKeyBlocks / kWaves, VB = T::kValueBlocks / kWaves;
@@ -79,15 +125,14 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, hf = lane >> 5;
     const int64_t index = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int h = (int)(index % a.Hk);
-    int b, row0;
-    const int64_t place = index / a.Hk / splits;
-    const int split = (int)(index / a.Hk % splits);
-    Unit* const told = reinterpret_cast<Unit*>(a.work) + place * a.Hk + h;
-    if (place >= units) return;
-    if (!find_unit(a, place, splits, units, found, b, row0)) {
-        if (splits > 1 && split == 0 && tid == 0) told->parts = 0;
+    Unit* const told = reinterpret_cast<Unit*>(a.work) + index;
+    Item item;
+    if (index >= groups) return;
+    if (!find_item(a, index / a.Hk, cut != 0, splits, slots_for(DP), units, found, item)) {
+        if (cut && tid == 0) told->parts = 0;
         return;
     }
+    const int b = item.b, row0 = item.row0;
     const PagedSeq q = paged_seq(a.batch, b, a.P);
     const int rows = min(q.n * a.group - row0, kTileRows);
 
@@ -100,14 +145,13 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     const bool idle = wave_row0 >= row0 + rows;
     const int wave_last = min(wave_row0 + kWaveRows, row0 + rows) - 1;
     const KeyRange wfirst = key_range(a, q, wave_row0 / a.group), wlast = key_range(a, q, wave_last / a.group);
-    int t0 = first.lo / kKeys, t1 = (last.hi + kKeys - 1) / kKeys, parts = 1;
-    if (splits > 1) {
-        const int each = max((t1 - t0 + splits - 1) / splits, kLeastTiles);
-        parts = max((t1 - t0 + each - 1) / each, 1);
-        if (split == 0 && tid == 0)
-            *told = Unit{0, parts > 1 ? parts : 0, 1, 1, q.row, h, row0, rows, 0};
-        if (split >= parts) return;
-        t0 += split * each;
+    int t0 = first.lo / kKeys, t1 = (last.hi + kKeys - 1) / kKeys;
+    if (cut) {
+        // a part that gets no tile has sums of nothing, which join like others
+        const int each = (t1 - t0 + item.parts - 1) / item.parts;
+        if (tid == 0)
+            *told = Unit{0, item.part == 0 && item.parts > 1 ? item.parts : 0, 1, 1, q.row, h, row0, rows, 0};
+        t0 = min(t0 + item.part * each, t1);
         t1 = min(t0 + each, t1);
     }
 
@@ -144,40 +188,45 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 
     x.l += __shfl_xor(x.l, 32);
     if (!have_row) return;
-    float* const part = parts_of<DP>(a, units) + ((place * a.Hk + h) * splits + split) * kPart<DP> +
-                        (wave * kWaveRows + r) * (DP + 4);
-    end_rows<DT, DP>(a, x, q.row + token, head, parts > 1 ? part : nullptr, hf);
+    float* const part = parts_of(a, groups) + (index * part_rows(a) + wave * kWaveRows + r) * (DP + 4);
+    end_rows<DT, DP>(a, x, q.row + token, head, item.parts > 1 ? part : nullptr, hf);
 }
 
-// Units of all sequences at most, and into how many parts of the keys each is cut: as many as make
-// one round of the workgroups that the chip holds at once.
-struct Cut {
-    int64_t units;
+// Units of all sequences at most; workgroups; whether units are cut, and into how many parts each
+// where the kernel does not choose.
+struct Plan {
+    int64_t units, groups;
     int splits;
+    bool cut;
 };
-Cut cut_of(const AttendArgs& a)
+Plan plan_of(const AttendArgs& a)
 {
     const int64_t loose = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
     const int64_t tight = a.batch.B * (((int64_t)a.batch.max_q * a.group + kTileRows - 1) / kTileRows);
-    const int64_t units = loose < tight ? loose : tight, slots = kCUs * (a.D <= 128 ? 2 : 1);
-    const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys, most = (tiles + kLeastTiles - 1) / kLeastTiles;
-    int64_t splits = slots / (units * a.Hk);
-    splits = splits < most ? splits : most;
-    return Cut{a.batch.B <= kRankedSeqs ? units : loose, (int)(splits < 1 ? 1 : splits > kMostParts ? kMostParts : splits)};
+    const int64_t units = loose < tight ? loose : tight, slots = slots_for((int)a.D);
+    const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys;
+    const bool cut = units * a.Hk * 2 <= slots && tiles > kLeastTiles;
+    if (a.batch.B <= kRankedSeqs)
+        return cut ? Plan{units, slots / a.Hk * a.Hk, 1, true} : Plan{units, units * a.Hk, 1, false};
+    const int64_t fit = cut ? slots / (units * a.Hk) : 1, most = (tiles + kLeastTiles - 1) / kLeastTiles;
+    const int64_t splits = fit < most ? fit : most;
+    return Plan{loose, loose * a.Hk * splits, (int)splits, cut};
 }
 
 template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    const Cut cut = cut_of(a);
-    const int64_t groups = cut.units * a.Hk * cut.splits, most = max_groups(kThreads), gx = groups < most ? groups : most;
+    const Plan plan = plan_of(a);
+    const int64_t groups = plan.groups, most = max_groups(kThreads), gx = groups < most ? groups : most;
     hipLaunchKernelGGL((attend_prompt_kernel<DT, DP, WIDE>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
-                       dim3(kThreads), 0, stream, a, cut.units, cut.splits);
+                       dim3(kThreads), 0, stream, a, plan.units, groups, plan.splits, plan.cut ? 1 : 0);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || cut.splits == 1) return e;
-    const float* const parts = parts_of<DP>(a, cut.units);
-    return launch_join<DT, DP>(a, Parts{reinterpret_cast<const Unit*>(a.work), parts, parts, cut.splits * kPart<DP>, kPart<DP>},
-                               (int)(cut.units * a.Hk), kTileRows, cut.splits, stream);
+    if (e != hipSuccess || !plan.cut) return e;
+    // the parts of a unit lie a key/value head's workgroups apart
+    const float* const parts = parts_of(a, groups);
+    const int64_t stride = part_rows(a) * (DP + 4);
+    return launch_join<DT, DP>(a, Parts{reinterpret_cast<const Unit*>(a.work), parts, parts, stride, a.Hk * stride},
+                               (int)groups, (int)part_rows(a), (int)(groups / (plan.units * a.Hk)), stream);
 }
 
 template <int DT, int DP>
@@ -199,10 +248,10 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
 
 int64_t attend_prompt_work_bytes(const AttendArgs& a)
 {
-    const Cut cut = cut_of(a);
-    if (cut.splits == 1) return 16;
+    const Plan plan = plan_of(a);
+    if (!plan.cut) return 16;
     const int64_t dp = (a.D + 63) / 64 * 64;
-    return cut.units * a.Hk * ((int64_t)sizeof(Unit) + cut.splits * kTileRows * (dp + 4) * 4);
+    return (plan.groups + 1) / 2 * 2 * (int64_t)sizeof(Unit) + plan.groups * part_rows(a) * (dp + 4) * 4;
 }
 
 hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream)
