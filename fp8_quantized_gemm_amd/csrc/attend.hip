@@ -1,107 +1,13 @@
 // Attention over the paged FP8 cache for few query rows (see paged.hpp).
-#include "join.hpp"
+#include "attend.hpp"
 
 namespace fp8q {
 namespace {
 
-constexpr int kWaves = 4, kThreads = kWaves * 64;
-constexpr int kPolicy = CP_DEFAULT;
-constexpr int kRows = 16;                 // query rows of a unit: (token, head of the group) pairs
+constexpr int kRows = kShortRows;         // query rows of a workgroup: (token, head of the group) pairs
 constexpr int kKeys = 64;                 // keys of a tile
-// Two workgroups on each of 256 CUs, one from 192 channels on (registers).
-constexpr int groups_for(int dp) { return dp <= 128 ? 512 : 256; }
-// Waves of a workgroup: eight where it takes a whole unit and the registers allow.
-constexpr int waves_for(int dp, bool shared) { return shared || dp > 128 ? 4 : 8; }
-constexpr int kMinShare = 3;              // what a wave takes at least
-
-// The work is a list of units (sequence, key/value head, row tile), each a run of
-// key tiles with one place before them for what a unit costs by itself; wave i
-// of the grid takes the places [i * share, (i + 1) * share) of the whole list.
-// That evens out any mixture of lengths, and is computed from the batch's arrays
-// by every workgroup, so the host needs no lengths and a graph can be replayed
-// with others.  A wave stores the units that it has whole; the pieces of the
-// others are joined in LDS, and those of units that several workgroups have by
-// attend_join_kernel.
-struct SeqWork {
-    PagedSeq q;
-    int tile0, tiles;                     // key tiles that some row of the sequence sees
-    int row_tiles;
-    __device__ __forceinline__ int64_t places(int Hk) const { return (int64_t)row_tiles * Hk * (tiles + 1); }
-};
-
-__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int b)
-{
-    SeqWork w;
-    w.q = paged_seq(a.batch, b, a.P);
-    const KeyRange first = key_range(a, w.q, 0), last = key_range(a, w.q, w.q.n - 1);
-    w.tile0 = first.lo / kKeys;
-    w.tiles = max((last.hi + kKeys - 1) / kKeys - w.tile0, 1);
-    w.row_tiles = (w.q.n * a.group + kRows - 1) / kRows;
-    return w;
-}
-
-struct ScanLds {
-    int64_t sums[kWaves];
-    int64_t before[kWaves];
-    int seq[kWaves];
-};
-
-__device__ __forceinline__ int64_t share_of(int64_t total, int waves)
-{
-    const int64_t s = (total + waves - 1) / waves;
-    return s > kMinShare ? s : kMinShare;
-}
-
-// Places of all sequences, and for the first place of each of the workgroup's waves the
-// sequence that holds it and the places before that sequence.  Every thread sums a run of
-// sequences.
-__device__ __forceinline__ int64_t scan_sequences(const AttendArgs& a, ScanLds& lds)
-{
-    const int B = a.batch.B, per = (B + kThreads - 1) / kThreads, lane = threadIdx.x & 63;
-    const int b0 = min((int)threadIdx.x * per, B), b1 = min(b0 + per, B);
-    int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_work(a, b).places(a.Hk);
-    int64_t sum = mine;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int64_t up = __shfl_up(sum, off);
-        if (lane >= off) sum += up;
-    }
-    if (lane == 63) lds.sums[threadIdx.x >> 6] = sum;
-    __syncthreads();
-    int64_t total = 0, before = sum - mine;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w < (int)(threadIdx.x >> 6)) before += lds.sums[w];
-        total += lds.sums[w];
-    }
-    const int64_t share = share_of(total, gridDim.x * kWaves);
-    for (int w = 0; w < kWaves; ++w) {
-        const int64_t at = ((int64_t)blockIdx.x * kWaves + w) * share;
-        if (at < before || at >= before + mine) continue;
-        int64_t from = before;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t n = seq_work(a, b).places(a.Hk);
-            if (at < from + n) {
-                lds.seq[w] = b;
-                lds.before[w] = from;
-                break;
-            }
-            from += n;
-        }
-    }
-    __syncthreads();
-    return total;
-}
-
-// The scratch: for each workgroup the unit that it begins and another one ends (parts = 0:
-// none), then its two partial results, of a unit that it goes on with and of one that it
-// begins: kRows rows of maximum, denominator and, from the fifth float on, DP sums.
-template <int DP>
-__host__ __device__ __forceinline__ float* part_of(float* work, int groups, int64_t group, bool begins)
-{
-    return work + groups * (int)(sizeof(Unit) / 4) + (group * 2 + (begins ? 1 : 0)) * (kRows * (DP + 4));
-}
+// Waves of a workgroup: eight where the registers allow.
+constexpr int waves_for(int dp) { return dp <= 128 ? 8 : 4; }
 
 // A key tile as a wave holds it: lane (r, g) has 16 channels for each 64 of the keys
 // 16 (r / 4) + 4 i + r % 4, i < 4, and the 16 keys from 16 g on of the channels 16 d + r.
@@ -170,7 +76,7 @@ __device__ __forceinline__ void load_keys(const AttendArgs& a, KvTile<DP>& t, co
                 const int d = 64 * c + 16 * g;
                 const uint32_t at = (uint32_t)((16 * (r >> 2) + (r & 3)) * a.D + d);
                 t.k[i][c] = __builtin_amdgcn_raw_buffer_load_b128(rk, d < a.D ? at : kOOB, uniform(4 * i * a.D),
-                                                                  kPolicy);
+                                                                  CP_DEFAULT);
             }
     } else {
         const uint8_t* kt = a.k_pages + p.k * pool_stride + h * page_bytes +
@@ -198,7 +104,7 @@ __device__ __forceinline__ void load_values(const AttendArgs& a, KvTile<DP>& t, 
 #pragma unroll
         for (int d = 0; d < ND; ++d)
             t.v[d] = __builtin_amdgcn_raw_buffer_load_b128(rv, (uint32_t)(r * a.P + 16 * g),
-                                                           uniform(16 * d * a.P), kPolicy);
+                                                           uniform(16 * d * a.P), CP_DEFAULT);
     } else {
         const uint8_t* vt = a.v_pages + p.v * pool_stride + h * page_bytes + p.v_inside;
 #pragma unroll
@@ -274,28 +180,22 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, KvTile<DP>& t, const PageS
     }
 }
 
-// A run of tiles [t0, t1) of a unit (key/value head h, rows from row0 on) by one wave.
+// Key/value head h of sequence b; its workgroup has the tiles from tile0 on, this wave `t0` .. of them.
 struct Run {
-    int h, row0, rows, t0, t1;
+    PagedSeq q;
+    int b, h, rows, tile0, t0, t1;
 };
 template <int DT, int DP, bool WIDE>
-__device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const SeqWork& w, const Run& u, Rows<DP>& x,
-                                           int& token, int& head)
+__device__ __forceinline__ void attend_run(const AttendArgs& a, const Run& u, Rows<DP>& x)
 {
     constexpr int NC = DP / 64, ND = DP / 16;
-    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, h = u.h;
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4, h = u.h, b = u.b;
     // this lane's query row and the keys it sees
-    const int my_row = u.row0 + r;
-    token = my_row / a.group;
-    head = h * a.group + (my_row - token * a.group);
-    KeyRange see = key_range(a, w.q, token);
-    if (r >= u.rows) see.lo = see.hi = 0;
-    const KeyRange first = key_range(a, w.q, uniform(token)),
-                   last = key_range(a, w.q, __builtin_amdgcn_readlane(token, u.rows - 1));
-    const auto key_of = [&](int t) { return (w.tile0 + t) * kKeys; };
-    Pages known = look_up<WIDE>(a, b, w.q.len, key_of(u.t0), h);
+    const int token = r / a.group, head = h * a.group + r % a.group;
+    const auto key_of = [&](int t) { return (u.tile0 + t) * kKeys; };
+    Pages known = look_up<WIDE>(a, b, u.q.len, key_of(u.t0), h);
     {
-        const uint16_t* src = a.q + (int64_t)(w.q.row + token) * a.q_stride + (int64_t)head * a.D;
+        const uint16_t* src = a.q + (int64_t)(u.q.row + token) * a.q_stride + (int64_t)head * a.D;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = 64 * c + 16 * g;
@@ -305,6 +205,10 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const Seq
             x.q[c][1] = have ? *reinterpret_cast<const v4i*>(src + d + 8) ^ a.q_flip : zero;
         }
     }
+    KeyRange see = key_range(a, u.q, token);
+    if (r >= u.rows) see.lo = see.hi = 0;
+    const KeyRange first = key_range(a, u.q, 0),
+                   last = key_range(a, u.q, __builtin_amdgcn_readlane(token, u.rows - 1));
 #pragma unroll
     for (int d = 0; d < ND; ++d) x.acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
     x.m = -__builtin_inff();
@@ -324,7 +228,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const Seq
         const bool valid = pages.valid;
         add_tile<DT, DP>(x, tile, sc, see, whole, valid, key0, g, [&] {
             if (!more) return;
-            if (next == 0) known = look_up<WIDE>(a, b, w.q.len, key0 + kKeys, h);
+            if (next == 0) known = look_up<WIDE>(a, b, u.q.len, key0 + kKeys, h);
             pages = tile_pages<WIDE>(a, known, next, key0 + kKeys, r, g);
             load_keys<DP, WIDE>(a, tile, pages, h, r, g);
         });
@@ -334,154 +238,60 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, int b, const Seq
     x.l += __shfl_xor(x.l, 32);
 }
 
-// SHARED: the grid's waves share the list of all units' tiles.  Else a workgroup takes one unit,
-// its waves equal runs of the tiles.
-template <int DT, int DP, bool WIDE, bool SHARED>
-__global__ void __launch_bounds__(waves_for(DP, SHARED) * 64, DP <= 128 ? 2 : 1)
-    attend_rows_kernel(const AttendArgs a)
+// A workgroup has all rows of a key/value head of a sequence, its waves equal runs of the key tiles;
+// the waves' sums are joined in LDS.
+template <int DT, int DP, bool WIDE>
+__global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_short_kernel(const AttendArgs a)
 {
-    constexpr int kWaves = waves_for(DP, SHARED), kThreads = kWaves * 64, kPieces = SHARED ? 2 * kWaves : kWaves;
-    constexpr int ND = DP / 16;
+    constexpr int kWaves = waves_for(DP), kThreads = kWaves * 64, ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
-    __shared__ Unit piece[kPieces];
-    __shared__ float stat[kPieces][kRows][2];
-    __shared__ __attribute__((aligned(16))) float sums[kPieces][kRows * RS];
+    __shared__ float stat[kWaves][kRows][2];
+    __shared__ __attribute__((aligned(16))) float sums[kWaves][kRows * RS];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
-    const auto keep = [&](const SeqWork& w, const Run& u, const Rows<DP>& x, int slot, int64_t unit_at, int parts) {
-        if (g == 0) { stat[slot][r][0] = x.m; stat[slot][r][1] = x.l; }
+    Run u;
+    u.b = blockIdx.x;
+    u.h = blockIdx.y;
+    u.q = paged_seq(a.batch, u.b, a.P);
+    u.rows = u.q.n * a.group;
+    if (u.rows == 0) return;
+    const int lo = key_range(a, u.q, 0).lo, hi = key_range(a, u.q, u.q.n - 1).hi;
+    u.tile0 = lo / kKeys;
+    const int tiles = max((hi + kKeys - 1) / kKeys - u.tile0, 1), each = (tiles + kWaves - 1) / kWaves;
+    const int used = (tiles + each - 1) / each;             // waves that have tiles
+    u.t0 = wave * each;
+    u.t1 = min(u.t0 + each, tiles);
+    if (wave < used) {
+        Rows<DP> x;
+        attend_run<DT, DP, WIDE>(a, u, x);
+        if (g == 0) { stat[wave][r][0] = x.m; stat[wave][r][1] = x.l; }
 #pragma unroll
-        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[slot][r * RS + 16 * d + 4 * g]) = x.acc[d];
-        if (lane == 0)
-            piece[slot] = Unit{unit_at, parts, u.t0 == 0, u.t1 == w.tiles, w.q.row, u.h, u.row0, u.rows, 0};
-    };
-    const auto store = [&](const SeqWork& w, const Run& u, const Rows<DP>& x, int token, int head) {
-        const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
-        if (r < u.rows)
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-                if (16 * d < a.D) store_row<DT>(a, w.q.row + token, head, 16 * d + 4 * g, x.acc[d], j);
-    };
-    Rows<DP> x;
-    int token, head;
-    if constexpr (SHARED) {
-        __shared__ ScanLds scan;
-        const int64_t total = uniform(scan_sequences(a, scan)), share = share_of(total, gridDim.x * kWaves);
-        int64_t at = ((int64_t)blockIdx.x * kWaves + wave) * share, seq_at = 0;
-        const int64_t end = at + share < total ? at + share : total;
-        int b = 0;
-        if (at < end) {
-            b = uniform(scan.seq[wave]);
-            seq_at = uniform(scan.before[wave]);
-        }
-        if (lane < 2) piece[2 * wave + lane].rows = 0;
-        while (at < end) {
-            const SeqWork w = seq_work(a, b);
-            const int64_t seq_places = w.places(a.Hk);
-            if (at >= seq_at + seq_places) { seq_at += seq_places; ++b; continue; }
-            const int unit = (int)((at - seq_at) / (w.tiles + 1));
-            const int64_t unit_at = seq_at + (int64_t)unit * (w.tiles + 1);
-            Run u;
-            u.t0 = max((int)(at - unit_at) - 1, 0);
-            u.t1 = (int)(end - unit_at - 1 < w.tiles ? end - unit_at - 1 : w.tiles);
-            at = unit_at + w.tiles + 1;
-            if (u.t0 >= u.t1) continue;                     // only the place before the tiles
-            u.h = unit / w.row_tiles;
-            u.row0 = (unit - u.h * w.row_tiles) * kRows;
-            u.rows = min(kRows, w.q.n * a.group - u.row0);
-            attend_run<DT, DP, WIDE>(a, b, w, u, x, token, head);
-            if (u.t0 == 0 && u.t1 == w.tiles) store(w, u, x, token, head);
-            else
-                keep(w, u, x, 2 * wave + (u.t0 == 0 ? 1 : 0), unit_at,
-                     1 + (int)((unit_at + w.tiles) / share / kWaves - (unit_at + 1) / share / kWaves));
-        }
-    } else {
-        const int b = blockIdx.x, unit = blockIdx.y;
-        const SeqWork w = seq_work(a, b);
-        if (unit >= w.row_tiles * a.Hk) return;
-        const int each = (w.tiles + kWaves - 1) / kWaves;
-        Run u;
-        u.t0 = wave * each;
-        u.t1 = min(u.t0 + each, w.tiles);
-        u.h = unit % a.Hk;
-        u.row0 = unit / a.Hk * kRows;
-        u.rows = min(kRows, w.q.n * a.group - u.row0);
-        if (u.t0 >= u.t1) {
-            if (lane == 0) piece[wave].rows = 0;
-        } else {
-            attend_run<DT, DP, WIDE>(a, b, w, u, x, token, head);
-            if (w.tiles == 1) { store(w, u, x, token, head); return; }
-            keep(w, u, x, wave, 0, 1);
-        }
-        if (w.tiles == 1) return;
+        for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[wave][r * RS + 16 * d + 4 * g]) = x.acc[d];
     }
-
-    // pieces of one unit lie next to each other, in order
     __syncthreads();
-    bool told = false;
-    for (int p0 = 0; p0 < kPieces;) {
-        const Unit u = piece[p0];
-        int p1 = p0 + 1;
-        if (u.rows == 0) { p0 = p1; continue; }
-        int ends = u.ends;
-        for (int p = p1; p < kPieces; ++p) {
-            if (piece[p].rows == 0) continue;
-            if (piece[p].at != u.at) break;
-            ends = piece[p].ends;
-            p1 = p + 1;
+
+    const int quads = a.D / 4;
+    for (int i = threadIdx.x; i < u.rows * quads; i += kThreads) {
+        const int row = i / quads, d = i % quads * 4;
+        Joined j{-__builtin_inff(), 0.0f, 0.0f};
+        for (int p = 0; p < used; ++p) j.m = fmaxf(j.m, stat[p][row][0]);
+        j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
+        v4f o = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < used; ++p) {
+            const float f = __builtin_amdgcn_exp2f(stat[p][row][0] - j.ref);
+            j.l += stat[p][row][1] * f;
+            o += *reinterpret_cast<const v4f*>(&sums[p][row * RS + d]) * f;
         }
-        const bool all = !SHARED || (u.begins && ends);
-        float* out = SHARED ? part_of<DP>(a.work, gridDim.x, blockIdx.x, u.begins) : nullptr;
-        if (SHARED && u.begins && !ends) {
-            told = true;
-            if (threadIdx.x == 0) reinterpret_cast<Unit*>(a.work)[blockIdx.x] = u;
-        }
-        const int quads = a.D / 4;
-        for (int i = threadIdx.x; i < u.rows * quads; i += kThreads) {
-            const int row = i / quads, d = i % quads * 4;
-            Joined j{-__builtin_inff(), 0.0f, 0.0f};
-            for (int p = p0; p < p1; ++p)
-                if (piece[p].rows != 0) j.m = fmaxf(j.m, stat[p][row][0]);
-            j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
-            v4f o = {0.f, 0.f, 0.f, 0.f};
-            for (int p = p0; p < p1; ++p)
-                if (piece[p].rows != 0) {
-                    const float f = __builtin_amdgcn_exp2f(stat[p][row][0] - j.ref);
-                    j.l += stat[p][row][1] * f;
-                    o += *reinterpret_cast<const v4f*>(&sums[p][row * RS + d]) * f;
-                }
-            if (all) {
-                const int gr = u.row0 + row;
-                store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, j);
-            } else {
-                *reinterpret_cast<v4f*>(out + row * RS + 4 + d) = o;
-                if (d == 0) { out[row * RS] = j.m; out[row * RS + 1] = j.l; }
-            }
-        }
-        p0 = p1;
+        store_row<DT>(a, u.q.row + row / a.group, u.h * a.group + row % a.group, d, o, j);
     }
-    if (SHARED && threadIdx.x == 0 && !told) reinterpret_cast<Unit*>(a.work)[blockIdx.x].parts = 0;
 }
 
 template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    const int64_t rows = (int64_t)a.batch.max_q * a.group;
-    if ((int64_t)a.batch.W * a.P <= kShortKeys) {
-        const dim3 grid((unsigned)a.batch.B, (unsigned)((rows + kRows - 1) / kRows * a.Hk));
-        hipLaunchKernelGGL((attend_rows_kernel<DT, DP, WIDE, false>), grid, dim3(waves_for(DP, false) * 64), 0,
-                           stream, a);
-        return hipGetLastError();
-    }
-    hipLaunchKernelGGL((attend_rows_kernel<DT, DP, WIDE, true>), dim3(groups_for(DP)), dim3(kThreads), 0, stream, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    constexpr int groups = groups_for(DP);
-    const Parts parts{reinterpret_cast<const Unit*>(a.work), part_of<DP>(a.work, groups, 0, true),
-                      part_of<DP>(a.work, groups, 0, false), 2 * kRows * (DP + 4), 2 * kRows * (DP + 4)};
-    // the parts that a unit has, about
-    const int64_t units = a.batch.B * a.Hk * ((rows + kRows - 1) / kRows);
-    return launch_join<DT, DP>(a, parts, groups, (int)(rows < kRows ? rows : kRows), (int)(groups / units), stream);
+    hipLaunchKernelGGL((attend_short_kernel<DT, DP, WIDE>), dim3((unsigned)a.batch.B, (unsigned)a.Hk),
+                       dim3(waves_for(DP) * 64), 0, stream, a);
+    return hipGetLastError();
 }
 
 template <int DT, int DP>
@@ -507,11 +317,6 @@ hipError_t launch_paged_attention(const AttendArgs& a, int dtype, hipStream_t st
     return dtype == DT_BF16 ? launch<DT_BF16>(a, stream) : launch<DT_FP16>(a, stream);
 }
 
-int64_t attend_work_bytes(const AttendArgs& a)
-{
-    if (attend_tiles(a)) return attend_prompt_work_bytes(a);
-    const int64_t dp = (a.D + 63) / 64 * 64;
-    return groups_for((int)dp) * ((int64_t)sizeof(Unit) + 2 * kRows * (dp + 4) * 4);
-}
+int64_t attend_work_bytes(const AttendArgs& a) { return attend_tiles(a) ? attend_prompt_work_bytes(a) : 16; }
 
 }  // namespace fp8q

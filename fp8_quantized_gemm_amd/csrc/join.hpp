@@ -5,20 +5,14 @@
 
 namespace fp8q {
 
-// A unit (rows of one key/value head of a sequence) that `parts` workgroups have parts of; 0: none.
+// A unit: rows row0 .. of a key/value head of a sequence (its first token's row: token0), which
+// `parts` workgroups have parts of, the first of them workgroup `group`; parts = 0: none.
 struct Unit {
-    int64_t at;                           // tells units apart
-    int parts, begins, ends, token0, head, row0, rows, unused;
+    int group, parts, token0, head, row0, rows, unused[2];
 };
 
-// Where the partial results lie, in floats: part k of unit i at first + i * stride for k = 0, else at
-// other + i * stride + k * step.  A part's rows are DP + 4 floats apart: maximum, denominator, two
-// unused, sums.
-struct Parts {
-    const Unit* units;
-    const float *first, *other;
-    int64_t stride, step;
-};
+// The parts of a unit are those of every Hk-th workgroup from its first on.  A part's rows are DP + 4
+// floats apart: maximum, denominator, two unused, sums.
 constexpr int kMostParts = 512;
 constexpr int kJoinThreads = 256;
 
@@ -27,17 +21,19 @@ namespace {
 // A workgroup joins R rows of a unit.  A row's threads have four channels each and take turns at
 // the parts; the parts' maxima come first, so that no load waits for another.
 template <int DT, int DP, int R>
-__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, const Parts parts)
+__global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendArgs a, const float* parts,
+                                                                    int part_rows)
 {
     constexpr int kEach = kJoinThreads / R, kLanes = kEach < 64 ? kEach : 64, kWaves = kJoinThreads / 64;
     __shared__ float factor[R][kMostParts], red[2][kWaves];
     __shared__ __attribute__((aligned(16))) float sums[kJoinThreads * 4];
-    const Unit u = parts.units[blockIdx.x];
+    const Unit u = reinterpret_cast<const Unit*>(a.work)[blockIdx.x];
     const int mine = threadIdx.x / kEach, tid = threadIdx.x % kEach, row = blockIdx.y * R + mine;
     if (u.parts == 0 || (int)(blockIdx.y * R) >= u.rows) return;
     const int count = row < u.rows ? u.parts : 0;
-    const int64_t at = blockIdx.x * parts.stride + (int64_t)row * (DP + 4);
-    const auto part = [&](int k) { return k == 0 ? parts.first + at : parts.other + at + k * parts.step; };
+    const auto part = [&](int k) {
+        return parts + (((int64_t)u.group + (int64_t)k * a.Hk) * part_rows + row) * (DP + 4);
+    };
     float m = -__builtin_inff(), l = 0.0f;
     for (int k = tid; k < count; k += kEach) {
         factor[mine][k] = part(k)[0];
@@ -79,16 +75,18 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, Joined{m, ref, l});
 }
 
-// `about`: the parts that a unit has, for the choice between a workgroup a row and one for several.
 template <int DT, int DP>
-hipError_t launch_join(const AttendArgs& a, const Parts& parts, int units, int rows, int about, hipStream_t stream)
+hipError_t launch_join(const AttendArgs& a, const float* parts, int64_t units, int part_rows, hipStream_t stream)
 {
+    // a workgroup a row where there are few, several rows where they fill the chip by far
     constexpr int kSeveral = DP <= 128 ? 8 : 4;
-    if (about >= 8) {
-        hipLaunchKernelGGL((attend_join_kernel<DT, DP, 1>), dim3(units, rows), dim3(kJoinThreads), 0, stream, a, parts);
+    const unsigned groups = (unsigned)(units * a.Hk);
+    if ((int64_t)groups * part_rows <= 2048) {
+        hipLaunchKernelGGL((attend_join_kernel<DT, DP, 1>), dim3(groups, part_rows), dim3(kJoinThreads), 0, stream, a,
+                           parts, part_rows);
     } else {
-        hipLaunchKernelGGL((attend_join_kernel<DT, DP, kSeveral>), dim3(units, (rows + kSeveral - 1) / kSeveral),
-                           dim3(kJoinThreads), 0, stream, a, parts);
+        hipLaunchKernelGGL((attend_join_kernel<DT, DP, kSeveral>), dim3(groups, (part_rows + kSeveral - 1) / kSeveral),
+                           dim3(kJoinThreads), 0, stream, a, parts, part_rows);
     }
     return hipGetLastError();
 }

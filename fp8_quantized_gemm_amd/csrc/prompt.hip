@@ -16,6 +16,7 @@ constexpr int kRankedSeqs = 64;           // sequences that a wave ranks by leng
 // that they see.
 struct Item {
     int b, row0, part, parts;
+    int64_t unit, units;                  // of the key/value head: this one, and how many there are
 };
 
 // The workgroups of a key/value head take the units of all sequences (kTileRows rows each), in parts
@@ -63,18 +64,25 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
             // a unit's key tiles, as those of the sequence's middle token
             const KeyRange mid = key_range(a, q, q.n / 2);
             const int keys = (mid.hi - mid.lo) / kKeys + 1, most = slots / a.Hk;
-            int each = max((int)(wave_total((float)tiles * (float)keys) / (float)most), kLeastTiles);
-            for (int i = 0;; ++i) {
-                parts = i < 12 ? (keys + each - 1) / each : 1;
-                if (i == 12 || wave_total((float)tiles * (float)parts) <= (float)most) break;
-                each += (each + 7) >> 3;
+            int each = max((int)ceilf(wave_total((float)tiles * (float)keys) / (float)most), kLeastTiles);
+            // twice the even share is always enough, as the units are half of what fits at most
+            for (int i = 0; i < 12; ++i) {
+                parts = (keys + each - 1) / each;
+                if (wave_total((float)tiles * (float)parts) <= (float)most) break;
+                each += (each + 15) >> 4;
+                parts = 1;
             }
         }
-        int before = 0, count = 0;
+        int before = 0, count = 0, units_before = 0;
+        item.units = 0;
         for (int k = 0; k < s.B; ++k) {
-            const int t = __builtin_amdgcn_readlane(tiles * parts, k), len = __builtin_amdgcn_readlane(q.len, k);
-            before += len > q.len || (len == q.len && k < lane) ? t : 0;
-            count += t;
+            const int t = __builtin_amdgcn_readlane(tiles, k), p = t * __builtin_amdgcn_readlane(parts, k);
+            const int len = __builtin_amdgcn_readlane(q.len, k);
+            const bool ahead = len > q.len || (len == q.len && k < lane);
+            before += ahead ? p : 0;
+            units_before += ahead ? t : 0;
+            count += p;
+            item.units += t;
         }
         if (place >= count) return false;
         const int rank = cut ? (int)place : (int)rank_of(place, count, first);
@@ -83,11 +91,14 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
         item.b = b;
         item.parts = __builtin_amdgcn_readlane(parts, b);
         item.part = i % item.parts;
-        item.row0 = (__builtin_amdgcn_readlane(tiles, b) - 1 - i / item.parts) * kTileRows;
+        const int u = i / item.parts;
+        item.unit = __builtin_amdgcn_readlane(units_before, b) + u;
+        item.row0 = (__builtin_amdgcn_readlane(tiles, b) - 1 - u) * kTileRows;
         return true;
     }
-    if (place >= units * splits) return false;
-    const int64_t u = units - 1 - (cut ? place / splits : rank_of(place, units, first));
+    item.units = 0;                       // every unit that is not there is told by its first part
+    item.unit = place / splits;
+    const int64_t u = units - 1 - (cut ? item.unit : rank_of(place, units, first));
     int below = 0;
     for (int k = threadIdx.x; k < s.B; k += kThreads)
         below += (int64_t)clamp_int(s.q_start[k], 0, s.T) * a.group / kTileRows + k <= u ? 1 : 0;
@@ -100,16 +111,17 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
     return row >= 0 && row < (int64_t)q.n * a.group;
 }
 
-// The scratch where units are cut: for each workgroup the unit that it has the first of several parts
-// of, then its part, of so many rows.
+// The scratch where units are cut: what each unit of each key/value head is, then a part for each
+// workgroup, of so many rows.
 __host__ __device__ __forceinline__ int64_t part_rows(const AttendArgs& a)
 {
     const int64_t rows = (int64_t)a.batch.max_q * a.group;
     return rows < kTileRows ? rows : kTileRows;
 }
-__host__ __device__ __forceinline__ float* parts_of(const AttendArgs& a, int64_t groups)
+__host__ __device__ __forceinline__ float* parts_of(const AttendArgs& a, int64_t units)
 {
-    return a.work + (groups + 1) / 2 * 2 * (int64_t)(sizeof(Unit) / 4);
+    static_assert(sizeof(Unit) % 16 == 0, "parts are read 16 bytes at a time");
+    return a.work + units * a.Hk * (int64_t)(sizeof(Unit) / 4);
 }
 
 template <int DT, int DP, bool WIDE>
@@ -125,13 +137,17 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), r = lane & 31, hf = lane >> 5;
     const int64_t index = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
     const int h = (int)(index % a.Hk);
-    Unit* const told = reinterpret_cast<Unit*>(a.work) + index;
     Item item;
     if (index >= groups) return;
-    if (!find_item(a, index / a.Hk, cut != 0, splits, slots_for(DP), units, found, item)) {
-        if (cut && tid == 0) told->parts = 0;
-        return;
+    const int64_t place = index / a.Hk;
+    const bool have = find_item(a, place, cut != 0, splits, slots_for(DP), units, found, item);
+    Unit* const told = reinterpret_cast<Unit*>(a.work);
+    if (cut && tid == 0) {
+        // units that the batch might have had, but has not
+        if (a.batch.B <= kRankedSeqs ? place >= item.units && place < units : !have && item.part == 0)
+            told[(a.batch.B <= kRankedSeqs ? place : item.unit) * a.Hk + h].parts = 0;
     }
+    if (!have) return;
     const int b = item.b, row0 = item.row0;
     const PagedSeq q = paged_seq(a.batch, b, a.P);
     const int rows = min(q.n * a.group - row0, kTileRows);
@@ -149,8 +165,9 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
     if (cut) {
         // a part that gets no tile has sums of nothing, which join like others
         const int each = (t1 - t0 + item.parts - 1) / item.parts;
-        if (tid == 0)
-            *told = Unit{0, item.part == 0 && item.parts > 1 ? item.parts : 0, 1, 1, q.row, h, row0, rows, 0};
+        if (tid == 0 && item.part == 0 && item.unit < units)
+            told[item.unit * a.Hk + h] =
+                Unit{(int)index, item.parts > 1 ? item.parts : 0, q.row, h, row0, rows, {0, 0}};
         t0 = min(t0 + item.part * each, t1);
         t1 = min(t0 + each, t1);
     }
@@ -188,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
 
     x.l += __shfl_xor(x.l, 32);
     if (!have_row) return;
-    float* const part = parts_of(a, groups) + (index * part_rows(a) + wave * kWaveRows + r) * (DP + 4);
+    float* const part = parts_of(a, units) + (index * part_rows(a) + wave * kWaveRows + r) * (DP + 4);
     end_rows<DT, DP>(a, x, q.row + token, head, item.parts > 1 ? part : nullptr, hf);
 }
 
@@ -222,11 +239,7 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
                        dim3(kThreads), 0, stream, a, plan.units, groups, plan.splits, plan.cut ? 1 : 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !plan.cut) return e;
-    // the parts of a unit lie a key/value head's workgroups apart
-    const float* const parts = parts_of(a, groups);
-    const int64_t stride = part_rows(a) * (DP + 4);
-    return launch_join<DT, DP>(a, Parts{reinterpret_cast<const Unit*>(a.work), parts, parts, stride, a.Hk * stride},
-                               (int)groups, (int)part_rows(a), (int)(groups / (plan.units * a.Hk)), stream);
+    return launch_join<DT, DP>(a, parts_of(a, plan.units), plan.units, (int)part_rows(a), stream);
 }
 
 template <int DT, int DP>
@@ -251,7 +264,7 @@ int64_t attend_prompt_work_bytes(const AttendArgs& a)
     const Plan plan = plan_of(a);
     if (!plan.cut) return 16;
     const int64_t dp = (a.D + 63) / 64 * 64;
-    return (plan.groups + 1) / 2 * 2 * (int64_t)sizeof(Unit) + plan.groups * part_rows(a) * (dp + 4) * 4;
+    return plan.units * a.Hk * (int64_t)sizeof(Unit) + plan.groups * part_rows(a) * (dp + 4) * 4;
 }
 
 hipError_t launch_attend_prompt(const AttendArgs& a, int dtype, hipStream_t stream)
