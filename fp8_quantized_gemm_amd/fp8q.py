@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -26,16 +27,12 @@ lib = ctypes.CDLL(LIB_PATH)
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i = ctypes.c_int
+_s = ctypes.c_char_p
 
-class _KvCache(ctypes.Structure):
-    _fields_ = [("k", _p), ("v", _p), ("k_scale", _p), ("v_scale", _p), ("pages", _i64),
-                ("kv_heads", _i64), ("page_size", _i64), ("head_dim", _i64)]
-
-
-class _KvBatch(ctypes.Structure):
-    _fields_ = [("page_table", _p), ("q_start", _p), ("kv_lens", _p), ("tokens", _i64),
-                ("seqs", _i64), ("table_width", _i64), ("max_q", _i64)]
-
+# fp8q_kv_cache (k, v, k_scale, v_scale, pages, kv_heads, page_size, head_dim) and fp8q_kv_batch
+# (page_table, q_start, kv_lens, tokens, seqs, table_width, max_q) as bytes
+_kv_cache_bytes = struct.Struct("=4Q4q").pack
+_kv_batch_bytes = struct.Struct("=3Q4q").pack
 
 _SIGS = {
     "fp8q_abi_version": (_i, []),
@@ -70,10 +67,9 @@ _SIGS = {
     "fp8_moe_blockwise_work_bytes": (_i64, [_i64, _i64, _i64]),
     "fp8_moe_blockwise": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64,
                                _i64, _i, _p]),
-    "fp8_kv_append": (_i, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _p, _i64, _p, _i64,
-                           _i, _p, _i64, _i64, _i, _p, _i64, _p, _i64, _i64, _p]),
-    "fp8_paged_attention_work_bytes": (_i64, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _i64]),
-    "fp8_paged_attention": (_i, [ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch), _p, _i64, _i,
+    "fp8_kv_append": (_i, [_s, _s, _p, _i64, _p, _i64, _i, _p, _i64, _i64, _i, _p, _i64, _p, _i64, _i64, _p]),
+    "fp8_paged_attention_work_bytes": (_i64, [_s, _s, _i64]),
+    "fp8_paged_attention": (_i, [_s, _s, _p, _i64, _i,
                                  _i64, ctypes.c_float, _i, _i64, _p, _p, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -470,41 +466,45 @@ def moe_work_bytes(tokens: int, inter: int, top_k: int) -> int:
     return int(lib.fp8_moe_blockwise_work_bytes(tokens, inter, top_k))
 
 
-def _kv_cache(k_pages, v_pages, k_scale, v_scale, index: int) -> _KvCache:
+def _kv_cache(k_pages, v_pages, k_scale, v_scale, index: int):
+    """fp8q_kv_cache of the cache's tensors, and its number of heads and head_dim."""
     if k_pages.dim() != 4:
         raise ValueError(f"k_pages must be [pages, kv_heads, page_size, head_dim], got "
                          f"{tuple(k_pages.shape)}")
-    pages, heads, size, dim = k_pages.shape
-    return _KvCache(_ptr(k_pages, "k_pages", torch.uint8, (pages, heads, size, dim), index),
-                    _ptr(v_pages, "v_pages", torch.uint8, (pages, heads, dim, size), index),
-                    _ptr(k_scale, "k_scale", torch.float32, (pages, heads), index),
-                    _ptr(v_scale, "v_scale", torch.float32, (pages, heads), index),
-                    pages, heads, size, dim)
+    pages, heads, size, dim = shape = k_pages.shape
+    cells = (pages, heads)
+    return _kv_cache_bytes(_ptr(k_pages, "k_pages", torch.uint8, shape, index),
+                           _ptr(v_pages, "v_pages", torch.uint8, (pages, heads, dim, size), index),
+                           _ptr(k_scale, "k_scale", torch.float32, cells, index),
+                           _ptr(v_scale, "v_scale", torch.float32, cells, index),
+                           pages, heads, size, dim), heads, dim
 
 
-def _kv_batch(page_table, q_start, kv_lens, tokens: int, max_q: int, index: int) -> _KvBatch:
+def _kv_batch(page_table, q_start, kv_lens, tokens: int, max_q: int, index: int) -> bytes:
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [seqs, width], got {tuple(page_table.shape)}")
-    seqs, width = page_table.shape
-    return _KvBatch(_ptr(page_table, "page_table", torch.int32, (seqs, width), index),
-                    _ptr(q_start, "q_start", torch.int32, (seqs + 1,), index),
-                    _ptr(kv_lens, "kv_lens", torch.int32, (seqs,), index),
-                    tokens, seqs, width, max_q)
+    seqs, width = shape = page_table.shape
+    return _kv_batch_bytes(_ptr(page_table, "page_table", torch.int32, shape, index),
+                           _ptr(q_start, "q_start", torch.int32, (seqs + 1,), index),
+                           _ptr(kv_lens, "kv_lens", torch.int32, (seqs,), index),
+                           tokens, seqs, width, max_q)
 
 
 def _rows(t: torch.Tensor, name: str, dtype, shape, index: int):
     """Pointer and row stride of a [tokens, heads, head_dim] tensor whose rows may lie apart."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
-    if t.get_device() != index:
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+        if t.get_device() != index:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{index}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     tokens, heads, dim = shape
     row, head, one = t.stride()
-    if t.numel() and ((dim > 1 and one != 1) or (heads > 1 and head != dim)):
+    if ((dim > 1 and one != 1) or (heads > 1 and head != dim)) and t.numel():
         raise ValueError(f"{name}: a row's heads must be contiguous, got strides {t.stride()}")
     return t.data_ptr(), row if tokens > 1 else max(row, heads * dim)
 
@@ -528,12 +528,12 @@ def fp8_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pag
     q_out may be q.  Returns q_out (None without q)."""
     code = _dtype_code(k)
     index, stream = _where(k)
-    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    cache, kv_heads, head_dim = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
     if k.dim() != 3 or (q is not None and q.dim() != 3):
         raise ValueError("k, v and q must be [tokens, heads, head_dim]")
     tokens = k.shape[0]
     batch = _kv_batch(page_table, q_start, kv_lens, tokens, max_q, index)
-    shape = (tokens, cache.kv_heads, cache.head_dim)
+    shape = (tokens, kv_heads, head_dim)
     rows, dim = 0, 0
     if rope is not None:
         if rope.dim() != 2:
@@ -544,7 +544,7 @@ def fp8_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pag
         heads = q.shape[1]
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qshape = (tokens, heads, cache.head_dim)
+        qshape = (tokens, heads, head_dim)
         qp, qs = _rows(q, "q", k.dtype, qshape, index)
         op, os_ = _rows(q_out, "q_out", k.dtype, qshape, index)
     elif q_out is not None:
@@ -560,8 +560,8 @@ def paged_attention_work_bytes(tokens: int, seqs: int, table_width: int, max_q: 
                                kv_heads: int, page_size: int, head_dim: int) -> int:
     """Bytes of scratch fp8_paged_attention needs (0 for sizes it refuses)."""
     return int(lib.fp8_paged_attention_work_bytes(
-        _KvCache(None, None, None, None, 1, kv_heads, page_size, head_dim),
-        _KvBatch(None, None, None, tokens, seqs, table_width, max_q), q_heads))
+        _kv_cache_bytes(0, 0, 0, 0, 1, kv_heads, page_size, head_dim),
+        _kv_batch_bytes(0, 0, 0, tokens, seqs, table_width, max_q), q_heads))
 
 
 def paged_attention_work(q: torch.Tensor, k_pages: torch.Tensor, page_table: torch.Tensor,
@@ -589,12 +589,12 @@ def fp8_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     q_heads]); a row that sees no token gets zeros and -inf."""
     code = _dtype_code(q)
     index, stream = _where(q)
-    cache = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
+    cache, kv_heads, head_dim = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
     if q.dim() != 3:
         raise ValueError(f"q must be [tokens, heads, head_dim], got {tuple(q.shape)}")
     tokens, heads = q.shape[:2]
     batch = _kv_batch(page_table, q_start, kv_lens, tokens, max_q, index)
-    shape = (tokens, heads, cache.head_dim)
+    shape = (tokens, heads, head_dim)
     if y is None:
         y = torch.empty(shape, dtype=q.dtype, device=q.device)
     if lse is None:
@@ -607,7 +607,7 @@ def fp8_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
         raise ValueError(f"work must hold at least {need} bytes, got {work.numel()}")
     _check("fp8_paged_attention", lib.fp8_paged_attention(
         cache, batch, *_rows(q, "q", q.dtype, shape, index), code, heads,
-        cache.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+        head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
         _ptr(y, "y", q.dtype, shape, index), _ptr(lse, "lse", torch.float32, (tokens, heads), index),
         _ptr(work, "work", torch.uint8, work.shape, index), stream))
     return y, lse

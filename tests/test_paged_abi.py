@@ -25,10 +25,32 @@ ATTEND = dict(q=at(10), q_stride=1024, dtype=0, q_heads=8, scale=0.1, causal=1, 
               lse=at(12), work=at(13), stream=None)
 
 
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p if n in ("k", "v", "k_scale", "v_scale") else ctypes.c_int64) for n in CACHE]
+
+
+class Batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p if n in ("page_table", "q_start", "kv_lens") else ctypes.c_int64)
+                for n in BATCH]
+
+
+def cache_of(c=CACHE):
+    return bytes(Cache(*c.values()))
+
+
+def batch_of(b=BATCH):
+    return bytes(Batch(*b.values()))
+
+
 def status(fn, own, change):
     c, b, a = ({k: change.get(k, v) for k, v in d.items()} for d in (CACHE, BATCH, own))
     assert set(change) <= set(c) | set(b) | set(a)
-    return fn(fp8q._KvCache(*c.values()), fp8q._KvBatch(*b.values()), *a.values())
+    return fn(cache_of(c), batch_of(b), *a.values())
+
+
+def test_structs_of_the_binding():
+    assert fp8q._kv_cache_bytes(*CACHE.values()) == cache_of()
+    assert fp8q._kv_batch_bytes(*BATCH.values()) == batch_of()
 
 
 COMMON = [
@@ -86,10 +108,10 @@ def test_attention_refused(change, want):
 
 def test_refused_without_structs():
     a, b = list(APPEND.values()), list(ATTEND.values())
-    assert fp8q.lib.fp8_kv_append(None, fp8q._KvBatch(*BATCH.values()), *a) == NULLP
-    assert fp8q.lib.fp8_kv_append(fp8q._KvCache(*CACHE.values()), None, *a) == NULLP
-    assert fp8q.lib.fp8_paged_attention(None, fp8q._KvBatch(*BATCH.values()), *b) == NULLP
-    assert fp8q.lib.fp8_paged_attention(fp8q._KvCache(*CACHE.values()), None, *b) == NULLP
+    assert fp8q.lib.fp8_kv_append(None, batch_of(), *a) == NULLP
+    assert fp8q.lib.fp8_kv_append(cache_of(), None, *a) == NULLP
+    assert fp8q.lib.fp8_paged_attention(None, batch_of(), *b) == NULLP
+    assert fp8q.lib.fp8_paged_attention(cache_of(), None, *b) == NULLP
 
 
 @pytest.mark.skipif(torch.cuda.is_available(), reason="without a GPU the device check ends the call")
