@@ -66,7 +66,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
             const int keys = (mid.hi - mid.lo) / kKeys + 1, most = slots / a.Hk;
             int each = max((int)ceilf(wave_total((float)tiles * (float)keys) / (float)most), kLeastTiles);
             // twice the even share is always enough, as the units are half of what fits at most
-            for (int i = 0; i < 12; ++i) {
+            for (int i = 0; i < 13; ++i) {
                 parts = (keys + each - 1) / each;
                 if (wave_total((float)tiles * (float)parts) <= (float)most) break;
                 each += (each + 15) >> 4;

@@ -200,13 +200,9 @@ def test_pages_past_32_bits():
 def test_graph_replays_and_another_stream():
     """A captured decode step replayed as the lengths advance, and the same steps called eagerly on
     another stream: both as the host form has them."""
-    bt = ref.Batch([1] * 5, [14 + 3 * b for b in range(5)], 4, 128, 16, seed=30, width=4)
-    spare = [p for p in range(bt.pages) if p not in bt.table.flatten().tolist()]
-    bt2 = ref.Batch([1] * 5, [60] * 5, 4, 128, 16, seed=31)
-    bt2.lens = [14 + 3 * b for b in range(5)]
-    bt2.kv_lens = torch.tensor(bt2.lens, dtype=torch.int32)
-    del bt, spare
-    bt = bt2
+    bt = ref.Batch([1] * 5, [60] * 5, 4, 128, 16, seed=31)      # pages for 60 tokens each
+    bt.lens = [14 + 3 * b for b in range(5)]
+    bt.kv_lens = torch.tensor(bt.lens, dtype=torch.int32)
     rope = ref.rope_table(bt.width * 16, 128).to(DEV)
     shape = (5, 4, 128)
     k, v = (torch.zeros(shape, dtype=torch.bfloat16, device=DEV) for _ in range(2))

@@ -115,6 +115,51 @@ def test_many_sequences():
     run(bt, 2, torch.float16)
 
 
+@pytest.mark.parametrize("heads,kv_heads,page", [(8, 1, 16), (4, 4, 64), (6, 2, 128)])
+def test_many_sequences_of_several_tokens(heads, kv_heads, page):
+    """More sequences than a wave has lanes, of which some bring many rows and some are long."""
+    new = [1 + (b * 5) % 7 if b % 9 else 0 for b in range(90)]
+    lens = [n + (b * 53) % 80 for b, n in enumerate(new)]
+    new[30], lens[30], lens[60] = 40, 700, 1300
+    say("many sequences of several tokens", heads, kv_heads, page)
+    bt = ref.Batch(new, lens, kv_heads, 32, page, seed=22, lead=2, tail=1)
+    run(bt, heads, torch.bfloat16)
+
+
+@pytest.mark.parametrize("seqs,kv_heads,page,length", [(70, 4, 16, 2500), (33, 8, 64, 5000), (70, 4, 128, 4500)])
+def test_long_among_many_units(seqs, kv_heads, page, length):
+    """A workgroup goes through more key tiles than it looks pages up for at once."""
+    lens = [length] + [1 + b % 40 for b in range(1, seqs)]
+    say("long among many", seqs, kv_heads, page, length)
+    bt = ref.Batch([1] * seqs, lens, kv_heads, 16, page, seed=23)
+    run(bt, kv_heads, torch.float16)
+
+
+@pytest.mark.parametrize("page,window", [(16, 1000), (64, 1), (128, 2100)])
+def test_windows_in_long_contexts(page, window):
+    say("window", page, window)
+    bt = ref.Batch([1, 3, 0, 20], [5000, 3001, 900, 2203], 2, 64, page, seed=24)
+    run(bt, 4, torch.bfloat16, window=window)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_mixtures(seed):
+    """Batches of any mixture of new tokens, lengths, layouts and masks."""
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda *xs: xs[int(torch.randint(len(xs), (1,), generator=g))]              # noqa: E731
+    most, longest = pick(1, 3, 90), pick(60, 900, 3500)
+    new = torch.randint(0, most + 1, (pick(3, 20),), generator=g).tolist()
+    lens = [n + int(torch.randint(longest, (1,), generator=g)) for n in new]
+    kv_heads, group = pick(1, 2, 3), pick(1, 3, 8)
+    dim, page, dtype = pick(48, 64, 128, 224), pick(16, 32, 64, 128), pick(torch.bfloat16, torch.float16)
+    causal, window = pick((True, 0), (True, 300), (False, 0))
+    say("mixture", seed, most, longest, len(new), kv_heads, group, dim, page, dtype, causal, window)
+    if sum(new) * group * kv_heads > 600:
+        new, lens = new[:3], lens[:3]
+    bt = ref.Batch(new or [1], lens or [1], kv_heads, dim, page, seed=seed, lead=1, tail=3)
+    run(bt, group * kv_heads, dtype, causal, window)
+
+
 def test_scales_far_apart():
     """Pages whose values' scales differ by 2^80, and scales that are no powers of two: every page
     keeps its bits where it is the one that counts."""
@@ -266,6 +311,25 @@ def test_strided_queries_are_the_dense_ones():
     b = call(d, wide[:, 3:7].contiguous(), 80)
     torch.cuda.synchronize()
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_scratch_of_the_callers():
+    bt = ref.Batch([2, 1], [3000, 70], 2, 64, 64, seed=25)
+    q, d = bt.values(8, torch.bfloat16).to(DEV), on_gpu(bt)
+    work = fp8q.paged_attention_work(q, d["k"], d["table"], 2)
+    say("scratch")
+    want = call(d, q, 2)
+    got = call(d, q, 2, work=torch.full((work.numel() + 64,), 0xFF, dtype=torch.uint8, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    with pytest.raises(ValueError, match="work must hold"):
+        call(d, q, 2, work=work[:-1])
+    with pytest.raises(ValueError, match="y must have shape"):
+        call(d, q, 2, y=torch.empty((3, 8, 32), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(TypeError, match="lse must be"):
+        call(d, q, 2, lse=torch.empty((3, 8), dtype=torch.bfloat16, device=DEV))
+    with pytest.raises(ValueError, match="heads must be contiguous"):
+        call(d, q.transpose(0, 1).contiguous().transpose(0, 1), 2)
 
 
 def test_results_repeat_bit_for_bit():
