@@ -772,9 +772,11 @@ fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch
 }
 
 namespace {
-bool query_heads_ok(int64_t q_heads, int64_t kv_heads)
+// Rows of a sequence and key/value head are counted in an int.
+bool query_heads_ok(const fp8q_kv_cache& c, const fp8q_kv_batch& s, int64_t q_heads)
 {
-    return q_heads >= 1 && q_heads <= kMaxPagedHeads && q_heads % kv_heads == 0;
+    return q_heads >= 1 && q_heads <= kMaxPagedHeads && q_heads % c.kv_heads == 0 &&
+           s.tokens * (q_heads / c.kv_heads) <= kMaxPagedRows;
 }
 AttendArgs attend_args(const fp8q_kv_cache& c, const fp8q_kv_batch& s, int64_t q_heads)
 {
@@ -797,7 +799,7 @@ AttendArgs attend_args(const fp8q_kv_cache& c, const fp8q_kv_batch& s, int64_t q
 
 int64_t fp8_paged_attention_work_bytes(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch, int64_t q_heads)
 {
-    if (!cache || !batch || check_paged_sizes(*cache, *batch) != FP8Q_OK || !query_heads_ok(q_heads, cache->kv_heads))
+    if (!cache || !batch || check_paged_sizes(*cache, *batch) != FP8Q_OK || !query_heads_ok(*cache, *batch, q_heads))
         return 0;
     return attend_work_bytes(attend_args(*cache, *batch, q_heads));
 }
@@ -811,7 +813,7 @@ fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch*
     if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
     FP8Q_TRY(check_paged(cache, batch));
     const int64_t D = cache->head_dim, Hk = cache->kv_heads, T = batch->tokens;
-    if (!query_heads_ok(q_heads, Hk) || !stride_ok(q_stride, q_heads, D) ||
+    if (!query_heads_ok(*cache, *batch, q_heads) || !stride_ok(q_stride, q_heads, D) ||
         !(scale >= -FLT_MAX && scale <= FLT_MAX) || window < 0 || window > kMaxPagedLen ||
         (window > 0 && !causal))
         return FP8Q_ERR_SHAPE;

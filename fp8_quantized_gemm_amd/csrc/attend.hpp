@@ -16,10 +16,6 @@ constexpr float kSlack = 6.0f, kShift = 9.0f, kShiftScale = 0x1p9f;
 
 // A value that all lanes of the wave have, told to the compiler.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ int64_t uniform(int64_t v)
-{
-    return (int64_t)((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32 | (uint32_t)uniform((int)v));
-}
 
 struct KeyRange {
     int lo, hi;
@@ -41,37 +37,25 @@ __device__ __forceinline__ KeyRange key_range(const AttendArgs& a, const PagedSe
 struct PageScales {
     float key, log_value, inverse_value;
 };
-__device__ __forceinline__ PageScales page_scales(const AttendArgs& a, float k_scale, float v_scale)
-{
-    const float v = page_scale(v_scale);
-    // never 0, which would make NaN of a masked key's -inf
-    const float k = fmaxf(page_scale(k_scale) * a.scale_log2, FLT_MIN);
-    return PageScales{k, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v) * (1.0f / kShiftScale)};
-}
 __device__ __forceinline__ PageScales page_scales(const AttendArgs& a, int64_t page, int h)
 {
     const int64_t cell = page * a.Hk + h;
-    return page_scales(a, a.k_scale[cell], a.v_scale[cell]);
+    const float v = page_scale(a.v_scale[cell]);
+    // never 0, which would make NaN of a masked key's -inf
+    const float k = fmaxf(page_scale(a.k_scale[cell]) * a.scale_log2, FLT_MIN);
+    return PageScales{k, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v) * (1.0f / kShiftScale)};
 }
 
 struct PageRef {
-    int64_t page;            // 0 where there is none, so that an address can be made of it
-    int inside;              // the token's place in its page
+    int page;                // 0 where there is none, so that an address can be made of it
     bool valid;
 };
-// The page table's entry for a key, -1 past the sequence's end.
-__device__ __forceinline__ int page_id(const AttendArgs& a, int b, int len, int key)
-{
-    return key < len ? a.batch.page_table[(int64_t)b * a.batch.W + (key >> a.page_shift)] : -1;
-}
-__device__ __forceinline__ PageRef page_ref(const AttendArgs& a, int id, int key)
-{
-    const bool valid = id >= 0 && id < a.pages;
-    return PageRef{valid ? id : 0, key & (a.P - 1), valid};
-}
+// The page with a key; none past the sequence's end.
 __device__ __forceinline__ PageRef page_ref(const AttendArgs& a, int b, int len, int key)
 {
-    return page_ref(a, page_id(a, b, len, key), key);
+    const int id = key < len ? a.batch.page_table[(int64_t)b * a.batch.W + (key >> a.page_shift)] : -1;
+    const bool valid = id >= 0 && id < a.pages;
+    return PageRef{valid ? id : 0, valid};
 }
 
 // The E4M3 codes of NaN in four codes, as 0x80 in their bytes.

@@ -7,10 +7,27 @@ namespace fp8q {
 namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64, kWaveRows = 32, kTileRows = kWaves * kWaveRows;
-constexpr int kLeastTiles = 4;            // of a part of a unit
 // Workgroups that the chip holds at once.
 constexpr int slots_for(int dp) { return kCUs * (dp <= 128 ? 2 : 1); }
 constexpr int kRankedSeqs = 64;           // sequences that a wave ranks by length
+
+// Rows of a part of a unit.
+__host__ __device__ __forceinline__ int part_rows(const AttendArgs& a)
+{
+    const int64_t rows = (int64_t)a.batch.max_q * a.group;
+    return (int)(rows < kTileRows ? rows : kTileRows);
+}
+// Key tiles that a part has at least: its rows go through the scratch.  Where units are few, parts of
+// 4 tiles are short enough to use the chip (64/8 heads, 128 tokens of 2000: 31 us, 36 with 20), and for
+// few rows parts of 2 (1 token of 1300: 12.7 us, 15.0 with 4; but 256 of 256: 21.1 us, 14.3 with 4).
+// Where they are more than a quarter of the workgroups that fit, cutting them doubles those on a
+// compute unit at best, which pays for many rows if the parts are long (512 of 512: 22 us, 33 with 4).
+__host__ __device__ __forceinline__ int least_tiles(const AttendArgs& a, int64_t units, int slots)
+{
+    const int rows = part_rows(a);
+    if (units * a.Hk * 4 > slots) return 4 + rows / 8;
+    return rows <= kShortRows ? 2 : 4;
+}
 
 // What a workgroup does: rows row0 .. of sequence b, the `part`-th of `parts` equal runs of the keys
 // that they see.
@@ -64,7 +81,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
             // a unit's key tiles, as those of the sequence's middle token
             const KeyRange mid = key_range(a, q, q.n / 2);
             const int keys = (mid.hi - mid.lo) / kKeys + 1, most = slots / a.Hk;
-            int each = max((int)ceilf(wave_total((float)tiles * (float)keys) / (float)most), kLeastTiles);
+            int each = max((int)ceilf(wave_total((float)tiles * (float)keys) / (float)most), least_tiles(a, units, slots));
             // twice the even share is always enough, as the units are half of what fits at most
             for (int i = 0; i < 13; ++i) {
                 parts = (keys + each - 1) / each;
@@ -112,12 +129,7 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
 }
 
 // The scratch where units are cut: what each unit of each key/value head is, then a part for each
-// workgroup, of so many rows.
-__host__ __device__ __forceinline__ int64_t part_rows(const AttendArgs& a)
-{
-    const int64_t rows = (int64_t)a.batch.max_q * a.group;
-    return rows < kTileRows ? rows : kTileRows;
-}
+// workgroup.
 __host__ __device__ __forceinline__ float* parts_of(const AttendArgs& a, int64_t units)
 {
     static_assert(sizeof(Unit) % 16 == 0, "parts are read 16 bytes at a time");
@@ -221,11 +233,11 @@ Plan plan_of(const AttendArgs& a)
     const int64_t loose = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
     const int64_t tight = a.batch.B * (((int64_t)a.batch.max_q * a.group + kTileRows - 1) / kTileRows);
     const int64_t units = loose < tight ? loose : tight, slots = slots_for((int)a.D);
-    const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys;
-    const bool cut = units * a.Hk * 2 <= slots && tiles > kLeastTiles;
+    const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys, least = least_tiles(a, units, (int)slots);
+    const bool cut = units * a.Hk * 2 <= slots && tiles > least;
     if (a.batch.B <= kRankedSeqs)
         return cut ? Plan{units, slots / a.Hk * a.Hk, 1, true} : Plan{units, units * a.Hk, 1, false};
-    const int64_t fit = cut ? slots / (units * a.Hk) : 1, most = (tiles + kLeastTiles - 1) / kLeastTiles;
+    const int64_t fit = cut ? slots / (units * a.Hk) : 1, most = (tiles + least - 1) / least;
     const int64_t splits = fit < most ? fit : most;
     return Plan{loose, loose * a.Hk * splits, (int)splits, cut};
 }
@@ -239,7 +251,7 @@ hipError_t launch(const AttendArgs& a, hipStream_t stream)
                        dim3(kThreads), 0, stream, a, plan.units, groups, plan.splits, plan.cut ? 1 : 0);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !plan.cut) return e;
-    return launch_join<DT, DP>(a, parts_of(a, plan.units), plan.units, (int)part_rows(a), stream);
+    return launch_join<DT, DP>(a, parts_of(a, plan.units), plan.units, part_rows(a), stream);
 }
 
 template <int DT, int DP>

@@ -307,7 +307,7 @@ __device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, in
 {
     const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
     const PageRef p = page_ref(a, b, len, key);
-    return Pages{(int)p.page, page_scales(a, p.page, h), __ballot(p.valid)};
+    return Pages{p.page, page_scales(a, p.page, h), __ballot(p.valid)};
 }
 // The scales of the i-th tile of a look-up as add_tile takes them, and whether its pages are there.
 template <bool WIDE>

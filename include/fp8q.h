@@ -194,7 +194,7 @@ FP8Q_API fp8q_status fp8_linear_rowwise(const void* x, int dtype, const uint8_t*
 /*
  * fp8_quantize_kv - FP8 KV cache: E4M3 codes of a K or V block with one scale
  *   per head ([RTX4060] §1 stores the KV cache in FP8, [C++FP8] §4.2 builds
- *   with an FP8 KV-cache type; attention itself is not part of this library).
+ *   with an FP8 KV-cache type; for a paged cache see fp8_kv_append).
  *
  *   x[T,H,D]  in : bf16/fp16 bit patterns, tokens x heads x head dimension
  *   q[T,H,D]  out: E4M3 codes; head h quantized with scale[h]
@@ -552,8 +552,9 @@ FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_bat
  *   work   scratch of fp8_paged_attention_work_bytes bytes, 16-byte aligned;
  *          contents before and after the call are of no meaning.  Calls that may
  *          run at the same time need one each.
- *   q_heads % kv_heads == 0, q_heads <= 1024;  scale finite;
- *   0 <= window <= 2^24.
+ *   q_heads % kv_heads == 0, q_heads <= 1024, tokens * (q_heads / kv_heads) <=
+ *   2^30;  scale finite;  0 <= window <= 2^24.  One launch, two where sequences
+ *   longer than 1024 (table_width * P) leave the GPU room to share their keys out.
  *   fp8_paged_attention_work_bytes looks at the sizes in the structs only (pages
  *   apart, which does not matter), and gives 0 for sizes that the call refuses.
  */

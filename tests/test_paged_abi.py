@@ -92,6 +92,7 @@ def test_append_refused(change, want):
 @pytest.mark.parametrize("change,want", COMMON + [
     *[({n: None}, NULLP) for n in ("q", "y", "work")],
     ({"q_heads": 7}, SHAPE), ({"q_heads": 1}, SHAPE),
+    ({"q_heads": 64, "q_stride": 64 * 128, "tokens": 2 ** 25 + 1}, SHAPE),
     *[({"scale": x}, SHAPE) for x in (math.inf, -math.inf, math.nan)],
     ({"window": -1}, SHAPE), ({"window": 2 ** 24 + 1}, SHAPE), ({"window": 5, "causal": 0}, SHAPE),
     *[({n: at(20, 8)}, ALIGN) for n in ("y", "work")],
@@ -139,7 +140,7 @@ def test_work_bytes():
     assert fp8q.paged_attention_work_bytes(**{**good, "max_q": 4, "q_heads": 64}) > 0
     for change in (dict(q_heads=0), dict(q_heads=3), dict(q_heads=2048), dict(kv_heads=0), dict(head_dim=24),
                    dict(head_dim=272), dict(max_q=0), dict(max_q=5), dict(page_size=48), dict(seqs=0),
-                   dict(tokens=0), dict(table_width=0), dict(table_width=2 ** 18 + 1)):
+                   dict(tokens=0), dict(tokens=2 ** 26, q_heads=64), dict(table_width=0), dict(table_width=2 ** 18 + 1)):
         assert fp8q.paged_attention_work_bytes(**{**good, **change}) == 0
 
 
