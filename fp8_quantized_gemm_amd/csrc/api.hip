@@ -812,7 +812,7 @@ fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch*
     if (!q || !y || !work) return FP8Q_ERR_NULL;
     if (dtype != FP8Q_BF16 && dtype != FP8Q_FP16) return FP8Q_ERR_DTYPE;
     FP8Q_TRY(check_paged(cache, batch));
-    const int64_t D = cache->head_dim, Hk = cache->kv_heads, T = batch->tokens;
+    const int64_t D = cache->head_dim, T = batch->tokens;
     if (!query_heads_ok(*cache, *batch, q_heads) || !stride_ok(q_stride, q_heads, D) ||
         !(scale >= -FLT_MAX && scale <= FLT_MAX) || window < 0 || window > kMaxPagedLen ||
         (window > 0 && !causal))
