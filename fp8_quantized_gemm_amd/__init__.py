@@ -1,6 +1,7 @@
 """fp8_quantized_gemm_amd: FP8 E4M3 linear layers (per-tensor, per-row or block
-scales), a mixture-of-experts layer on block-scaled weights and the NestedFP
-dual-precision GEMM for AMD MI355X (gfx950).
+scales), a mixture-of-experts layer on block-scaled weights, a paged FP8
+key/value cache with attention over it and the NestedFP dual-precision GEMM
+for AMD MI355X (gfx950).
 
 The compute lives in ``libfp8q.so`` (hand-written HIP kernels behind a C ABI,
 declared in ``include/fp8q.h``).  ``fp8_quantized_gemm_amd.fp8q`` is the thin
