@@ -57,8 +57,17 @@ struct Item {
 // first `first` to a compute unit each, the next join them, the others follow where one ends; so the
 // longest come first, then the shortest, so that every compute unit has one of both, then the rest.
 //
-// More sequences are taken in their order; those of sequence b begin at unit q_start[b] * group /
-// kTileRows + b, and every unit has `splits` parts.
+// More sequences are taken in their order, and every unit has `splits` parts.  Units are numbered in
+// the way that needs fewer numbers: as many for each sequence as max_q allows, or those of sequence b
+// from q_start[b] * group / kTileRows + b on.
+__host__ __device__ __forceinline__ int64_t loose_units(const AttendArgs& a)
+{
+    return (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
+}
+__host__ __device__ __forceinline__ int most_units(const AttendArgs& a)           // of a sequence
+{
+    return (int)(((int64_t)a.batch.max_q * a.group + kTileRows - 1) / kTileRows);
+}
 __device__ __forceinline__ int64_t rank_of(int64_t place, int64_t count, int first)
 {
     if (place < first) return place;
@@ -127,15 +136,22 @@ __device__ __forceinline__ bool find_item(const AttendArgs& a, int64_t place, bo
     item.units = 0;                       // every unit that is not there is told by its first part
     item.unit = place / splits;
     const int64_t u = units - 1 - (cut ? item.unit : rank_of(place, units, first));
-    int below = 0;
-    for (int k = threadIdx.x; k < s.B; k += kThreads)
-        below += (int64_t)clamp_int(s.q_start[k], 0, s.T) * a.group / kTileRows + k <= u ? 1 : 0;
-    item.b = uniform(max(block_sum_int<kThreads>(below, lds) - 1, 0));
-    const PagedSeq q = paged_seq(s, item.b, a.P);
-    const int64_t row = (u - ((int64_t)q.row * a.group / kTileRows + item.b)) * kTileRows;
-    item.row0 = (int)row;
     item.parts = splits;
     item.part = (int)(place % splits);
+    int64_t first_unit;
+    if (most_units(a) * (int64_t)s.B <= loose_units(a)) {
+        item.b = (int)(u / most_units(a));
+        first_unit = (int64_t)item.b * most_units(a);
+    } else {
+        int below = 0;
+        for (int k = threadIdx.x; k < s.B; k += kThreads)
+            below += (int64_t)clamp_int(s.q_start[k], 0, s.T) * a.group / kTileRows + k <= u ? 1 : 0;
+        item.b = uniform(max(block_sum_int<kThreads>(below, lds) - 1, 0));
+        first_unit = (int64_t)clamp_int(s.q_start[item.b], 0, s.T) * a.group / kTileRows + item.b;
+    }
+    const PagedSeq q = paged_seq(s, item.b, a.P);
+    const int64_t row = (u - first_unit) * kTileRows;
+    item.row0 = (int)row;
     return row >= 0 && row < (int64_t)q.n * a.group;
 }
 
@@ -241,16 +257,15 @@ struct Plan {
 };
 Plan plan_of(const AttendArgs& a)
 {
-    const int64_t loose = (int64_t)a.batch.T * a.group / kTileRows + a.batch.B;
-    const int64_t tight = a.batch.B * (((int64_t)a.batch.max_q * a.group + kTileRows - 1) / kTileRows);
-    const int64_t units = loose < tight ? loose : tight, slots = slots_for((int)a.D);
+    const int64_t loose = loose_units(a), even = (int64_t)a.batch.B * most_units(a);
+    const int64_t units = loose < even ? loose : even, slots = slots_for((int)a.D);
     const int64_t tiles = ((int64_t)a.batch.W * a.P + kKeys - 1) / kKeys, least = least_tiles(a, units, (int)slots);
     const bool cut = units * a.Hk * 2 <= slots && tiles > least;
     if (a.batch.B <= kRankedSeqs)
         return cut ? Plan{units, slots / a.Hk * a.Hk, 1, true} : Plan{units, units * a.Hk, 1, false};
     const int64_t fit = cut ? slots / (units * a.Hk) : 1, most = (tiles + least - 1) / least;
     const int64_t splits = fit < most ? fit : most;
-    return Plan{loose, loose * a.Hk * splits, (int)splits, cut};
+    return Plan{units, units * a.Hk * splits, (int)splits, cut};
 }
 
 template <int DT, int DP, bool WIDE>
