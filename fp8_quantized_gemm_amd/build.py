@@ -18,7 +18,7 @@ OUT = os.path.join(HERE, "libfp8q.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["quant.hip", "gemv.hip", "linear.hip", "gemm.hip", "nested.hip", "block.hip",
-           "moe.hip", "append.hip", "attend_short.hip", "attend_tiles.hip", "api.hip"]
+           "moe.hip", "append.hip", "attend_tiles.hip", "attend_whole.hip", "api.hip"]
 
 FLAGS = [
     "--offload-arch=gfx950",

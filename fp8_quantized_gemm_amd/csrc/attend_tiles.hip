@@ -9,9 +9,8 @@
 // tokens with 64/8 heads x 128 take 297 us, 0.93 PFLOP/s (a library product of
 // 8192^3 reaches 1.2), vector units busy 71% and matrix units 45% of the time;
 // 2048 with 32/32 heads 58 us, where one workgroup of a compute unit's two ends
-// early.  Decoding is bound by HBM: 64 sequences of 8192 (1.08 GB) 199 us, 5.4
-// TB/s, with rows of a wave that are not there: a kernel of 16 rows a wave that
-// held its tiles in registers took 212.
+// early.  Decoding few long sequences is bound by HBM: 1 of 131072 (268 MB) in
+// 512 parts 54 us and 6 to join them.
 #include "tile32.hpp"
 
 namespace fp8q {
@@ -30,14 +29,14 @@ __host__ __device__ __forceinline__ int part_rows(const AttendArgs& a)
 }
 // Key tiles that a part has at least: its rows go through the scratch.  Where units are few, parts of
 // 4 tiles are short enough to use the chip (64/8 heads, 128 tokens of 2000: 31 us, 36 with 20), and for
-// few rows parts of 2 (1 token of 1300: 12.7 us, 15.0 with 4; but 256 of 256: 21.1 us, 14.3 with 4).
+// few rows parts of 2 (here 1 token of 1300 12.7 us, 15.0 with 4; but 256 of 256: 21.1 us, 14.3 with 4).
 // Where they are more than a quarter of the workgroups that fit, cutting them doubles those on a
 // compute unit at best, which pays for many rows if the parts are long (512 of 512: 22 us, 33 with 4).
 __host__ __device__ __forceinline__ int least_tiles(const AttendArgs& a, int64_t units, int slots)
 {
     const int rows = part_rows(a);
     if (units * a.Hk * 4 > slots) return 4 + rows / 8;
-    return rows <= kShortRows ? 2 : 4;
+    return rows <= kWholeRows ? 2 : 4;
 }
 
 // What a workgroup does: rows row0 .. of sequence b, the `part`-th of `parts` equal runs of the keys

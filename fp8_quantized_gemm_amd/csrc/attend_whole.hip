@@ -1,24 +1,26 @@
-// Attention over the paged FP8 cache for few query rows of short sequences (see
-// paged.hpp): all of a key/value head's keys in one launch.
+// Attention over the paged FP8 cache for few query rows, a key/value head of a
+// sequence whole in one workgroup (see paged.hpp for when).
 //
 //   S^T = K Q^T   MFMA 16x16x32, keys along M, the (token, head) rows along N
 //   P   = 2^(S^T * ks + lv - m)   in the lanes of its row
 //   Y^T = V^T P   MFMA 16x16x32, channels along M
 //
-// What such a call takes is the chain of a launch, the lengths, the page ids,
-// the codes and the arithmetic on one tile, so a workgroup of 8 waves takes a
-// key/value head, a wave one or two tiles of 64 keys straight into registers,
-// and the waves' sums are joined in LDS: 1 token of 500 with 64/8 heads takes
-// 8.2 us, of 64 5.2 us, 16 tokens of 500 9.9 us.  On the tile kernel, which cuts
-// the keys over workgroups and joins them in a second launch, 1 of 500 takes
-// 15.8, 128 of up to 600 44.9 (34.7 here), 16 of 1000 with 32/32 heads 35.4
-// (33.8 here); past 1024 keys the tile kernel is ahead.
+// The 8 waves have equal runs of the key tiles, which they load straight into
+// registers, a tile of 64 keys ahead, and join their sums in LDS: no wave waits
+// for another before the end, and there is one launch.  Short calls are bound
+// by the chain of a launch, the lengths, the page ids, the codes and the
+// arithmetic on a tile or two: 1 token of 500 with 64/8 heads takes 8.2 us, of
+// 64 5.2 us.  A workgroup by itself reads about 45 GB/s, so from about 128 of
+// them on HBM is the bound: 32 tokens of 4000 51 us (5.2 TB/s), 64 of 8192 199 us
+// (5.4 TB/s).  Workgroups of neighbouring heads follow each other, so that a
+// long sequence's run side by side (24 of up to 2048 with 32/32 heads: 55.6 us,
+// 61.9 with neighbouring sequences; the longest first: 59.7).
 #include "attend.hpp"
 
 namespace fp8q {
 namespace {
 
-constexpr int kRows = kShortRows;         // query rows of a workgroup: (token, head of the group) pairs
+constexpr int kRows = kWholeRows;         // query rows of a workgroup: (token, head of the group) pairs
 constexpr int kKeys = 64;                 // keys of a tile
 // Waves of a workgroup: eight where the registers allow.
 constexpr int waves_for(int dp) { return dp <= 128 ? 8 : 4; }
@@ -255,7 +257,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Run& u, Ro
 // A workgroup has all rows of a key/value head of a sequence, its waves equal runs of the key tiles;
 // the waves' sums are joined in LDS.
 template <int DT, int DP, bool WIDE>
-__global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_short_kernel(const AttendArgs a)
+__global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_whole_kernel(const AttendArgs a)
 {
     constexpr int kWaves = waves_for(DP), kThreads = kWaves * 64, ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
@@ -263,9 +265,11 @@ __global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_
     __shared__ __attribute__((aligned(16))) float sums[kWaves][kRows * RS];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+    const uint32_t index = blockIdx.y * gridDim.x + blockIdx.x;         // at most 2^26, and a row of the grid
+    if (index >= (uint32_t)(a.batch.B * a.Hk)) return;
     Run u;
-    u.b = blockIdx.x;
-    u.h = blockIdx.y;
+    u.b = (int)(index / (uint32_t)a.Hk);
+    u.h = (int)(index % (uint32_t)a.Hk);
     u.q = paged_seq(a.batch, u.b, a.P);
     u.rows = u.q.n * a.group;
     if (u.rows == 0) return;
@@ -303,8 +307,10 @@ __global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_
 template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    hipLaunchKernelGGL((attend_short_kernel<DT, DP, WIDE>), dim3((unsigned)a.batch.B, (unsigned)a.Hk),
-                       dim3(waves_for(DP) * 64), 0, stream, a);
+    constexpr int kThreads = waves_for(DP) * 64;
+    const int64_t groups = (int64_t)a.batch.B * a.Hk, most = max_groups(kThreads), gx = groups < most ? groups : most;
+    hipLaunchKernelGGL((attend_whole_kernel<DT, DP, WIDE>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
+                       dim3(kThreads), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -72,13 +72,23 @@ struct AttendArgs {
     int q_flip;                      // sign bits of two queries where the scale is negative, else 0
     int causal, window;
 };
-// Sequences of at most this many keys with few query rows have a kernel of their own: 1 token of 500
-// takes 8.2 us there (15.8 on the tile kernel), 128 of up to 600 34.7 (44.9), 16 of 1000 with 32/32 heads
-// 33.8 (35.4).  The host knows the page table's room only, not the lengths.
-constexpr int kShortKeys = 1024, kShortRows = 16;
+// With at most this many query rows a sequence, a workgroup can have a key/value head of it whole
+// (attend_whole.hip); the tile kernel cuts the keys over workgroups where there are few, with a second
+// launch.  Whole, in us, against the tile kernel, 64/8 heads x 128, u = sequences * key/value heads:
+//   u = 8    1 x 500 8.2 (15.8)     1 x 2000 16.4 (13.9)   1 x 4000 26.3 (14.0)
+//   u = 64   8 x 2000 18.1 (20.6)   8 x 4000 28.1 (24.4)   8 x 8000 57 (39)
+//   u = 128  16 x 4000 39 (43)      16 x 8000 62 (68), of up to 8000 56 (42)
+//   u = 192  24 x 4000 41 (62)      24 of up to 16000 115 (98)
+//   u = 256  32 x 4000 51 (63)      32 of up to 8000 71 (83)
+//   u = 512  64 of up to 8000 133 (166), of up to 32000 489 (620)
+// So whole up to 2048 keys, or 32 u, and always from two workgroups for each of 256 compute units on.
+// The host knows the page table's room only, not the lengths.
+constexpr int kWholeRows = 16;
 inline bool takes_tiles(const AttendArgs& a)
 {
-    return (int64_t)a.batch.max_q * a.group > kShortRows || (int64_t)a.batch.W * a.P > kShortKeys;
+    if ((int64_t)a.batch.max_q * a.group > kWholeRows) return true;
+    const int64_t u = (int64_t)a.batch.B * a.Hk, keys = (int64_t)a.batch.W * a.P;
+    return u < 512 && keys > 2048 && keys > 32 * u;
 }
 hipError_t launch_attend_tiles(const AttendArgs& a, int dtype, hipStream_t stream);
 int64_t attend_tiles_work_bytes(const AttendArgs& a);

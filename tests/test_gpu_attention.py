@@ -57,7 +57,7 @@ def run(bt, heads, dtype, causal=True, window=0, spread=1.0, spoil=True):
     want = ref.attend(bt, q, scale, causal, window)
     d = on_gpu(bt)
     # a narrow page table, and one that has room for more keys than a workgroup takes by itself
-    for room in (0, 1100):
+    for room in (0, 20000):
         d["table"] = torch.nn.functional.pad(bt.table, (0, -(-room // bt.page)), value=-1).to(DEV)
         y = torch.full(q.shape, 7.0, dtype=dtype, device=DEV)
         lse = torch.full(q.shape[:2], 7.0, device=DEV)
@@ -126,13 +126,15 @@ def test_many_sequences_of_several_tokens(heads, kv_heads, page):
     run(bt, heads, torch.bfloat16)
 
 
-@pytest.mark.parametrize("seqs,kv_heads,page,length", [(70, 4, 16, 2500), (33, 8, 64, 5000), (70, 4, 128, 4500)])
-def test_long_among_many_units(seqs, kv_heads, page, length):
-    """A workgroup goes through more key tiles than it looks pages up for at once."""
+@pytest.mark.parametrize("seqs,kv_heads,page,length,group", [
+    (70, 4, 16, 2500, 1), (33, 8, 64, 5000, 1), (70, 4, 128, 4500, 1), (1, 512, 16, 10000, 1),
+    (260, 2, 64, 40000, 1), (70, 4, 16, 2500, 17), (33, 8, 64, 5000, 17)])
+def test_long_among_many_units(seqs, kv_heads, page, length, group):
+    """A wave goes through more key tiles than it looks pages up for at once."""
     lens = [length] + [1 + b % 40 for b in range(1, seqs)]
-    say("long among many", seqs, kv_heads, page, length)
+    say("long among many", seqs, kv_heads, page, length, group)
     bt = ref.Batch([1] * seqs, lens, kv_heads, 16, page, seed=23)
-    run(bt, kv_heads, torch.float16)
+    run(bt, kv_heads * group, torch.float16)
 
 
 @pytest.mark.parametrize("page,window", [(16, 1000), (64, 1), (128, 2100)])

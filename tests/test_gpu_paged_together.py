@@ -75,7 +75,7 @@ def check(layer, got):
     assert torch.all((out.double() - a @ w.T).abs() <= bound)
 
 
-@pytest.mark.parametrize("room", [0, 1100])
+@pytest.mark.parametrize("room", [0, 2500])
 def test_prompts_then_single_tokens(room):
     prompts, steps = [37, 1, 90, 64], 4
     layer = Layer(prompts, steps, seed=40, room=room)
@@ -99,7 +99,7 @@ def test_prompts_in_chunks_are_prompts():
         check(layer, layer.forward(layer.hidden()))
 
 
-@pytest.mark.parametrize("room", [0, 1100])
+@pytest.mark.parametrize("room", [0, 2500])
 def test_two_captured_layers(room):
     """A decode step of two layers, each with its scratch, captured as one graph and replayed as
     the sequences grow: every replay gives what eager calls on another stream give."""
