@@ -5,7 +5,7 @@
 //   P   = 2^(S^T * ks + lv - m)   in the lanes of its row
 //   Y^T = V^T P   MFMA 16x16x32, channels along M
 //
-// The 8 waves have equal runs of the key tiles, which they load straight into
+// The waves (8 at most) have equal runs of the key tiles, which they load straight into
 // registers, a tile of 64 keys ahead, and join their sums in LDS: no wave waits
 // for another before the end, and there is one launch.  Short calls are bound
 // by the chain of a launch, the lengths, the page ids, the codes and the
@@ -22,7 +22,7 @@ namespace {
 
 constexpr int kRows = kWholeRows;         // query rows of a workgroup: (token, head of the group) pairs
 constexpr int kKeys = 64;                 // keys of a tile
-// Waves of a workgroup: eight where the registers allow.
+// Waves of a workgroup at most: eight where the registers allow.
 constexpr int waves_for(int dp) { return dp <= 128 ? 8 : 4; }
 
 // A key tile as a wave holds it: lane (r, g) has 16 channels for each 64 of the keys
@@ -256,10 +256,10 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Run& u, Ro
 
 // A workgroup has all rows of a key/value head of a sequence, its waves equal runs of the key tiles;
 // the waves' sums are joined in LDS.
-template <int DT, int DP, bool WIDE>
-__global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_whole_kernel(const AttendArgs a)
+template <int DT, int DP, bool WIDE, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64, DP <= 128 ? 2 : 1) attend_whole_kernel(const AttendArgs a)
 {
-    constexpr int kWaves = waves_for(DP), kThreads = kWaves * 64, ND = DP / 16;
+    constexpr int kWaves = WAVES, kThreads = kWaves * 64, ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
     __shared__ float stat[kWaves][kRows][2];
     __shared__ __attribute__((aligned(16))) float sums[kWaves][kRows * RS];
@@ -304,14 +304,26 @@ __global__ void __launch_bounds__(waves_for(DP) * 64, DP <= 128 ? 2 : 1) attend_
     }
 }
 
+template <int DT, int DP, bool WIDE, int WAVES>
+hipError_t launch_waves(const AttendArgs& a, hipStream_t stream)
+{
+    constexpr int kThreads = WAVES * 64;
+    const int64_t groups = (int64_t)a.batch.B * a.Hk, most = max_groups(kThreads), gx = groups < most ? groups : most;
+    hipLaunchKernelGGL((attend_whole_kernel<DT, DP, WIDE, WAVES>),
+                       dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)), dim3(kThreads), 0, stream, a);
+    return hipGetLastError();
+}
+// Fewer waves where there may be few key tiles: their registers and LDS keep other workgroups away (54
+// sequences of up to 200 tokens, 32/32 heads x 128: 24 us with 4 waves, 36 with 8; of up to 4 tokens x 96:
+// 10 with 1, 32 with 8).  With few workgroups more waves store the rows sooner (1 of 60, 64/8 heads: 5.8 us
+// with 8, 6.8 with 1).
 template <int DT, int DP, bool WIDE>
 hipError_t launch(const AttendArgs& a, hipStream_t stream)
 {
-    constexpr int kThreads = waves_for(DP) * 64;
-    const int64_t groups = (int64_t)a.batch.B * a.Hk, most = max_groups(kThreads), gx = groups < most ? groups : most;
-    hipLaunchKernelGGL((attend_whole_kernel<DT, DP, WIDE>), dim3((unsigned)gx, (unsigned)((groups + gx - 1) / gx)),
-                       dim3(kThreads), 0, stream, a);
-    return hipGetLastError();
+    const int64_t keys = (int64_t)a.batch.W * a.P, groups = (int64_t)a.batch.B * a.Hk;
+    if (keys <= kKeys && groups >= 512) return launch_waves<DT, DP, WIDE, 1>(a, stream);
+    if (DP <= 128 && keys <= 4 * kKeys) return launch_waves<DT, DP, WIDE, 4>(a, stream);
+    return launch_waves<DT, DP, WIDE, waves_for(DP)>(a, stream);
 }
 
 template <int DT, int DP>

@@ -115,6 +115,15 @@ def test_many_sequences():
     run(bt, 2, torch.float16)
 
 
+@pytest.mark.parametrize("kv_heads,dim,page", [(1, 32, 16), (2, 128, 64), (1, 256, 32)])
+def test_many_short_sequences(kv_heads, dim, page):
+    """So many that a workgroup of one wave has a sequence and head whole."""
+    lens = [(b * 29) % 62 for b in range(520)]
+    say("many short sequences", kv_heads, dim, page)
+    bt = ref.Batch([1] * 520, lens, kv_heads, dim, page, seed=26)
+    run(bt, kv_heads * 2, torch.bfloat16)
+
+
 @pytest.mark.parametrize("heads,kv_heads,page", [(8, 1, 16), (4, 4, 64), (6, 2, 128)])
 def test_many_sequences_of_several_tokens(heads, kv_heads, page):
     """More sequences than a wave has lanes, of which some bring many rows and some are long."""
