@@ -32,20 +32,6 @@ __device__ __forceinline__ KeyRange key_range(const AttendArgs& a, const PagedSe
     return k;
 }
 
-// Scales of a page and head: a term is 2^(s * key + log_value) with s = q k^T,
-// times the values' scale, and counts inverse_value times that in the sum.
-struct PageScales {
-    float key, log_value, inverse_value;
-};
-__device__ __forceinline__ PageScales page_scales(const AttendArgs& a, int64_t page, int h)
-{
-    const int64_t cell = page * a.Hk + h;
-    const float v = page_scale(a.v_scale[cell]);
-    // never 0, which would make NaN of a masked key's -inf
-    const float k = fmaxf(page_scale(a.k_scale[cell]) * a.scale_log2, FLT_MIN);
-    return PageScales{k, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v) * (1.0f / kShiftScale)};
-}
-
 struct PageRef {
     int page;                // 0 where there is none, so that an address can be made of it
     bool valid;
@@ -56,6 +42,52 @@ __device__ __forceinline__ PageRef page_ref(const AttendArgs& a, int b, int len,
     const int id = key < len ? a.batch.page_table[(int64_t)b * a.batch.W + (key >> a.page_shift)] : -1;
     const bool valid = id >= 0 && id < a.pages;
     return PageRef{valid ? id : 0, valid};
+}
+
+// Scales of a page and head: a term is 2^(s * key + log_value) with s = q k^T,
+// times the values' scale, and counts inverse_value times that in the sum.
+struct PageScales {
+    float key, log_value, inverse_value;
+};
+__device__ __forceinline__ PageScales page_scales(const AttendArgs& a, const PageRef& page, int h)
+{
+    const int64_t cell = (int64_t)page.page * a.Hk + h;
+    const float held = page_scale(a.v_scale[cell]), v = page.valid ? held : 1.0f;
+    // never 0, which would make NaN of a masked key's -inf
+    const float k = fmaxf(page_scale(a.k_scale[cell]) * a.scale_log2, FLT_MIN);
+    return PageScales{k, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v) * (1.0f / kShiftScale)};
+}
+
+// The denominator is summed from the terms of the numerators, which have the values' scale in them,
+// as long as all scales of values lie within 2^-kNear .. 2^kNear.  A key that matters in the denominator
+// (2^24 keys of 2^-48 of the largest do not, to fp32) is then a term, and the sum that it is in has a
+// factor when the reference moves, of at least 2^(-48 - 2 kNear - kSlack) = 2^-126: nothing is lost.
+// From the first scale outside on (`apart`), a wave sums its denominators from exponentials of their
+// own, over a reference of their own: on pages of 2^-100 and 2^100 the keys that count most in the
+// denominator may be 2^-200 of those in the numerator.  Asking costs prompts 1 to 3% (4096 tokens,
+// 64/8 heads x 128: 297 us before, 301 with it) and other calls up to 0.7 us.
+constexpr float kNear = 36.0f;
+// Whether a lane's scale is apart.  Asked after the first codes of its pages are requested: before, they
+// would wait for the scales.
+__device__ __forceinline__ bool any_apart(const PageScales& s) { return __ballot(fabsf(s.log_value) > kNear) != 0; }
+// 16 logarithms s(i) * key, of which `top` is the largest, to the sum l over the reference z.
+template <class S>
+__device__ __forceinline__ void add_apart(float& z, float& l, float top, float key, S s)
+{
+    const float z1 = fmaxf(z, top), ref = z1 == -__builtin_inff() ? 0.0f : z1;
+    l *= __builtin_amdgcn_exp2f(z - ref);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) l += __builtin_amdgcn_exp2f(__builtin_fmaf(s(i), key, -ref));
+    z = z1;
+}
+// A row's denominator from the lanes that are `off` apart.
+__device__ __forceinline__ void join_lanes(float& z, float& l, int off)
+{
+    const float mine = z;
+    const float other = __shfl_xor(z, off), more = __shfl_xor(l, off);
+    z = fmaxf(z, other);
+    const float ref = z == -__builtin_inff() ? 0.0f : z;
+    l = l * __builtin_amdgcn_exp2f(mine - ref) + more * __builtin_amdgcn_exp2f(other - ref);
 }
 
 // The E4M3 codes of NaN in four codes, as 0x80 in their bytes.
@@ -123,9 +155,9 @@ __device__ __forceinline__ void mask_tile(v4f (&s)[4], v4f (&acc)[ND], v4i (&vf)
     }
 }
 
-// A row's reference (0 for ref where there was no key), and its denominator over it.
+// References of a row's sums and of its denominator (0 where there was no key), and its denominator.
 struct Joined {
-    float m, ref, l;
+    float ref, z, l;
 };
 // Four channels of a row from its sums, and the row's lse from its first channels.
 template <int DT>
@@ -133,18 +165,18 @@ __device__ __forceinline__ void store_row(const AttendArgs& a, int64_t token, in
                                           const Joined& j)
 {
     const bool empty = j.l == 0.0f;         // not by the maximum, which skips NaN
-    const float f = empty ? 0.0f : 1.0f / (j.l * kShiftScale);
+    const float f = empty ? 0.0f : 1.0f / (j.l * kShiftScale), e = __builtin_amdgcn_exp2f(j.ref - j.z);
     const int64_t row = token * a.Hq + head;
     uint32_t w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const v2f x = {empty ? 0.0f : o[2 * i] * f, empty ? 0.0f : o[2 * i + 1] * f};
+        const v2f x = {empty ? 0.0f : o[2 * i] * f * e, empty ? 0.0f : o[2 * i + 1] * f * e};
         if constexpr (DT == DT_BF16) w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2b));
         else w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, v2h));
     }
     *reinterpret_cast<v2i*>(a.y + row * a.D + d) = v2i{(int)w[0], (int)w[1]};
     if (d == 0 && a.lse != nullptr)
-        a.lse[row] = empty ? -__builtin_inff() : (j.ref + __builtin_amdgcn_logf(j.l)) * 0.6931471805599453f;
+        a.lse[row] = empty ? -__builtin_inff() : (j.z + __builtin_amdgcn_logf(j.l)) * 0.6931471805599453f;
 }
 
 }  // namespace fp8q

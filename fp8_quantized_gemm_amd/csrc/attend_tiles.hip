@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
         const int i = (t - t0) % kLookUp<WIDE>;
         if (i == 0) pages = look_up<WIDE>(a, b, q.len, t * kKeys, h);
         request_tile<DP, WIDE, KB, VB>(a, pages, i, t * kKeys, h, wave, lds_at + slot * (uint32_t)sizeof(lds[0]));
+        if (i == 0) x.apart |= any_apart(pages.sc);
     };
     if (t0 < t1) request(t0, 0);
     for (int t = t0; t < t1; ++t) {
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, DP <= 128 ? 2 : 1)
         add_tile<DT, DP, WIDE>(x, lds[slot], now, see, key0, valid, whole, clean[wave]);
     }
 
-    x.l += __shfl_xor(x.l, 32);
+    join_lanes(x.z, x.l, 32);
     if (!have_row) return;
     float* const part = parts_of(a, units) + (index * part_rows(a) + wave * kWaveRows + r) * (DP + 4);
     end_rows<DT, DP>(a, x, q.row + token, head, item.parts > 1 ? part : nullptr, hf);

@@ -47,7 +47,7 @@ __device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, in
 {
     const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
     const PageRef p = page_ref(a, b, len, key);
-    return Pages{p.page, page_scales(a, p.page, h), __ballot(p.valid)};
+    return Pages{p.page, page_scales(a, p, h), __ballot(p.valid)};
 }
 // What a lane needs of the i-th tile of a look-up: the pages of the keys and of the values that it
 // loads, the scales of its terms.
@@ -132,12 +132,14 @@ __device__ __forceinline__ void load_values(const AttendArgs& a, KvTile<DP>& t, 
 }
 
 // What a wave has of 16 query rows: lane (r, g) the sums of row r's channels 16 d + 4 g ..,
-// the reference, and its own keys' share of the denominator.
+// the reference, its own keys' share of the denominator and the reference of that (m, or one of its own
+// once a scale of values was `apart`).
 template <int DP>
 struct Rows {
     v4i q[DP / 64][2];
     v4f acc[DP / 16];
-    float m, l;
+    float m, l, z;
+    bool apart;
 };
 
 // A tile's terms; keys_read is called when its keys are no longer needed.
@@ -162,16 +164,18 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, KvTile<DP>& t, const PageS
     float top = s[0][0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i >> 2][i & 3]);
+    if (x.apart) add_apart(x.z, x.l, top * sc.key, sc.key, [&](int i) { return s[i >> 2][i & 3]; });
     top = __builtin_fmaf(top, sc.key, sc.log_value);
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     if (__any(top > x.m + kSlack)) {
         const float m1 = fmaxf(x.m, top);
         const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.m - m1);
-        x.l *= alpha;
 #pragma unroll
         for (int d = 0; d < ND; ++d) x.acc[d] *= alpha;
         x.m = m1;
+        x.l *= x.apart ? 1.0f : alpha;
+        x.z = x.apart ? x.z : m1;
     }
     const float offset = sc.log_value - ((x.m == -__builtin_inff() ? 0.0f : x.m) - kShift);
     float sum = 0.0f;
@@ -186,7 +190,7 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, KvTile<DP>& t, const PageS
         p[i >> 3][i & 7] = w[0];
         p[i >> 3][(i & 7) + 1] = w[1];
     }
-    x.l = __builtin_fmaf(sum, sc.inverse_value, x.l);
+    x.l = __builtin_fmaf(sum, x.apart ? 0.0f : sc.inverse_value, x.l);
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
         x.acc[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(Half<DT_FP16>::widen(t.v[d][0], t.v[d][1]), p[0],
@@ -227,7 +231,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Run& u, Ro
                    last = key_range(a, u.q, __builtin_amdgcn_readlane(token, u.rows - 1));
 #pragma unroll
     for (int d = 0; d < ND; ++d) x.acc[d] = v4f{0.f, 0.f, 0.f, 0.f};
-    x.m = -__builtin_inff();
+    x.m = x.z = -__builtin_inff();
     x.l = 0.0f;
 
     // the next tile's keys are asked for when this tile's have been read, its values likewise
@@ -235,6 +239,7 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Run& u, Ro
     TilePages pages = tile_pages<WIDE>(a, known, 0, key_of(u.t0), r, g);
     load_keys<DP, WIDE>(a, tile, pages, h, r, g);
     load_values<DP, WIDE>(a, tile, pages, h, r, g);
+    x.apart = any_apart(known.sc);
     for (int t = u.t0; t < u.t1; ++t) {
         const int key0 = key_of(t), next = (t + 1 - u.t0) % kLookUp<WIDE>;
         const bool more = t + 1 < u.t1;
@@ -247,11 +252,12 @@ __device__ __forceinline__ void attend_run(const AttendArgs& a, const Run& u, Ro
             if (next == 0) known = look_up<WIDE>(a, b, u.q.len, key0 + kKeys, h);
             pages = tile_pages<WIDE>(a, known, next, key0 + kKeys, r, g);
             load_keys<DP, WIDE>(a, tile, pages, h, r, g);
+            if (next == 0) x.apart |= any_apart(known.sc);
         });
         if (more) load_values<DP, WIDE>(a, tile, pages, h, r, g);
     }
-    x.l += __shfl_xor(x.l, 16);                             // the lane groups had keys of their own
-    x.l += __shfl_xor(x.l, 32);
+    join_lanes(x.z, x.l, 16);                               // the lane groups had keys of their own
+    join_lanes(x.z, x.l, 32);
 }
 
 // A workgroup has all rows of a key/value head of a sequence, its waves equal runs of the key tiles;
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(WAVES * 64, DP <= 128 ? 2 : 1) attend_whole_ke
 {
     constexpr int kWaves = WAVES, kThreads = kWaves * 64, ND = DP / 16;
     constexpr int RS = DP + 4;                              // floats of a row in LDS
-    __shared__ float stat[kWaves][kRows][2];
+    __shared__ __attribute__((aligned(16))) float stat[kWaves][kRows][4];      // m, l, z
     __shared__ __attribute__((aligned(16))) float sums[kWaves][kRows * RS];
 
     const int lane = threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -282,7 +288,7 @@ __global__ void __launch_bounds__(WAVES * 64, DP <= 128 ? 2 : 1) attend_whole_ke
     if (wave < used) {
         Rows<DP> x;
         attend_run<DT, DP, WIDE>(a, u, x);
-        if (g == 0) { stat[wave][r][0] = x.m; stat[wave][r][1] = x.l; }
+        if (g == 0) *reinterpret_cast<v4f*>(stat[wave][r]) = v4f{x.m, x.l, x.z, 0.0f};
 #pragma unroll
         for (int d = 0; d < ND; ++d) *reinterpret_cast<v4f*>(&sums[wave][r * RS + 16 * d + 4 * g]) = x.acc[d];
     }
@@ -291,13 +297,19 @@ __global__ void __launch_bounds__(WAVES * 64, DP <= 128 ? 2 : 1) attend_whole_ke
     const int quads = a.D / 4;
     for (int i = threadIdx.x; i < u.rows * quads; i += kThreads) {
         const int row = i / quads, d = i % quads * 4;
-        Joined j{-__builtin_inff(), 0.0f, 0.0f};
-        for (int p = 0; p < used; ++p) j.m = fmaxf(j.m, stat[p][row][0]);
-        j.ref = j.m == -__builtin_inff() ? 0.0f : j.m;
+        Joined j{-__builtin_inff(), -__builtin_inff(), 0.0f};
+        for (int p = 0; p < used; ++p) {
+            const v4f s = *reinterpret_cast<const v4f*>(stat[p][row]);
+            j.ref = fmaxf(j.ref, s[0]);
+            j.z = fmaxf(j.z, s[2]);
+        }
+        if (j.ref == -__builtin_inff()) j.ref = 0.0f;
+        if (j.z == -__builtin_inff()) j.z = 0.0f;
         v4f o = {0.f, 0.f, 0.f, 0.f};
         for (int p = 0; p < used; ++p) {
-            const float f = __builtin_amdgcn_exp2f(stat[p][row][0] - j.ref);
-            j.l += stat[p][row][1] * f;
+            const v4f s = *reinterpret_cast<const v4f*>(stat[p][row]);
+            const float f = __builtin_amdgcn_exp2f(s[0] - j.ref);
+            j.l += s[1] * __builtin_amdgcn_exp2f(s[2] - j.z);
             o += *reinterpret_cast<const v4f*>(&sums[p][row * RS + d]) * f;
         }
         store_row<DT>(a, u.q.row + row / a.group, u.h * a.group + row % a.group, d, o, j);

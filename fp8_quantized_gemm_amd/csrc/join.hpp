@@ -1,5 +1,5 @@
 // Joining the partial results of attention over parts of the keys:
-//   m = max m_i,  l = sum l_i 2^(m_i - m),  y = sum y_i 2^(m_i - m) / l
+//   m = max m_i,  z = max z_i,  l = sum l_i 2^(z_i - z),  y = 2^(m - z) sum y_i 2^(m_i - m) / l
 // A second launch of 4 to 6 us (8 rows of 128 parts 5.6 us, 52 units of 35 rows in 4 parts 4.4), bound by
 // the latency of two dependent rounds of loads; the parts come in a fixed order, so results repeat.
 #pragma once
@@ -15,7 +15,7 @@ struct Unit {
 };
 
 // The parts of a unit are those of every Hk-th workgroup from its first on.  A part's rows are DP + 4
-// floats apart: maximum, denominator, two unused, sums.
+// floats apart: the sums' reference m, the denominator l and its reference z, one unused, sums y.
 constexpr int kMostParts = 512;
 constexpr int kJoinThreads = 256;
 
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
                                                                     int part_rows)
 {
     constexpr int kEach = kJoinThreads / R, kLanes = kEach < 64 ? kEach : 64, kWaves = kJoinThreads / 64;
-    __shared__ float factor[R][kMostParts], red[2][kWaves];
+    __shared__ float factor[R][kMostParts], red[3][kWaves];
     __shared__ __attribute__((aligned(16))) float sums[kJoinThreads * 4];
     const Unit u = reinterpret_cast<const Unit*>(a.work)[blockIdx.x];
     const int mine = threadIdx.x / kEach, tid = threadIdx.x % kEach, row = blockIdx.y * R + mine;
@@ -37,24 +37,27 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     const auto part = [&](int k) {
         return parts + (((int64_t)u.group + (int64_t)k * a.Hk) * part_rows + row) * (DP + 4);
     };
-    float m = -__builtin_inff(), l = 0.0f;
+    float m = -__builtin_inff(), z = m, l = 0.0f;
     for (int k = tid; k < count; k += kEach) {
         factor[mine][k] = part(k)[0];
         m = fmaxf(m, factor[mine][k]);
+        z = fmaxf(z, part(k)[2]);
     }
 #pragma unroll
-    for (int off = kLanes / 2; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+    for (int off = kLanes / 2; off >= 1; off >>= 1) {
+        m = fmaxf(m, __shfl_xor(m, off));
+        z = fmaxf(z, __shfl_xor(z, off));
+    }
     if constexpr (kEach > 64) {
-        if ((threadIdx.x & 63) == 0) red[0][threadIdx.x >> 6] = m;
+        if ((threadIdx.x & 63) == 0) { red[0][threadIdx.x >> 6] = m; red[2][threadIdx.x >> 6] = z; }
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red[0][w]);
+        for (int w = 0; w < kWaves; ++w) { m = fmaxf(m, red[0][w]); z = fmaxf(z, red[2][w]); }
     }
-    const float ref = m == -__builtin_inff() ? 0.0f : m;
+    const float ref = m == -__builtin_inff() ? 0.0f : m, zref = z == -__builtin_inff() ? 0.0f : z;
     for (int k = tid; k < count; k += kEach) {
-        const float f = __builtin_amdgcn_exp2f(factor[mine][k] - ref);
-        factor[mine][k] = f;
-        l += part(k)[1] * f;
+        factor[mine][k] = __builtin_amdgcn_exp2f(factor[mine][k] - ref);
+        l += part(k)[1] * __builtin_amdgcn_exp2f(part(k)[2] - zref);
     }
 #pragma unroll
     for (int off = kLanes / 2; off >= 1; off >>= 1) l += __shfl_xor(l, off);
@@ -75,7 +78,7 @@ __global__ void __launch_bounds__(kJoinThreads) attend_join_kernel(const AttendA
     for (int k = 1; k < sets; ++k) o += *reinterpret_cast<const v4f*>(&sums[4 * (threadIdx.x + k * quads)]);
     if constexpr (kEach > 64) l = red[1][0] + red[1][1] + red[1][2] + red[1][3];
     const int gr = u.row0 + row;
-    store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, Joined{m, ref, l});
+    store_row<DT>(a, u.token0 + gr / a.group, u.head * a.group + gr % a.group, d, o, Joined{ref, zref, l});
 }
 
 template <int DT, int DP>

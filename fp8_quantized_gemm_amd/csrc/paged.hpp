@@ -7,8 +7,8 @@
 namespace fp8q {
 
 // A scale of the cache counts as the nearest value of this range (NaN as the
-// lowest): both ends and their reciprocals are normal fp32 numbers, and a sum of
-// 2^24 softmax terms, each divided by a scale, stays below fp32's largest.
+// lowest): both ends and their reciprocals are normal fp32 numbers, with room
+// for a code's or a softmax term's own exponent.
 constexpr float kMinPageScale = 0x1p-100f, kMaxPageScale = 0x1p100f;
 constexpr int kMinPageExp = -100, kMaxPageExp = 100;
 __device__ __forceinline__ float page_scale(float s)

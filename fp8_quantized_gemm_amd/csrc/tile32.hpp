@@ -141,14 +141,15 @@ __device__ __forceinline__ float max_halves(float v)
 }
 
 // What a wave has of its 32 query rows: lane (r, hf) half of row r's channels (32 d + 8 i + 4 hf ..),
-// the row's reference, and its own keys' share of the denominator; a bit of `nan` for each channel
-// that has seen NaN.
+// the row's reference, its own keys' share of the denominator and the reference of that (m, or one of
+// its own once a scale of values was `apart`); a bit of `nan` for each channel that has seen NaN.
 template <int DP>
 struct Rows {
     v4i q[DP / 32][2];
     v16f acc[DP / 32];
     uint32_t nan[DP / 64];
-    float m, l;
+    float m, l, z;
+    bool apart;
 };
 
 // A tile's terms.  whole: every row sees every key; clean: room for a tile of values.
@@ -205,16 +206,22 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
         top[tb] = s[tb][0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) top[tb] = fmaxf(top[tb], s[tb][i]);
-        top[tb] = __builtin_fmaf(top[tb], ks[tb], lv[tb]);
     }
+    if (x.apart) {
+#pragma unroll
+        for (int tb = 0; tb < 2; ++tb) add_apart(x.z, x.l, top[tb] * ks[tb], ks[tb], [&](int i) { return s[tb][i]; });
+    }
+#pragma unroll
+    for (int tb = 0; tb < 2; ++tb) top[tb] = __builtin_fmaf(top[tb], ks[tb], lv[tb]);
     const float both = fmaxf(top[0], top[1]), highest = max_halves(both);
     if (__any(highest > x.m + kSlack)) {
         const float m1 = fmaxf(x.m, highest);
         const float alpha = m1 == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(x.m - m1);
-        x.l *= alpha;
 #pragma unroll
         for (int d = 0; d < ND; ++d) x.acc[d] *= alpha;
         x.m = m1;
+        x.l *= x.apart ? 1.0f : alpha;
+        x.z = x.apart ? x.z : m1;
     }
     const float ref = x.m == -__builtin_inff() ? 0.0f : x.m;
     v8h p[2][2];
@@ -232,7 +239,8 @@ __device__ __forceinline__ void add_tile(Rows<DP>& x, const uint8_t* kt, const P
             p[tb][i >> 3][i & 7] = w[0];
             p[tb][i >> 3][(i & 7) + 1] = w[1];
         }
-        x.l = __builtin_fmaf(sum, WIDE ? sc.inverse_value : __shfl(sc.inverse_value, 2 * tb + hf), x.l);
+        const float inverse = WIDE ? sc.inverse_value : __shfl(sc.inverse_value, 2 * tb + hf);
+        x.l = __builtin_fmaf(sum, x.apart ? 0.0f : inverse, x.l);
     }
 #pragma unroll
     for (int tb = 0; tb < 2; ++tb)
@@ -267,16 +275,17 @@ __device__ __forceinline__ void begin_rows(const AttendArgs& a, Rows<DP>& x, boo
         for (int i = 0; i < 16; ++i) x.acc[d][i] = 0.0f;
 #pragma unroll
     for (int d = 0; d < DP / 64; ++d) x.nan[d] = 0u;
-    x.m = -__builtin_inff();
+    x.m = x.z = -__builtin_inff();
     x.l = 0.0f;
+    x.apart = false;
 }
 
 // The rows' results: to the output, or to a partial result (at this lane's row).  l is whole already.
 template <int DT, int DP>
 __device__ __forceinline__ void end_rows(const AttendArgs& a, const Rows<DP>& x, int64_t token, int head, float* part, int hf)
 {
-    const Joined j{x.m, x.m == -__builtin_inff() ? 0.0f : x.m, x.l};
-    if (part != nullptr && hf == 0) { part[0] = x.m; part[1] = x.l; }
+    const Joined j{x.m == -__builtin_inff() ? 0.0f : x.m, x.z == -__builtin_inff() ? 0.0f : x.z, x.l};
+    if (part != nullptr && hf == 0) { part[0] = x.m; part[1] = x.l; part[2] = x.z; }
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -307,7 +316,7 @@ __device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, in
 {
     const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
     const PageRef p = page_ref(a, b, len, key);
-    return Pages{p.page, page_scales(a, p.page, h), __ballot(p.valid)};
+    return Pages{p.page, page_scales(a, p, h), __ballot(p.valid)};
 }
 // The scales of the i-th tile of a look-up as add_tile takes them, and whether its pages are there.
 template <bool WIDE>
