@@ -3,7 +3,6 @@
 // GEMV) and the MFMA tile kernels (M > 16), and launch on the caller's stream.  No device memory is allocated and no host
 // synchronization happens in any call.
 #include <atomic>
-#include <cfloat>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -814,7 +813,7 @@ fp8q_status fp8_paged_attention(const fp8q_kv_cache* cache, const fp8q_kv_batch*
     FP8Q_TRY(check_paged(cache, batch));
     const int64_t D = cache->head_dim, T = batch->tokens;
     if (!query_heads_ok(*cache, *batch, q_heads) || !stride_ok(q_stride, q_heads, D) ||
-        !(scale >= -FLT_MAX && scale <= FLT_MAX) || window < 0 || window > kMaxPagedLen ||
+        !(std::fabs(scale) <= kMaxSoftmaxScale) || window < 0 || window > kMaxPagedLen ||
         (window > 0 && !causal))
         return FP8Q_ERR_SHAPE;
     if (!aligned16(q) || !aligned16(y) || !aligned16(work) || !aligned4(lse)) return FP8Q_ERR_ALIGN;

@@ -53,8 +53,8 @@ __device__ __forceinline__ PageScales page_scales(const AttendArgs& a, const Pag
 {
     const int64_t cell = (int64_t)page.page * a.Hk + h;
     const float held = page_scale(a.v_scale[cell]), v = page.valid ? held : 1.0f;
-    // never 0, which would make NaN of a masked key's -inf
-    const float k = fmaxf(page_scale(a.k_scale[cell]) * a.scale_log2, FLT_MIN);
+    // never 0, which would make NaN of a masked key's -inf, nor infinite, which would of a logit of 0
+    const float k = fminf(fmaxf(page_scale(a.k_scale[cell]) * a.scale_log2, FLT_MIN), FLT_MAX);
     return PageScales{k, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v) * (1.0f / kShiftScale)};
 }
 

@@ -21,6 +21,7 @@ constexpr int64_t kMaxPagedLen = (int64_t)1 << 24;      // table_width * page_si
 constexpr int64_t kMaxPagedTokens = (int64_t)1 << 26;   // new tokens of a batch
 constexpr int64_t kMaxPagedSeqs = (int64_t)1 << 16;
 constexpr int64_t kMaxPagedHeads = 1024;
+constexpr float kMaxSoftmaxScale = 0x1p127f;            // times log2(e) it is finite
 constexpr int64_t kMaxPagedRows = (int64_t)1 << 30;     // tokens * (q_heads / kv_heads)
 
 struct PagedBatch {

@@ -553,8 +553,10 @@ FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_bat
  *          contents before and after the call are of no meaning.  Calls that may
  *          run at the same time need one each.
  *   q_heads % kv_heads == 0, q_heads <= 1024, tokens * (q_heads / kv_heads) <=
- *   2^30;  scale finite;  0 <= window <= 2^24.  One launch, two where few
- *   sequences that may be long leave the GPU room to share their keys out.
+ *   2^30;  |scale| <= 2^127;  0 <= window <= 2^24.  |scale| * log2(e) * k_scale
+ *   counts as the nearest normal fp32 number, and logits times log2(e) have to
+ *   stay within fp32 (else NaN).  One launch, two where few sequences that may be
+ *   long leave the GPU room to share their keys out.
  *   fp8_paged_attention_work_bytes looks at the sizes in the structs only (pages
  *   apart, which does not matter), and gives 0 for sizes that the call refuses.
  */

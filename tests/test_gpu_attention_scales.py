@@ -1,6 +1,6 @@
-"""fp8_paged_attention where the scales of a row's pages lie at the ends of their range, in each of
-its kernels: y and lse against the host form in 64 bits, within the bounds that follow from the
-roundings (see paged_ref.attend)."""
+"""fp8_paged_attention where the scales of a row's pages, or the softmax scale, lie at the ends of
+their ranges, in each of its kernels: y and lse against the host form in 64 bits, within the bounds
+that follow from the roundings (see paged_ref.attend)."""
 import math
 
 import pytest
@@ -131,6 +131,24 @@ def test_many_keys_above_the_first(seqs, new, scale):
     say("many keys", seqs, new, scale)
     want = ref.attend(bt, q, 1.0)
     compare(bt, q, attend(bt, q, 0, 1.0), want)
+
+
+@pytest.mark.parametrize("kernel", list(KERNELS))
+@pytest.mark.parametrize("k_scale,scale", [(2.0 ** 100, 2.0 ** 30), (2.0 ** 100, -2.0 ** 127), (1.0, 2.0 ** 127),
+                                           (math.inf, 2.0 ** 28)])
+def test_logits_of_zero_under_large_scales(kernel, k_scale, scale):
+    """A product of scales beyond fp32 counts as its largest number: a query or a key of zeros has
+    logits of zero all the same."""
+    bt, room = batch(kernel, 64 if kernel != "one tile" else 16, seed=35)
+    bt.ks.fill_(k_scale)
+    q = bt.values(4, torch.bfloat16)
+    zero = torch.zeros_like(q)
+    say("zero queries", kernel, k_scale, scale)
+    compare(bt, zero, attend(bt, zero, room, scale), ref.attend(bt, zero, scale))
+    bt.k.zero_()
+    spoil_unused(bt)
+    say("zero keys", kernel, k_scale, scale)
+    compare(bt, q, attend(bt, q, room, scale), ref.attend(bt, q, scale))
 
 
 @pytest.mark.parametrize("new,lens,room", [([1] * 3, [300, 64, 900], 0), ([1] * 3, [300, 64, 900], 20000),
