@@ -506,7 +506,7 @@ def _rows(t: torch.Tensor, name: str, dtype, shape, index: int):
     row, head, one = t.stride()
     if ((dim > 1 and one != 1) or (heads > 1 and head != dim)) and t.numel():
         raise ValueError(f"{name}: a row's heads must be contiguous, got strides {t.stride()}")
-    return t.data_ptr(), row if tokens > 1 else max(row, heads * dim)
+    return t.data_ptr(), row if tokens > 1 else heads * dim
 
 
 def fp8_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,

@@ -16,3 +16,14 @@ def test_softmax_scales_that_overflow_in_powers_of_two(scale):
 @pytest.mark.parametrize("scale", [2.0 ** 127, -2.0 ** 127, 0.0])
 def test_largest_softmax_scale(scale):
     assert status(fp8q.lib.fp8_paged_attention, ATTEND, {"scale": scale}) != SHAPE
+
+
+@pytest.mark.parametrize("heads", [1, 4])
+def test_one_token_of_any_row_stride(heads):
+    """The rows of one token have no distance: whatever its tensor's stride says is taken."""
+    row = torch.zeros(1, 1001, dtype=torch.bfloat16)             # a stride that rows could not have
+    t = row.as_strided((1, heads, 64), (1001, 64, 1))
+    assert t.stride(0) == 1001
+    assert fp8q._rows(t, "q", torch.bfloat16, t.shape, t.get_device()) == (t.data_ptr(), heads * 64)
+    two = torch.zeros(2, 1001, dtype=torch.bfloat16).as_strided((2, heads, 64), (1001, 64, 1))
+    assert fp8q._rows(two, "q", torch.bfloat16, two.shape, two.get_device()) == (two.data_ptr(), 1001)
