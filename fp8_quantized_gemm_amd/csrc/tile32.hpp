@@ -34,6 +34,9 @@ __device__ __forceinline__ v16f mfma32(typename Half<DT>::vec a, v4i b, v16f c)
 // address.  Written as assembly because the compiler, which cannot tell the buffer being filled from
 // the one being read, would wait for builtin loads of this kind before the next read of LDS, and no
 // tile would be under way during the arithmetic.  They write no register; the kernel waits itself.
+// Nor does the compiler look into the blocks for what an instruction needs before it reads a register: one
+// wait state after a write of m0, five after a vector instruction wrote a word of the resource, which may be
+// the last instruction before the block.
 __device__ __forceinline__ uint32_t lds_address(const void* p)
 {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
@@ -41,7 +44,7 @@ __device__ __forceinline__ uint32_t lds_address(const void* p)
 __device__ __forceinline__ void buffer_to_lds(const v4i& rsrc, uint32_t lds_block, uint32_t offset)
 {
     int m0;                               // kept for the compiler
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\t"
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 2\n\t"
                  "buffer_load_dwordx4 %2, %3, 0 offen lds\n\ts_mov_b32 m0, %0"
                  : "=&s"(m0)
                  : "s"(uniform((int)lds_block)), "v"(offset), "s"(rsrc)
