@@ -14,6 +14,8 @@ namespace fp8q {
 // down to 2^-23 of the reference with all its 11 bits.
 constexpr float kSlack = 6.0f, kShift = 9.0f, kShiftScale = 0x1p9f;
 
+constexpr int kKeys = 64;                 // keys of a tile
+
 // A value that all lanes of the wave have, told to the compiler.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
@@ -88,6 +90,24 @@ __device__ __forceinline__ void join_lanes(float& z, float& l, int off)
     z = fmaxf(z, other);
     const float ref = z == -__builtin_inff() ? 0.0f : z;
     l = l * __builtin_amdgcn_exp2f(mine - ref) + more * __builtin_amdgcn_exp2f(other - ref);
+}
+
+// What a wave knows of the pages of the next tiles: lane i of the page with the i-th of 64 tiles where
+// a page holds whole tiles (WIDE), else of the i-th of 64 groups of 16 keys.  Looked up together, so
+// that no tile waits for its page's id or scales.
+struct Pages {
+    int page;                             // 0 where there is none
+    PageScales sc;
+    uint64_t valid;
+};
+template <bool WIDE>
+constexpr int kLookUp = WIDE ? 64 : 16;   // tiles of a look-up
+template <bool WIDE>
+__device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, int key0, int h)
+{
+    const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
+    const PageRef p = page_ref(a, b, len, key);
+    return Pages{p.page, page_scales(a, p, h), __ballot(p.valid)};
 }
 
 // The E4M3 codes of NaN in four codes, as 0x80 in their bytes.

@@ -21,7 +21,6 @@ namespace fp8q {
 namespace {
 
 constexpr int kRows = kWholeRows;         // query rows of a workgroup: (token, head of the group) pairs
-constexpr int kKeys = 64;                 // keys of a tile
 // Waves of a workgroup at most: eight where the registers allow.
 constexpr int waves_for(int dp) { return dp <= 128 ? 8 : 4; }
 
@@ -32,23 +31,6 @@ struct KvTile {
     v4i k[4][DP / 64], v[DP / 16];
 };
 
-// What a wave knows of the pages of the next tiles: lane i of the page with the i-th of 64 tiles where
-// a page holds whole tiles (WIDE), else of the i-th of 64 groups of 16 keys.  Looked up together, so
-// that no tile waits for its page's id or scales.
-struct Pages {
-    int page;                             // 0 where there is none
-    PageScales sc;
-    uint64_t valid;
-};
-template <bool WIDE>
-constexpr int kLookUp = WIDE ? 64 : 16;   // tiles of a look-up
-template <bool WIDE>
-__device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, int key0, int h)
-{
-    const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
-    const PageRef p = page_ref(a, b, len, key);
-    return Pages{p.page, page_scales(a, p, h), __ballot(p.valid)};
-}
 // What a lane needs of the i-th tile of a look-up: the pages of the keys and of the values that it
 // loads, the scales of its terms.
 struct TilePages {

@@ -19,8 +19,6 @@ namespace {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-constexpr int kKeys = 64;                 // keys of a tile
-
 template <int DT>
 __device__ __forceinline__ v16f mfma32(typename Half<DT>::vec a, v4i b, v16f c)
 {
@@ -304,23 +302,6 @@ __device__ __forceinline__ void end_rows(const AttendArgs& a, const Rows<DP>& x,
         }
 }
 
-// What a wave knows of the pages of the next tiles: lane i of the page with the i-th of 64 tiles where
-// a page holds whole tiles (WIDE), else of the i-th of 64 groups of 16 keys.  Looked up together, so
-// that no tile waits for its page's id or scales.
-struct Pages {
-    int page;                             // 0 where there is none
-    PageScales sc;
-    uint64_t valid;
-};
-template <bool WIDE>
-constexpr int kLookUp = WIDE ? 64 : 16;   // tiles of a look-up
-template <bool WIDE>
-__device__ __forceinline__ Pages look_up(const AttendArgs& a, int b, int len, int key0, int h)
-{
-    const int key = key0 + (int)(threadIdx.x & 63) * (WIDE ? kKeys : 16);
-    const PageRef p = page_ref(a, b, len, key);
-    return Pages{p.page, page_scales(a, p, h), __ballot(p.valid)};
-}
 // The scales of the i-th tile of a look-up as add_tile takes them, and whether its pages are there.
 template <bool WIDE>
 __device__ __forceinline__ PageScales tile_scales(const Pages& p, int i, bool& valid)
