@@ -29,7 +29,7 @@ __host__ __device__ __forceinline__ int part_rows(const AttendArgs& a)
 }
 // Key tiles that a part has at least: its rows go through the scratch.  Where units are few, parts of
 // 4 tiles are short enough to use the chip (64/8 heads, 128 tokens of 2000: 31 us, 36 with 20), and for
-// few rows parts of 2 (here 1 token of 1300 12.7 us, 15.0 with 4; but 256 of 256: 21.1 us, 14.3 with 4).
+// few rows parts of 2 (here 1 token of 2000 14.0 us, 16.4 with 4; but 256 of 256: 21.1 us, 14.3 with 4).
 // Where they are more than a quarter of the workgroups that fit, cutting them doubles those on a
 // compute unit at best, which pays for many rows if the parts are long (512 of 512: 22 us, 33 with 4).
 __host__ __device__ __forceinline__ int least_tiles(const AttendArgs& a, int64_t units, int slots)

@@ -76,20 +76,23 @@ struct AttendArgs {
 // With at most this many query rows a sequence, a workgroup can have a key/value head of it whole
 // (attend_whole.hip); the tile kernel cuts the keys over workgroups where there are few, with a second
 // launch.  Whole, in us, against the tile kernel, 64/8 heads x 128, u = sequences * key/value heads:
-//   u = 8    1 x 500 8.2 (15.8)     1 x 2000 16.4 (13.9)   1 x 4000 26.3 (14.0)
-//   u = 64   8 x 2000 18.1 (20.6)   8 x 4000 28.1 (24.4)   8 x 8000 57 (39)
+//   u = 8    1 x 500 8.5 (13.8)     1 x 1400 12.9 (14.0)   1 x 1700 15.0 (13.0)   1 x 4000 26.6 (14.1)
+//   u = 64   8 x 2000 18.3 (21.0)   8 x 2600 21.6 (22.6)   8 x 4000 28.5 (25.6)
 //   u = 128  16 x 4000 39 (43)      16 x 8000 62 (68), of up to 8000 56 (42)
 //   u = 192  24 x 4000 41 (62)      24 of up to 16000 115 (98)
 //   u = 256  32 x 4000 51 (63)      32 of up to 8000 71 (83)
 //   u = 512  64 of up to 8000 133 (166), of up to 32000 489 (620)
-// So whole up to 2048 keys, or 32 u, and always from two workgroups for each of 256 compute units on.
-// The host knows the page table's room only, not the lengths.
+// Alone, a workgroup's time goes by the codes that it reads, the tile kernel's by its two launches: 2 heads
+// x 64, 2 x 2600 11.6 (12.6), 2 x 4000 13.6 (12.7); 4 x 192 1400 15.0 (17.4), 2600 23.0 (16.6); 4 x 256 1000
+// 18.4 (19.6), 1400 21.9 (20.1) (four waves, not eight, above 128).
+// So whole up to 200 Ki codes of a head's keys, 288 Ki above 128 channels, or 32 u keys, and always from two
+// workgroups for each of 256 compute units on.  The host knows the page table's room only, not the lengths.
 constexpr int kWholeRows = 16;
 inline bool takes_tiles(const AttendArgs& a)
 {
     if ((int64_t)a.batch.max_q * a.group > kWholeRows) return true;
     const int64_t u = (int64_t)a.batch.B * a.Hk, keys = (int64_t)a.batch.W * a.P;
-    return u < 512 && keys > 2048 && keys > 32 * u;
+    return u < 512 && keys * a.D > (a.D <= 128 ? 200 : 288) * 1024 && keys > 32 * u;
 }
 hipError_t launch_attend_tiles(const AttendArgs& a, int dtype, hipStream_t stream);
 int64_t attend_tiles_work_bytes(const AttendArgs& a);
