@@ -585,7 +585,9 @@ def fp8_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     q [tokens, q_heads, head_dim] bf16/fp16; query head j reads key/value head j // (q_heads //
     kv_heads).  scale: 1/sqrt(head_dim) when not given.  causal: a token sees those at or before
     its position; window > 0: of these only the last `window`.  work is scratch (uint8,
-    allocated when not given; paged_attention_work).  Returns (y like q, lse float32 [tokens,
+    allocated when not given; paged_attention_work).  The kernel goes by the page table's width,
+    which is known on the host: a table no wider than the longest sequence needs is the fastest.
+    Returns (y like q, lse float32 [tokens,
     q_heads]); a row that sees no token gets zeros and -inf."""
     code = _dtype_code(q)
     index, stream = _where(q)

@@ -480,7 +480,8 @@ typedef struct {
  * the i-th has the position kv_lens[b] - n + i.
  *   page_table[seqs, table_width]  page of the tokens jP .. jP+P-1 of each
  *                  sequence; an id outside 0 .. pages-1 is no page: tokens on it
- *                  are neither stored nor seen
+ *                  are neither stored nor seen.  A page may be in several places,
+ *                  but only one may gain tokens on it
  *   q_start[seqs+1] ascending, within 0 .. tokens
  *   kv_lens[seqs]  tokens of each sequence, the new ones included (0: an idle
  *                  slot of the batch); at most table_width * P count
@@ -488,7 +489,10 @@ typedef struct {
  *                  left out
  *   1 <= tokens <= 2^26;  1 <= seqs <= 65536;  1 <= max_q <= tokens;
  *   table_width >= 1 and table_width * P <= 2^24.
- * The arrays are device memory; the struct itself is read during the call.
+ * The arrays are device memory; the struct itself is read during the call.  So the
+ * attention's kernel, its launches and its scratch go by the room of the table,
+ * table_width * P tokens a sequence, not by the lengths: a table much wider than
+ * the sequences at hand can double the time of short ones.
  */
 typedef struct {
     const int32_t *page_table, *q_start, *kv_lens;
@@ -521,7 +525,7 @@ typedef struct {
  *       q_out_stride values apart; may be q itself (with q's stride)
  *   Rows outside q_start[0] .. q_start[seqs]-1 and tokens at negative positions are
  *   left out.  Calls that append to one page must not overlap in time, and two
- *   sequences of a call must not append to one page.  1 <= q_heads <= 1024.
+ *   places of a call's page table must not append to one page.  1 <= q_heads <= 1024.
  *   One launch.
  */
 FP8Q_API fp8q_status fp8_kv_append(const fp8q_kv_cache* cache, const fp8q_kv_batch* batch,
