@@ -5,12 +5,13 @@
 // tile's on the way during the arithmetic; two workgroups share a compute unit.
 //
 // Prompts are bound by the vector units: a tile takes a wave 32 MFMAs and about
-// 320 other instructions, of which 128 widen codes and 150 are the softmax.  4096
-// tokens with 64/8 heads x 128 take 297 us, 0.93 PFLOP/s (a library product of
-// 8192^3 reaches 1.2), vector units busy 71% and matrix units 45% of the time;
-// 2048 with 32/32 heads 58 us, where one workgroup of a compute unit's two ends
+// 330 other instructions, of which 128 widen codes and 150 are the softmax.  4096
+// tokens with 64/8 heads x 128 take 293 us, 0.94 PFLOP/s (a library product of
+// 8192^3 reaches 1.2), vector units busy 70% and matrix units 43% of the time;
+// 2048 with 32/32 heads 55 us, where one workgroup of a compute unit's two ends
 // early.  Decoding few long sequences is bound by HBM: 1 of 131072 (268 MB) in
-// 512 parts 54 us and 6 to join them.
+// 512 parts 54 us and 6 to join them.  (Calls on a busy stream; after a pause
+// they take up to a sixth longer, until the clocks have risen.)
 #include "tile32.hpp"
 
 namespace fp8q {

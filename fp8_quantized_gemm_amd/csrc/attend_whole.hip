@@ -9,12 +9,12 @@
 // registers, a tile of 64 keys ahead, and join their sums in LDS: no wave waits
 // for another before the end, and there is one launch.  Short calls are bound
 // by the chain of a launch, the lengths, the page ids, the codes and the
-// arithmetic on a tile or two: 1 token of 500 with 64/8 heads takes 8.2 us, of
-// 64 5.2 us.  A workgroup by itself reads about 45 GB/s, so from about 128 of
-// them on HBM is the bound: 32 tokens of 4000 51 us (5.2 TB/s), 64 of 8192 199 us
-// (5.4 TB/s).  Workgroups of neighbouring heads follow each other, so that a
-// long sequence's run side by side (24 of up to 2048 with 32/32 heads: 55.6 us,
-// 61.9 with neighbouring sequences; the longest first: 59.7).
+// arithmetic on a tile or two: 1 token of 500 with 64/8 heads takes 8.5 us, of
+// 64 5.3 us.  A workgroup by itself reads about 45 GB/s, so from about 128 of
+// them on HBM is the bound: 64 of 8192 185 us (5.8 TB/s; reads alone reach 6.45).
+// Workgroups of neighbouring heads follow each other, so that a long sequence's
+// run side by side: 24 of up to 2048 with 32/32 heads take 50 us, 11% more with
+// neighbouring sequences and 7% more with the longest first.
 #include "attend.hpp"
 
 namespace fp8q {

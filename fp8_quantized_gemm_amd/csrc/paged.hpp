@@ -78,10 +78,10 @@ struct AttendArgs {
 // launch.  Whole, in us, against the tile kernel, 64/8 heads x 128, u = sequences * key/value heads:
 //   u = 8    1 x 500 8.5 (13.8)     1 x 1400 12.9 (14.0)   1 x 1700 15.0 (13.0)   1 x 4000 26.6 (14.1)
 //   u = 64   8 x 2000 18.3 (21.0)   8 x 2600 21.6 (22.6)   8 x 4000 28.5 (25.6)
-//   u = 128  16 x 4000 39 (43)      16 x 8000 62 (68), of up to 8000 56 (42)
-//   u = 192  24 x 4000 41 (62)      24 of up to 16000 115 (98)
-//   u = 256  32 x 4000 51 (63)      32 of up to 8000 71 (83)
-//   u = 512  64 of up to 8000 133 (166), of up to 32000 489 (620)
+//   u = 128  16 x 4000 38 (41)      16 x 8000 67 (64), of up to 8000 57 (45)
+//   u = 192  24 x 4000 44 (64)      24 of up to 16000 115 (99)
+//   u = 256  32 x 4000 55 (72)      32 of up to 8000 73 (85)
+//   u = 512  64 of up to 8000 131 (173), of up to 32000 490 (648)
 // Alone, a workgroup's time goes by the codes that it reads, the tile kernel's by its two launches: 2 heads
 // x 64, 2 x 2600 11.6 (12.6), 2 x 4000 13.6 (12.7); 4 x 192 1400 15.0 (17.4), 2600 23.0 (16.6); 4 x 256 1000
 // 18.4 (19.6), 1400 21.9 (20.1) (four waves, not eight, above 128).

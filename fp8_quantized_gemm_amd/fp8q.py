@@ -587,8 +587,7 @@ def fp8_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
     its position; window > 0: of these only the last `window`.  work is scratch (uint8,
     allocated when not given; paged_attention_work).  The kernel goes by the page table's width,
     which is known on the host: a table no wider than the longest sequence needs is the fastest.
-    Returns (y like q, lse float32 [tokens,
-    q_heads]); a row that sees no token gets zeros and -inf."""
+    Returns (y like q, lse float32 [tokens, q_heads]); a row that sees no token gets zeros and -inf."""
     code = _dtype_code(q)
     index, stream = _where(q)
     cache, kv_heads, head_dim = _kv_cache(k_pages, v_pages, k_scale, v_scale, index)
